@@ -21,10 +21,12 @@ import re
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmoe_nvfp4.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_nvfp4.h")
+LEARNER_HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_learner.h")
 
 MOE_OK, MOE_ERR_POINTER, MOE_ERR_SHAPE, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE = 0, -1, -2, -3, -4, -5
 STATUS_NONFINITE_X, STATUS_NONFINITE_LOGITS, STATUS_NONFINITE_WEIGHT = 0x1, 0x2, 0x4
-STATUS_BAD_ROUTING, STATUS_TIMEOUT = 0x8, 0x10
+STATUS_BAD_ROUTING, STATUS_TIMEOUT, STATUS_BAD_TOKEN = 0x8, 0x10, 0x20
+LOGPROBS_MAX_TOP, DISTILL_MAX_K, DISTILL_MAX_V = 32, 256, 1 << 20
 
 WS_FIELDS = ["topk_ids", "topk_w", "token_slot_row", "counts", "offsets", "row_to_token",
              "amax_tok", "x_codes", "x_sf", "x_g", "h_codes", "h_sf", "h_g", "slots",
@@ -37,7 +39,7 @@ class MoeError(RuntimeError):
         super().__init__("%s failed: %d (%s)" % (fn, code, status_string(code)))
 
 
-P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _SIGS = {
     "moe_abi_version": (I32, []),
     "moe_status_string": (ctypes.c_char_p, [I32]),
@@ -65,6 +67,15 @@ _SIGS = {
     "moe_expert_forward_train": (I32, [P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P, P, P, P]),
     "moe_expert_backward_workspace_bytes": (SZ, [I32, I32, I32, I32, I32]),
     "moe_expert_backward": (I32, [P, P, I32, I32, I32, I32, I32] + [P] * 21 + [SZ, P, P]),
+    "moe_mx8_sf_bytes": (SZ, [I64, I32]),
+    "moe_add_rmsnorm": (I32, [P, I64, P, I64, P, F32, I32, I32, P, P, P, P, P, P, P]),
+    "moe_add_rmsnorm_backward_workspace_bytes": (SZ, [I32, I32]),
+    "moe_add_rmsnorm_backward": (I32, [P, P, P, P, P, I32, I32, P, P, P, SZ, P, P]),
+    "moe_token_logprobs": (I32, [P, I32, I64, I32, I32, P, F32, I32] + [P] * 7),
+    "moe_token_logprobs_backward": (I32, [P, I32, I64, I32, I32, P, F32, P, P, P, P, P, I64, P, P]),
+    "moe_distill_topk": (I32, [P, I32, I64, I32, I32, P, P, P, I32, F32, P, P, P, P]),
+    "moe_distill_topk_backward": (I32, [P, I32, I64, I32, I32, P, P, P, I32, F32, P, P, P, I64, P, P]),
+    "moe_distill_topk_train": (I32, [P, I32, I64, I32, I32, P, P, P, I32, F32, P, P, P, I64, P, P]),
 }
 
 _lib = None
@@ -84,9 +95,10 @@ def lib():
     return _lib
 
 
-def header_functions():
-    """Names of the functions include/moe_nvfp4.h declares."""
-    src = open(HEADER).read()
+def header_functions(header=HEADER):
+    """Names of the functions a header declares (include/moe_nvfp4.h unless
+    another is given)."""
+    src = open(header).read()
     src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
     return sorted(set(re.findall(r"\b([a-z][a-z0-9_]*)\s*\(", src)) - {"defined"})
 
@@ -260,6 +272,177 @@ def moe_expert_backward(dY, x, T, E, k, d, d_ff, W1, W2, w2_codes, w2_sf, w2_g, 
 
 def backward_workspace_bytes(T, E, k, d, d_ff):
     return int(lib().moe_expert_backward_workspace_bytes(T, E, k, d, d_ff))
+
+
+# --------------------------------------------------------------------------
+# learner operators (include/moe_learner.h): sizes and strides come from the
+# tensors, whose types and sizes are checked here
+# --------------------------------------------------------------------------
+def _tensor(t, dtypes, shape, what):
+    """Pointer of a contiguous device tensor of one of `dtypes` and of `shape`
+    (None: an optional argument left out)."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s: a contiguous CUDA tensor %s of %s expected, got %s of %s"
+                         % (what, tuple(shape), " or ".join(map(str, dtypes)), tuple(t.shape), t.dtype))
+    return t.data_ptr()
+
+
+def _rows(t, dtypes, shape, what):
+    """Pointer and row stride of a 2-D device tensor whose rows are contiguous."""
+    if t.dim() != 2 or (shape is not None and t.shape != shape) or t.dtype not in dtypes or not t.is_cuda or \
+            (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("%s: a 2-D CUDA tensor%s of %s with contiguous rows expected, got %s of %s, strides %s"
+                         % (what, "" if shape is None else " %s" % (tuple(shape),), " or ".join(map(str, dtypes)),
+                            tuple(t.shape), t.dtype, t.stride()))
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+_types = {}
+
+
+def _dt():
+    """The element types of the learner operators' tensors."""
+    if not _types:
+        import torch
+        b16 = (torch.bfloat16, torch.int16, torch.uint16)
+        _types.update(b16=b16, f32=(torch.float32,), i32=(torch.int32,), logits=b16 + (torch.float32,),
+                      codes=(torch.uint8, torch.float8_e4m3fn), scales=(torch.uint8, torch.float8_e8m0fnu),
+                      same={t: b16 for t in b16} | {torch.float32: (torch.float32,)})
+    return _types
+
+
+def _stream(stream):
+    import torch
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def mx8_sf_bytes(rows, d):
+    return int(lib().moe_mx8_sf_bytes(rows, d))
+
+
+def add_rmsnorm_backward_workspace_bytes(T, d):
+    return int(lib().moe_add_rmsnorm_backward_workspace_bytes(T, d))
+
+
+def moe_add_rmsnorm(x, res, w, eps, h, y, y8=None, y8_sf=None, rstd=None, status=None, stream=None):
+    """Residual add + RMS norm: h = x + res, y = h / rms(h) * w in BF16 and,
+    with y8 and y8_sf, in E4M3 with a power-of-two scale per 32 values.  x and
+    res [T][d] may have strided rows."""
+    ty = _dt()
+    b16 = ty["b16"]
+    px, ldx = _rows(x, b16, None, "x")
+    shape = x.shape
+    T, d = shape
+    pr, ldr = (None, d) if res is None else _rows(res, b16, shape, "res")
+    if y8_sf is not None and (not y8_sf.is_contiguous() or y8_sf.dtype not in ty["scales"]
+                              or y8_sf.numel() < mx8_sf_bytes(T, d)):
+        raise ValueError("y8_sf: at least %d contiguous scale bytes expected" % mx8_sf_bytes(T, d))
+    _check("moe_add_rmsnorm", lib().moe_add_rmsnorm(
+        px, ldx, pr, ldr, _tensor(w, b16, (d,), "w"), eps, T, d, _tensor(h, b16, shape, "h"),
+        _tensor(y, b16, shape, "y"), _tensor(y8, ty["codes"], shape, "y8"),
+        None if y8_sf is None else y8_sf.data_ptr(), _tensor(rstd, ty["f32"], (T,), "rstd"), _p(status),
+        _stream(stream)))
+
+
+def moe_add_rmsnorm_backward(dy, dh, h, rstd, w, dx, dw, ws, status=None, stream=None):
+    """Gradients of moe_add_rmsnorm; dh (the gradient of h) and dw may be
+    None."""
+    ty = _dt()
+    b16 = ty["b16"]
+    shape = dy.shape
+    if dy.dim() != 2:
+        raise ValueError("dy: a 2-D tensor expected, got %s" % (tuple(shape),))
+    T, d = shape
+    _check("moe_add_rmsnorm_backward", lib().moe_add_rmsnorm_backward(
+        _tensor(dy, b16, shape, "dy"), _tensor(dh, b16, shape, "dh"), _tensor(h, b16, shape, "h"),
+        _tensor(rstd, ty["f32"], (T,), "rstd"), _tensor(w, b16, (d,), "w"), T, d, _tensor(dx, b16, shape, "dx"),
+        _tensor(dw, ty["f32"], (d,), "dw"), None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.numel() * ws.element_size(), _p(status), _stream(stream)))
+
+
+def moe_token_logprobs(logits, targets, inv_temperature, n_top, logprob, entropy, stats, top_ids=None,
+                       top_logprob=None, status=None, stream=None):
+    """Log-probabilities of the targets, entropy, softmax statistics and the
+    n_top most likely ids of each row of logits [T][V] (strided rows
+    allowed).  Outputs that are None are left out."""
+    ty = _dt()
+    f32 = ty["f32"]
+    pl, ld = _rows(logits, ty["logits"], None, "logits")
+    T, V = logits.shape
+    _check("moe_token_logprobs", lib().moe_token_logprobs(
+        pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty["i32"], (T,), "targets"), inv_temperature,
+        n_top, _tensor(logprob, f32, (T,), "logprob"), _tensor(entropy, f32, (T,), "entropy"),
+        _tensor(stats, f32, (T, 2), "stats"), _tensor(top_ids, ty["i32"], (T, n_top), "top_ids"),
+        _tensor(top_logprob, f32, (T, n_top), "top_logprob"), _p(status), _stream(stream)))
+
+
+def moe_token_logprobs_backward(logits, targets, inv_temperature, stats, entropy, g_logprob, g_entropy, dlogits,
+                                status=None, stream=None):
+    """Gradient of moe_token_logprobs with respect to the logits; dlogits may
+    be the logits themselves."""
+    ty = _dt()
+    f32 = ty["f32"]
+    pl, ld = _rows(logits, ty["logits"], None, "logits")
+    T, V = logits.shape
+    pd, ldd = _rows(dlogits, ty["same"][logits.dtype], logits.shape, "dlogits")
+    _check("moe_token_logprobs_backward", lib().moe_token_logprobs_backward(
+        pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty["i32"], (T,), "targets"), inv_temperature,
+        _tensor(stats, f32, (T, 2), "stats"), _tensor(entropy, f32, (T,), "entropy"),
+        _tensor(g_logprob, f32, (T,), "g_logprob"), _tensor(g_entropy, f32, (T,), "g_entropy"), pd, ldd, _p(status),
+        _stream(stream)))
+
+
+def _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature):
+    pl, ld = _rows(logits, ty["logits"], None, "logits")
+    T, V = logits.shape
+    if teacher_ids.dim() != 2:
+        raise ValueError("teacher_ids: a 2-D tensor expected, got %s" % (tuple(teacher_ids.shape),))
+    K = teacher_ids.shape[1]
+    return (pl, 1 if logits.dtype in ty["f32"] else 0, ld, T, V,
+            _tensor(teacher_ids, ty["i32"], (T, K), "teacher_ids"),
+            _tensor(teacher_logits, ty["f32"], (T, K), "teacher_logits"),
+            _tensor(teacher_lse, ty["f32"], (T,), "teacher_lse"), K, inv_temperature)
+
+
+def moe_distill_topk(logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature, loss, stats, status=None,
+                     stream=None):
+    """KL divergence of the rows of logits [T][V] from a teacher's top
+    logits [T][K] (teacher_lse [T]: with the teacher's remaining mass as one
+    outcome; None: over the listed ids)."""
+    ty = _dt()
+    T = logits.shape[0]
+    a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
+    _check("moe_distill_topk", lib().moe_distill_topk(
+        *a, _tensor(loss, ty["f32"], (T,), "loss"), _tensor(stats, ty["f32"], (T, 4), "stats"), _p(status),
+        _stream(stream)))
+
+
+def moe_distill_topk_backward(logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature, stats, g, dlogits,
+                              status=None, stream=None):
+    """Gradient of moe_distill_topk from its stats; dlogits may be the logits
+    themselves."""
+    ty = _dt()
+    T = logits.shape[0]
+    a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
+    pd, ldd = _rows(dlogits, ty["same"][logits.dtype], logits.shape, "dlogits")
+    _check("moe_distill_topk_backward", lib().moe_distill_topk_backward(
+        *a, _tensor(stats, ty["f32"], (T, 4), "stats"), _tensor(g, ty["f32"], (T,), "g"), pd, ldd, _p(status),
+        _stream(stream)))
+
+
+def moe_distill_topk_train(logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature, g, loss, dlogits,
+                           status=None, stream=None):
+    """moe_distill_topk and its gradient in one call, each row's gradient
+    weighted by g."""
+    ty = _dt()
+    T = logits.shape[0]
+    a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
+    pd, ldd = _rows(dlogits, ty["same"][logits.dtype], logits.shape, "dlogits")
+    _check("moe_distill_topk_train", lib().moe_distill_topk_train(
+        *a, _tensor(g, ty["f32"], (T,), "g"), _tensor(loss, ty["f32"], (T,), "loss"), pd, ldd, _p(status),
+        _stream(stream)))
 
 
 class Pipeline:

@@ -204,6 +204,8 @@ int forward_impl(const uint16_t* x, const float* logits, int T, int E, int k, in
 
 }  // namespace
 
+int moe::check_device() { return ::check_device(); }
+
 extern "C" {
 
 int moe_abi_version(void) { return MOE_NVFP4_ABI_VERSION; }

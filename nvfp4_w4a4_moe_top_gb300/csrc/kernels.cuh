@@ -134,6 +134,7 @@ int launch_bwd_logits(const float* dw, const float* topk_w, const int32_t* topk_
                       float* dlogits, cudaStream_t stream);
 int launch_bwd_dx(const float* dxr, const int32_t* token_slot_row, int T, int k, int d, float* dx, cudaStream_t stream);
 
+int check_device();  // MOE_OK on compute capability 10.3, else the error code (abi.cu)
 int gemm_num_ctas();  // persistent grid size on the current device
 int launch_fc1(Fc1Args& a, int64_t m_cap, cudaStream_t stream);
 int launch_fc2(Fc2Args& a, int64_t m_cap, cudaStream_t stream);
