@@ -111,6 +111,39 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// ---- thread-block clusters: a row's blocks exchange their parts ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The 4 bytes at shared address p of block `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_load(const void* p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float cluster_load_f32(const float* p, uint32_t rank) {
+  return __uint_as_float(cluster_load(p, rank));
+}
+
 // A row of V elements as `head` elements up to the first 16-byte boundary,
 // `nvec` vectors of 16 bytes, and `tail` elements after them.
 template <typename E>
@@ -179,6 +212,89 @@ struct Soft {
       if (ENT) e = fmaf(w, fmaxf(d, -1e30f), e);
     }
   }
+  // A batch of 16-byte vectors of FP32 or BF16 logits.  One maximum and one
+  // rescaling for the batch, then packed arithmetic on pairs.  BF16 pairs are
+  // held at -2^119 at least before the differences: one packed instruction in
+  // place of two on the differences, and no difference from a maximum above
+  // -1e30 overflows.  Batches without such a maximum take add().
+  template <int U>
+  __device__ __forceinline__ void add_batch(const uint4 (&v)[U], float c, uint16_t) {
+    uint32_t w[4 * U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[4 * u] = v[u].x, w[4 * u + 1] = v[u].y, w[4 * u + 2] = v[u].z, w[4 * u + 3] = v[u].w;
+    uint32_t mx[4] = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+    for (int i = 4; i < 4 * U; ++i) mx[i & 3] = max_nan_bf16x2(mx[i & 3], w[i]);
+    const uint32_t mp = max_nan_bf16x2(max_nan_bf16x2(mx[0], mx[1]), max_nan_bf16x2(mx[2], mx[3]));
+    const float nm = max_nan(m, max_nan(bf16_lo(mp), bf16_hi(mp)));
+    if (ENT && !(nm >= -1e30f)) {  // masked so far, or NaN
+#pragma unroll 1
+      for (int u = 0; u < U; ++u) {
+        float x[8];
+        unpack(v[u], x);
+        add(x, c);
+      }
+      return;
+    }
+    rescale(nm, c);
+    const uint64_t nm2 = f32x2_pack(-nm, -nm), c2 = f32x2_pack(c, c);
+    uint64_t s2[2] = {f32x2_pack(s, 0.0f), 0ull}, e2[2] = {f32x2_pack(e, 0.0f), 0ull};
+#pragma unroll
+    for (int i = 0; i < 4 * U; ++i) {
+      const uint32_t p = ENT ? max_nan_bf16x2(w[i], 0xFB00FB00u) : w[i];  // -2^119
+      step(f32x2_pack(bf16_lo(p), bf16_hi(p)), nm2, c2, s2[i & 1], e2[i & 1]);
+    }
+    s = sum2(add_f32x2(s2[0], s2[1]));
+    if (ENT) e = sum2(add_f32x2(e2[0], e2[1]));
+  }
+  template <int U>
+  __device__ __forceinline__ void add_batch(const uint4 (&v)[U], float c, float) {
+    float mx[4] = {m, kLowest, kLowest, kLowest};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      mx[0] = max_nan(mx[0], __uint_as_float(v[u].x));
+      mx[1] = max_nan(mx[1], __uint_as_float(v[u].y));
+      mx[2] = max_nan(mx[2], __uint_as_float(v[u].z));
+      mx[3] = max_nan(mx[3], __uint_as_float(v[u].w));
+    }
+    const float nm = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
+    rescale(nm, c);
+    const uint64_t nm2 = f32x2_pack(-nm, -nm), c2 = f32x2_pack(c, c);
+    uint64_t s2[2] = {f32x2_pack(s, 0.0f), 0ull}, e2[2] = {f32x2_pack(e, 0.0f), 0ull};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      step_clamped(f32x2_pack(__uint_as_float(v[u].x), __uint_as_float(v[u].y)), nm2, c2, s2[0], e2[0]);
+      step_clamped(f32x2_pack(__uint_as_float(v[u].z), __uint_as_float(v[u].w)), nm2, c2, s2[1], e2[1]);
+    }
+    s = sum2(add_f32x2(s2[0], s2[1]));
+    if (ENT) e = sum2(add_f32x2(e2[0], e2[1]));
+  }
+  static __device__ __forceinline__ float sum2(uint64_t v) {
+    float a, b;
+    unpack2(v, a, b);
+    return a + b;
+  }
+  static __device__ __forceinline__ void step(uint64_t x, uint64_t nm2, uint64_t c2, uint64_t& s2, uint64_t& e2) {
+    const uint64_t d = add_f32x2(x, nm2);
+    float a, b;
+    unpack2(mul_f32x2(d, c2), a, b);
+    const uint64_t w = f32x2_pack(exp2_fast(a), exp2_fast(b));
+    s2 = add_f32x2(s2, w);
+    if (ENT) e2 = fma_f32x2(w, d, e2);
+  }
+  static __device__ __forceinline__ void step_clamped(uint64_t x, uint64_t nm2, uint64_t c2, uint64_t& s2, uint64_t& e2) {
+    uint64_t d = add_f32x2(x, nm2);
+    if (ENT) {
+      float a, b;
+      unpack2(d, a, b);
+      d = f32x2_pack(fmaxf(a, -1e30f), fmaxf(b, -1e30f));
+    }
+    float a, b;
+    unpack2(mul_f32x2(d, c2), a, b);
+    const uint64_t w = f32x2_pack(exp2_fast(a), exp2_fast(b));
+    s2 = add_f32x2(s2, w);
+    if (ENT) e2 = fma_f32x2(w, d, e2);
+  }
   __device__ __forceinline__ void merge(const Soft& o, float c) {
     const float nm = max_nan(m, o.m);
     Soft b = o;
@@ -238,15 +354,52 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 
 // Order of the alternatives: larger logit first, then the lower id.
 // -0 and +0 are equal.
-__device__ __forceinline__ uint64_t rank_key(float x, uint32_t id) {
+__device__ __forceinline__ uint32_t rank_value(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
-  const uint32_t o = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return ((uint64_t)o << 32) | (0xFFFFFFFFu - id);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t rank_key(float x, uint32_t id) {
+  return ((uint64_t)rank_value(x) << 32) | (0xFFFFFFFFu - id);
 }
 __device__ __forceinline__ float rank_logit(uint64_t key) {
   const uint32_t o = (uint32_t)(key >> 32);
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 __device__ __forceinline__ int rank_id(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
+
+// ---- lists of 32 keys held by a warp, lane i the i-th largest ----
+template <typename K>
+__device__ __forceinline__ K order_step(K v, int j, bool desc) {
+  const K p = __shfl_xor_sync(0xFFFFFFFFu, v, j);
+  return (((threadIdx.x & j) == 0) == desc) ? max(v, p) : min(v, p);
+}
+template <typename K>
+__device__ __forceinline__ K list_sort(K v) {
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+    for (int j = k >> 1; j > 0; j >>= 1) v = order_step(v, j, (threadIdx.x & 31 & k) == 0);
+  return v;
+}
+// The 32 largest of two sorted lists, sorted (a bitonic sequence, cleaned).
+template <typename K>
+__device__ __forceinline__ K list_merge(K a, K b) {
+  K v = max(a, __shfl_sync(0xFFFFFFFFu, b, 31 - (int)(threadIdx.x & 31)));
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) v = order_step(v, j, true);
+  return v;
+}
+// The 32 largest of the lists of the block's NW warps; warp 0 gets it.
+template <int NW, typename K>
+__device__ __forceinline__ K block_list_merge(K v, K (*lists)[32]) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = NW / 2; n > 0; n >>= 1) {
+    if (w >= n && w < 2 * n) lists[w][lane] = v;
+    __syncthreads();
+    if (w < n) v = list_merge(v, lists[w + n][lane]);
+  }
+  return v;
+}
 
 }  // namespace moe
