@@ -299,23 +299,37 @@ def _rows(t, dtypes, shape, what):
     return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
 
 
-_types = {}
+class _Types:
+    """The element types of the learner operators' tensors, once torch is
+    imported."""
+    ready = False
+
+    def load(self):
+        import torch
+        self.b16 = (torch.bfloat16, torch.int16, torch.uint16)
+        self.f32 = (torch.float32,)
+        self.i32 = (torch.int32,)
+        self.logits = self.b16 + self.f32
+        self.codes = (torch.uint8, torch.float8_e4m3fn)
+        self.scales = (torch.uint8, torch.float8_e8m0fnu)
+        self.same = {t: self.b16 for t in self.b16} | {torch.float32: self.f32}
+        # handle of the current stream; torch.cuda.current_stream() builds an
+        # object first, which takes as long as the launch
+        self.raw_stream, self.device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        self.ready = True
+
+
+_types = _Types()
 
 
 def _dt():
-    """The element types of the learner operators' tensors."""
-    if not _types:
-        import torch
-        b16 = (torch.bfloat16, torch.int16, torch.uint16)
-        _types.update(b16=b16, f32=(torch.float32,), i32=(torch.int32,), logits=b16 + (torch.float32,),
-                      codes=(torch.uint8, torch.float8_e4m3fn), scales=(torch.uint8, torch.float8_e8m0fnu),
-                      same={t: b16 for t in b16} | {torch.float32: (torch.float32,)})
+    if not _types.ready:
+        _types.load()
     return _types
 
 
 def _stream(stream):
-    import torch
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    return _types.raw_stream(_types.device()) if stream is None else stream.cuda_stream
 
 
 def mx8_sf_bytes(rows, d):
@@ -331,18 +345,18 @@ def moe_add_rmsnorm(x, res, w, eps, h, y, y8=None, y8_sf=None, rstd=None, status
     with y8 and y8_sf, in E4M3 with a power-of-two scale per 32 values.  x and
     res [T][d] may have strided rows."""
     ty = _dt()
-    b16 = ty["b16"]
+    b16 = ty.b16
     px, ldx = _rows(x, b16, None, "x")
     shape = x.shape
     T, d = shape
     pr, ldr = (None, d) if res is None else _rows(res, b16, shape, "res")
-    if y8_sf is not None and (not y8_sf.is_contiguous() or y8_sf.dtype not in ty["scales"]
-                              or y8_sf.numel() < mx8_sf_bytes(T, d)):
-        raise ValueError("y8_sf: at least %d contiguous scale bytes expected" % mx8_sf_bytes(T, d))
+    if y8_sf is not None and (not y8_sf.is_contiguous() or y8_sf.dtype not in ty.scales or not y8_sf.is_cuda
+                              or y8_sf.numel() < (T + 127) // 128 * (d // 128) * 512):
+        raise ValueError("y8_sf: at least %d contiguous scale bytes on the GPU expected" % mx8_sf_bytes(T, d))
     _check("moe_add_rmsnorm", lib().moe_add_rmsnorm(
         px, ldx, pr, ldr, _tensor(w, b16, (d,), "w"), eps, T, d, _tensor(h, b16, shape, "h"),
-        _tensor(y, b16, shape, "y"), _tensor(y8, ty["codes"], shape, "y8"),
-        None if y8_sf is None else y8_sf.data_ptr(), _tensor(rstd, ty["f32"], (T,), "rstd"), _p(status),
+        _tensor(y, b16, shape, "y"), _tensor(y8, ty.codes, shape, "y8"),
+        None if y8_sf is None else y8_sf.data_ptr(), _tensor(rstd, ty.f32, (T,), "rstd"), None if status is None else status.data_ptr(),
         _stream(stream)))
 
 
@@ -350,16 +364,16 @@ def moe_add_rmsnorm_backward(dy, dh, h, rstd, w, dx, dw, ws, status=None, stream
     """Gradients of moe_add_rmsnorm; dh (the gradient of h) and dw may be
     None."""
     ty = _dt()
-    b16 = ty["b16"]
+    b16 = ty.b16
     shape = dy.shape
     if dy.dim() != 2:
         raise ValueError("dy: a 2-D tensor expected, got %s" % (tuple(shape),))
     T, d = shape
     _check("moe_add_rmsnorm_backward", lib().moe_add_rmsnorm_backward(
         _tensor(dy, b16, shape, "dy"), _tensor(dh, b16, shape, "dh"), _tensor(h, b16, shape, "h"),
-        _tensor(rstd, ty["f32"], (T,), "rstd"), _tensor(w, b16, (d,), "w"), T, d, _tensor(dx, b16, shape, "dx"),
-        _tensor(dw, ty["f32"], (d,), "dw"), None if ws is None else ws.data_ptr(),
-        0 if ws is None else ws.numel() * ws.element_size(), _p(status), _stream(stream)))
+        _tensor(rstd, ty.f32, (T,), "rstd"), _tensor(w, b16, (d,), "w"), T, d, _tensor(dx, b16, shape, "dx"),
+        _tensor(dw, ty.f32, (d,), "dw"), None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.numel() * ws.element_size(), None if status is None else status.data_ptr(), _stream(stream)))
 
 
 def moe_token_logprobs(logits, targets, inv_temperature, n_top, logprob, entropy, stats, top_ids=None,
@@ -368,14 +382,14 @@ def moe_token_logprobs(logits, targets, inv_temperature, n_top, logprob, entropy
     n_top most likely ids of each row of logits [T][V] (strided rows
     allowed).  Outputs that are None are left out."""
     ty = _dt()
-    f32 = ty["f32"]
-    pl, ld = _rows(logits, ty["logits"], None, "logits")
+    f32 = ty.f32
+    pl, ld = _rows(logits, ty.logits, None, "logits")
     T, V = logits.shape
     _check("moe_token_logprobs", lib().moe_token_logprobs(
-        pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty["i32"], (T,), "targets"), inv_temperature,
+        pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty.i32, (T,), "targets"), inv_temperature,
         n_top, _tensor(logprob, f32, (T,), "logprob"), _tensor(entropy, f32, (T,), "entropy"),
-        _tensor(stats, f32, (T, 2), "stats"), _tensor(top_ids, ty["i32"], (T, n_top), "top_ids"),
-        _tensor(top_logprob, f32, (T, n_top), "top_logprob"), _p(status), _stream(stream)))
+        _tensor(stats, f32, (T, 2), "stats"), _tensor(top_ids, ty.i32, (T, n_top), "top_ids"),
+        _tensor(top_logprob, f32, (T, n_top), "top_logprob"), None if status is None else status.data_ptr(), _stream(stream)))
 
 
 def moe_token_logprobs_backward(logits, targets, inv_temperature, stats, entropy, g_logprob, g_entropy, dlogits,
@@ -383,27 +397,27 @@ def moe_token_logprobs_backward(logits, targets, inv_temperature, stats, entropy
     """Gradient of moe_token_logprobs with respect to the logits; dlogits may
     be the logits themselves."""
     ty = _dt()
-    f32 = ty["f32"]
-    pl, ld = _rows(logits, ty["logits"], None, "logits")
+    f32 = ty.f32
+    pl, ld = _rows(logits, ty.logits, None, "logits")
     T, V = logits.shape
-    pd, ldd = _rows(dlogits, ty["same"][logits.dtype], logits.shape, "dlogits")
+    pd, ldd = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
     _check("moe_token_logprobs_backward", lib().moe_token_logprobs_backward(
-        pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty["i32"], (T,), "targets"), inv_temperature,
+        pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty.i32, (T,), "targets"), inv_temperature,
         _tensor(stats, f32, (T, 2), "stats"), _tensor(entropy, f32, (T,), "entropy"),
-        _tensor(g_logprob, f32, (T,), "g_logprob"), _tensor(g_entropy, f32, (T,), "g_entropy"), pd, ldd, _p(status),
+        _tensor(g_logprob, f32, (T,), "g_logprob"), _tensor(g_entropy, f32, (T,), "g_entropy"), pd, ldd, None if status is None else status.data_ptr(),
         _stream(stream)))
 
 
 def _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature):
-    pl, ld = _rows(logits, ty["logits"], None, "logits")
+    pl, ld = _rows(logits, ty.logits, None, "logits")
     T, V = logits.shape
     if teacher_ids.dim() != 2:
         raise ValueError("teacher_ids: a 2-D tensor expected, got %s" % (tuple(teacher_ids.shape),))
     K = teacher_ids.shape[1]
-    return (pl, 1 if logits.dtype in ty["f32"] else 0, ld, T, V,
-            _tensor(teacher_ids, ty["i32"], (T, K), "teacher_ids"),
-            _tensor(teacher_logits, ty["f32"], (T, K), "teacher_logits"),
-            _tensor(teacher_lse, ty["f32"], (T,), "teacher_lse"), K, inv_temperature)
+    return (pl, 1 if logits.dtype in ty.f32 else 0, ld, T, V,
+            _tensor(teacher_ids, ty.i32, (T, K), "teacher_ids"),
+            _tensor(teacher_logits, ty.f32, (T, K), "teacher_logits"),
+            _tensor(teacher_lse, ty.f32, (T,), "teacher_lse"), K, inv_temperature)
 
 
 def moe_distill_topk(logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature, loss, stats, status=None,
@@ -415,7 +429,7 @@ def moe_distill_topk(logits, teacher_ids, teacher_logits, teacher_lse, inv_tempe
     T = logits.shape[0]
     a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
     _check("moe_distill_topk", lib().moe_distill_topk(
-        *a, _tensor(loss, ty["f32"], (T,), "loss"), _tensor(stats, ty["f32"], (T, 4), "stats"), _p(status),
+        *a, _tensor(loss, ty.f32, (T,), "loss"), _tensor(stats, ty.f32, (T, 4), "stats"), None if status is None else status.data_ptr(),
         _stream(stream)))
 
 
@@ -426,9 +440,9 @@ def moe_distill_topk_backward(logits, teacher_ids, teacher_logits, teacher_lse, 
     ty = _dt()
     T = logits.shape[0]
     a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
-    pd, ldd = _rows(dlogits, ty["same"][logits.dtype], logits.shape, "dlogits")
+    pd, ldd = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
     _check("moe_distill_topk_backward", lib().moe_distill_topk_backward(
-        *a, _tensor(stats, ty["f32"], (T, 4), "stats"), _tensor(g, ty["f32"], (T,), "g"), pd, ldd, _p(status),
+        *a, _tensor(stats, ty.f32, (T, 4), "stats"), _tensor(g, ty.f32, (T,), "g"), pd, ldd, None if status is None else status.data_ptr(),
         _stream(stream)))
 
 
@@ -439,9 +453,9 @@ def moe_distill_topk_train(logits, teacher_ids, teacher_logits, teacher_lse, inv
     ty = _dt()
     T = logits.shape[0]
     a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
-    pd, ldd = _rows(dlogits, ty["same"][logits.dtype], logits.shape, "dlogits")
+    pd, ldd = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
     _check("moe_distill_topk_train", lib().moe_distill_topk_train(
-        *a, _tensor(g, ty["f32"], (T,), "g"), _tensor(loss, ty["f32"], (T,), "loss"), pd, ldd, _p(status),
+        *a, _tensor(g, ty.f32, (T,), "g"), _tensor(loss, ty.f32, (T,), "loss"), pd, ldd, None if status is None else status.data_ptr(),
         _stream(stream)))
 
 

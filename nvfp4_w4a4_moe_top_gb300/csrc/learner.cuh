@@ -85,6 +85,9 @@ struct DistillArgs {
   int64_t ldd;
   int* status;
 };
+// Lets a kernel use `bytes` of dynamic shared memory on the current device.
+bool allow_smem(const void* kernel, int bytes);
+
 int launch_add_rmsnorm(const NormArgs& a, cudaStream_t s);
 size_t add_rmsnorm_backward_ws(int T, int d);
 int launch_add_rmsnorm_backward(const NormBwdArgs& a, cudaStream_t s);
@@ -93,7 +96,7 @@ int launch_token_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t s);
 int launch_distill(const DistillArgs& a, cudaStream_t s);
 
 constexpr float kLowest = -3.402823466e+38f;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FFFFFFFu); }
@@ -131,8 +134,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // The 4 bytes at shared address p of block `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_load(const void* p, uint32_t rank) {
   uint32_t a, v;
@@ -157,7 +160,10 @@ struct Row {
     nvec = (V - head) / kVec;
     tail = V - head - nvec * kVec;
   }
-  __device__ __forceinline__ const uint4* vec() const { return reinterpret_cast<const uint4*>(p + head); }
+  // The vectors; on a 16-byte boundary also where there are none.
+  __device__ __forceinline__ const uint4* vec() const {
+    return reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p + head) & ~(uintptr_t)15);
+  }
   __device__ __forceinline__ int tail_start() const { return head + nvec * kVec; }
 };
 
@@ -180,6 +186,22 @@ __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
 __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
   return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
+
+// Order of the alternatives: larger logit first, then the lower id.
+// -0 and +0 are equal, and max_nan's NaN is above all numbers.
+__device__ __forceinline__ uint32_t rank_value(float x) {
+  uint32_t b = __float_as_uint(x);
+  if (b == 0x80000000u) b = 0u;
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t rank_key(float x, uint32_t id) {
+  return ((uint64_t)rank_value(x) << 32) | (0xFFFFFFFFu - id);
+}
+__device__ __forceinline__ float rank_logit(uint64_t key) {
+  const uint32_t o = (uint32_t)(key >> 32);
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+__device__ __forceinline__ int rank_id(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
 // Softmax statistics of a set of logits: m their maximum (kLowest for none
 // but -inf, NaN with a NaN), s = sum 2^((x - m) c), and with ENT e = sum
@@ -211,89 +233,6 @@ struct Soft {
       s += w;
       if (ENT) e = fmaf(w, fmaxf(d, -1e30f), e);
     }
-  }
-  // A batch of 16-byte vectors of FP32 or BF16 logits.  One maximum and one
-  // rescaling for the batch, then packed arithmetic on pairs.  BF16 pairs are
-  // held at -2^119 at least before the differences: one packed instruction in
-  // place of two on the differences, and no difference from a maximum above
-  // -1e30 overflows.  Batches without such a maximum take add().
-  template <int U>
-  __device__ __forceinline__ void add_batch(const uint4 (&v)[U], float c, uint16_t) {
-    uint32_t w[4 * U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) w[4 * u] = v[u].x, w[4 * u + 1] = v[u].y, w[4 * u + 2] = v[u].z, w[4 * u + 3] = v[u].w;
-    uint32_t mx[4] = {w[0], w[1], w[2], w[3]};
-#pragma unroll
-    for (int i = 4; i < 4 * U; ++i) mx[i & 3] = max_nan_bf16x2(mx[i & 3], w[i]);
-    const uint32_t mp = max_nan_bf16x2(max_nan_bf16x2(mx[0], mx[1]), max_nan_bf16x2(mx[2], mx[3]));
-    const float nm = max_nan(m, max_nan(bf16_lo(mp), bf16_hi(mp)));
-    if (ENT && !(nm >= -1e30f)) {  // masked so far, or NaN
-#pragma unroll 1
-      for (int u = 0; u < U; ++u) {
-        float x[8];
-        unpack(v[u], x);
-        add(x, c);
-      }
-      return;
-    }
-    rescale(nm, c);
-    const uint64_t nm2 = f32x2_pack(-nm, -nm), c2 = f32x2_pack(c, c);
-    uint64_t s2[2] = {f32x2_pack(s, 0.0f), 0ull}, e2[2] = {f32x2_pack(e, 0.0f), 0ull};
-#pragma unroll
-    for (int i = 0; i < 4 * U; ++i) {
-      const uint32_t p = ENT ? max_nan_bf16x2(w[i], 0xFB00FB00u) : w[i];  // -2^119
-      step(f32x2_pack(bf16_lo(p), bf16_hi(p)), nm2, c2, s2[i & 1], e2[i & 1]);
-    }
-    s = sum2(add_f32x2(s2[0], s2[1]));
-    if (ENT) e = sum2(add_f32x2(e2[0], e2[1]));
-  }
-  template <int U>
-  __device__ __forceinline__ void add_batch(const uint4 (&v)[U], float c, float) {
-    float mx[4] = {m, kLowest, kLowest, kLowest};
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      mx[0] = max_nan(mx[0], __uint_as_float(v[u].x));
-      mx[1] = max_nan(mx[1], __uint_as_float(v[u].y));
-      mx[2] = max_nan(mx[2], __uint_as_float(v[u].z));
-      mx[3] = max_nan(mx[3], __uint_as_float(v[u].w));
-    }
-    const float nm = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
-    rescale(nm, c);
-    const uint64_t nm2 = f32x2_pack(-nm, -nm), c2 = f32x2_pack(c, c);
-    uint64_t s2[2] = {f32x2_pack(s, 0.0f), 0ull}, e2[2] = {f32x2_pack(e, 0.0f), 0ull};
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      step_clamped(f32x2_pack(__uint_as_float(v[u].x), __uint_as_float(v[u].y)), nm2, c2, s2[0], e2[0]);
-      step_clamped(f32x2_pack(__uint_as_float(v[u].z), __uint_as_float(v[u].w)), nm2, c2, s2[1], e2[1]);
-    }
-    s = sum2(add_f32x2(s2[0], s2[1]));
-    if (ENT) e = sum2(add_f32x2(e2[0], e2[1]));
-  }
-  static __device__ __forceinline__ float sum2(uint64_t v) {
-    float a, b;
-    unpack2(v, a, b);
-    return a + b;
-  }
-  static __device__ __forceinline__ void step(uint64_t x, uint64_t nm2, uint64_t c2, uint64_t& s2, uint64_t& e2) {
-    const uint64_t d = add_f32x2(x, nm2);
-    float a, b;
-    unpack2(mul_f32x2(d, c2), a, b);
-    const uint64_t w = f32x2_pack(exp2_fast(a), exp2_fast(b));
-    s2 = add_f32x2(s2, w);
-    if (ENT) e2 = fma_f32x2(w, d, e2);
-  }
-  static __device__ __forceinline__ void step_clamped(uint64_t x, uint64_t nm2, uint64_t c2, uint64_t& s2, uint64_t& e2) {
-    uint64_t d = add_f32x2(x, nm2);
-    if (ENT) {
-      float a, b;
-      unpack2(d, a, b);
-      d = f32x2_pack(fmaxf(a, -1e30f), fmaxf(b, -1e30f));
-    }
-    float a, b;
-    unpack2(mul_f32x2(d, c2), a, b);
-    const uint64_t w = f32x2_pack(exp2_fast(a), exp2_fast(b));
-    s2 = add_f32x2(s2, w);
-    if (ENT) e2 = fma_f32x2(w, d, e2);
   }
   __device__ __forceinline__ void merge(const Soft& o, float c) {
     const float nm = max_nan(m, o.m);
@@ -338,6 +277,200 @@ struct Soft {
   }
 };
 
+// Softmax statistics of a stream of logits, in base 2 about an integer shift:
+// m the maximum, M >= ceil(m c) an integer, s = sum 2^(x c - M), and with ENT
+// e = sum 2^(x c - M) (x c - M).  The exponent is one FMA, rounded once
+// whatever the size of x c, and changing the shift multiplies by a power of
+// two.  M stays at -2^20 or above, so parts of a row that hold only masks
+// (-inf or the type's lowest value) add zeros.  Rows whose own maximum leaves
+// |m c| above 2^20 need the differences formed first (Soft): see shift_ok.
+// BF16 pairs are held at -2^100 at least for ENT, so that a zero weight meets
+// a finite exponent.
+constexpr float kShiftLimit = 1048576.0f;  // 2^20
+
+template <bool ENT>
+struct Run {
+  float m = kLowest, M = -kShiftLimit, s = 0.0f, e = 0.0f;
+  // Whether the sums may be used, for the row's c (m is the row's maximum).
+  __device__ __forceinline__ bool shift_ok(float c) const { return fabsf(m * c) <= kShiftLimit; }
+  __device__ __forceinline__ void shift(float nM) {
+    const float d = M - nM;
+    const float f = exp2_fast(d);
+    if (ENT) e = f * fmaf(s, d, e);
+    s *= f;
+    M = nM;
+  }
+  __device__ __forceinline__ float raise(float x, float c) {
+    m = max_nan(m, x);
+    shift(fmaxf(ceilf(m * c), -kShiftLimit));
+    return x;
+  }
+  static __device__ __forceinline__ void step(uint64_t x, uint64_t c2, uint64_t nM2, uint64_t& s2, uint64_t& e2) {
+    const uint64_t t = fma_f32x2(x, c2, nM2);
+    float a, b;
+    unpack2(t, a, b);
+    const uint64_t w = f32x2_pack(exp2_fast(a), exp2_fast(b));
+    s2 = add_f32x2(s2, w);
+    if (ENT) e2 = fma_f32x2(w, t, e2);
+  }
+  __device__ __forceinline__ void take(const uint64_t (&s2)[2], const uint64_t (&e2)[2]) {
+    float a, b;
+    unpack2(add_f32x2(s2[0], s2[1]), a, b);
+    s += a + b;
+    if (ENT) {
+      unpack2(add_f32x2(e2[0], e2[1]), a, b);
+      e += a + b;
+    }
+  }
+  // A batch of 16-byte vectors of BF16 (or FP32) logits: one maximum and one
+  // shift for the batch, then packed arithmetic on pairs.  Returns the maximum.
+  template <int U>
+  __device__ __forceinline__ float add(const uint4 (&v)[U], float c, uint16_t) {
+    uint32_t w[4 * U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[4 * u] = v[u].x, w[4 * u + 1] = v[u].y, w[4 * u + 2] = v[u].z, w[4 * u + 3] = v[u].w;
+    uint32_t mx[4] = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+    for (int i = 4; i < 4 * U; ++i) mx[i & 3] = max_nan_bf16x2(mx[i & 3], w[i]);
+    const uint32_t mp = max_nan_bf16x2(max_nan_bf16x2(mx[0], mx[1]), max_nan_bf16x2(mx[2], mx[3]));
+    const float top = raise(max_nan(bf16_lo(mp), bf16_hi(mp)), c);
+    const uint64_t nM2 = f32x2_pack(-M, -M), c2 = f32x2_pack(c, c);
+    uint64_t s2[2] = {0ull, 0ull}, e2[2] = {0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < 4 * U; ++i) {
+      const uint32_t p = ENT ? max_nan_bf16x2(w[i], 0xF180F180u) : w[i];  // -2^100
+      step(f32x2_pack(bf16_lo(p), bf16_hi(p)), c2, nM2, s2[i & 1], e2[i & 1]);
+    }
+    take(s2, e2);
+    return top;
+  }
+  template <int U>
+  __device__ __forceinline__ float add(const uint4 (&v)[U], float c, float) {
+    float x[4 * U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      x[4 * u] = __uint_as_float(v[u].x), x[4 * u + 1] = __uint_as_float(v[u].y);
+      x[4 * u + 2] = __uint_as_float(v[u].z), x[4 * u + 3] = __uint_as_float(v[u].w);
+    }
+    return add(x, c);
+  }
+  template <int N>
+  __device__ __forceinline__ float add(const float (&x)[N], float c) {
+    float mx[2] = {x[0], x[N - 1]};
+#pragma unroll
+    for (int i = 1; i < N - 1; ++i) mx[i & 1] = max_nan(mx[i & 1], x[i]);
+    const float top = raise(max_nan(mx[0], mx[1]), c);
+    const uint64_t nM2 = f32x2_pack(-M, -M), c2 = f32x2_pack(c, c);
+    uint64_t s2[2] = {0ull, 0ull}, e2[2] = {0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float a = x[i], b = i + 1 < N ? x[i + 1] : neg_inf();
+      step(ENT ? f32x2_pack(fmaxf(a, -0x1p100f), fmaxf(b, -0x1p100f)) : f32x2_pack(a, b), c2, nM2, s2[i / 2 & 1],
+           e2[i / 2 & 1]);
+    }
+    take(s2, e2);
+    return top;
+  }
+  __device__ __forceinline__ void merge(const Run& o) {
+    const float nM = fmaxf(M, o.M);
+    Run b = o;
+    shift(nM);
+    b.shift(nM);
+    m = max_nan(m, o.m);
+    s += b.s;
+    e += b.e;
+  }
+  // Merged over the first 2^k lanes' parts (k from N), every lane gets it:
+  // the largest shift first, so that each part is scaled once.
+  template <int N>
+  __device__ __forceinline__ void warp_merge() {
+    const int top = __reduce_max_sync(0xFFFFFFFFu, (int)M);
+    m = rank_logit((uint64_t)__reduce_max_sync(0xFFFFFFFFu, rank_value(m)) << 32);
+    shift((float)top);
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      if (ENT) e += __shfl_xor_sync(0xFFFFFFFFu, e, o);
+    }
+  }
+};
+
+// `count` vectors of a part of a row, from vec.
+struct Part {
+  const uint4* vec;
+  int count;
+};
+
+// A sequence of row parts read by TH threads (thread k takes the vectors k, k
+// + TH, ..) through a ring of slots of the thread's own in shared memory: D
+// groups of U asynchronous 16-byte copies in flight, across the ends of rows,
+// and no barrier between threads.  part(t) names row t's part.
+template <int TH, int U, int D, typename E, typename P>
+struct Stream {
+  static constexpr int kBytesPerThread = U * D * 16;
+  P part;
+  uint4* ring;  // this thread's first slot; slots kStride apart
+  int stride, k;
+  int64_t T, step;
+  // next group to fetch: of row t, from vector i (this thread's)
+  int64_t t;
+  Part cur;
+  int i, fill, use;
+
+  __device__ __forceinline__ Stream(P p, uint4* ring_, int stride_, int k_, int64_t t0, int64_t step_, int64_t T_)
+      : part(p), ring(ring_), stride(stride_), k(k_), T(T_), step(step_), t(t0), i(0), fill(0), use(0) {
+    if (t < T) cur = part(t);
+#pragma unroll
+    for (int g = 0; g < D; ++g) fetch();
+  }
+  static __device__ __forceinline__ uint4 none(uint16_t) {
+    return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+  }
+  static __device__ __forceinline__ uint4 none(float) {
+    return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+  }
+  __device__ __forceinline__ void fetch() {
+    if (t < T) {
+      uint4* slot = ring + fill * U * stride;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = i + u * TH + k;
+        const bool in = at < cur.count;
+        cp_async16(smem_u32(slot + u * stride), cur.vec + (in ? at : 0), in);
+      }
+      fill = fill + 1 == D ? 0 : fill + 1;
+      i += U * TH;
+      if (i >= cur.count) {
+        i = 0;
+        t += step;
+        if (t < T) cur = part(t);
+      }
+    }
+    cp_async_commit();
+  }
+  // The vectors of the next row part (of `count`) in groups: f(v, g), g = 0, 1,
+  // ..  Places past the end hold -inf; an empty part is one group of such.
+  template <typename F>
+  __device__ __forceinline__ void row(int count, F f) {
+    int g = 0;
+    for (int j = 0; j == 0 || j < count; j += U * TH, ++g) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+      const uint4* slot = ring + use * U * stride;
+      use = use + 1 == D ? 0 : use + 1;
+      uint4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = slot[u * stride];
+      if (j + U * TH > count) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (j + u * TH + k >= count) v[u] = none(E());
+      }
+      f(v, g);
+      fetch();  // into the slots just read
+    }
+  }
+};
+
 // Sum over the block's NW warps in a fixed order; every thread gets it.
 template <int NW>
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -351,21 +484,6 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   __syncthreads();
   return v;
 }
-
-// Order of the alternatives: larger logit first, then the lower id.
-// -0 and +0 are equal.
-__device__ __forceinline__ uint32_t rank_value(float x) {
-  const uint32_t b = __float_as_uint(x + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ uint64_t rank_key(float x, uint32_t id) {
-  return ((uint64_t)rank_value(x) << 32) | (0xFFFFFFFFu - id);
-}
-__device__ __forceinline__ float rank_logit(uint64_t key) {
-  const uint32_t o = (uint32_t)(key >> 32);
-  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
-}
-__device__ __forceinline__ int rank_id(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
 // ---- lists of 32 keys held by a warp, lane i the i-th largest ----
 template <typename K>

@@ -4,50 +4,105 @@
 
 namespace moe {
 
-constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32;
-constexpr int kLpBatch = 4;     // 16-byte loads a thread has in flight
-constexpr int kLpPending = 64;  // candidates a warp holds before it sorts them
+constexpr int kLpThreads = 256;
+constexpr int kLpU = 4;  // vectors per group of copies
+constexpr int kLpBlocksPerSm = 3;
+// Groups in flight: 64 KB of ring per block, or 48 KB and the 8 KB of maxima
+// that the alternatives need.
+template <bool TOP>
+constexpr int kLpD = TOP ? 3 : 4;
+constexpr int kLpSlots = 8;  // maxima kept per thread
+// Resident grids of rows per launch at most: blocks that end early make room
+// for others (one grid of blocks that take all rows in turn waits for the
+// slowest SM: 4096 rows of 131072, 178 us against 158), and each still has a
+// next row to fetch while it ends one.
+constexpr int kLpTurns = 8;
+template <bool TOP>
+constexpr int kLpSmem = kLpThreads * (kLpU * kLpD<TOP> * 16 + (TOP ? kLpSlots * 4 : 0));
 
 __device__ __forceinline__ bool finite_max(float m) { return m <= 3.402823466e+38f; }  // not NaN, not +inf
 
-// The alternatives of a block's part of the row, from the threads' maxima: the
-// n-th largest of them is a lower bound of the n-th largest logit, so only the
-// threads that reach it (about n of them) hold candidates, and only their
-// vectors are read again (from L2).  Each warp takes its own threads one by
-// one, a vector per lane; candidates wait in shared memory until there are 32
-// to sort into the warp's list.  Returns the block's list in warp 0.
-template <typename E>
+// Barrier of the TH threads of a row.
+template <int TH>
+__device__ __forceinline__ void group_sync() {
+  if (TH == 32) __syncwarp();
+  else if (TH == kLpThreads) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"((int)threadIdx.x / TH + 1), "n"(TH) : "memory");
+}
+
+// The alternatives of a part of a row, read by TH threads.  A value that n
+// threads' maxima reach is a lower bound of the n-th largest logit.  Each
+// thread also keeps the maxima of up to kLpSlots runs of its vectors, so that
+// only the runs that reach the bound (little more than n) are read again, from
+// L2, by all threads together.  The few logits at or above the bound (ties
+// among them) are listed, and each finds its place by counting the larger
+// ones: no sorting, and no order of atomics in the result.  More runs or
+// candidates than fit (long ties) go through sorted lists of 32 per warp
+// instead (list_top).
+template <int TH>
 struct TopShared {
-  uint64_t lists[kLpWarps][32];
-  uint32_t vals[kLpWarps][32];
-  uint64_t pending[kLpWarps][kLpPending];
-  uint32_t bound;
+  static constexpr int NW = TH / 32, kCap = TH < 128 ? 128 : 256, kHot = TH < 64 ? 64 : TH;
+  uint64_t cand[kCap];
+  uint64_t pending[NW][64];
+  uint64_t lists[NW][32];
+  uint32_t vals[2][NW];
+  int hot[kHot];  // thread * kLpSlots + slot
+  int nhot, ncand;
 };
 
-template <typename E>
-__device__ __forceinline__ uint64_t block_top(const Row<E>& r, int v0, int v1, bool ends, float tmax, int n,
-                                              TopShared<E>& sh) {
-  constexpr int N = Row<E>::kVec;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t mine = rank_value(tmax);
-  const uint32_t top = block_list_merge<kLpWarps>(list_sort(mine), sh.vals);
-  if (warp == 0 && lane == n - 1) sh.bound = top;
-  __syncthreads();
-  const uint32_t bound = sh.bound;
+// A lower bound, reached by at least n of the threads, of the threads' maxima
+// (as rank_value): the n-th largest for one warp; else "k warps reach it with
+// j threads each", k j >= n, for the two smallest j that allow it.  Part 1,
+// before the group_sync: each warp's (j + 1)-th largest maximum, j = j0, j0 +
+// 1.
+template <int TH>
+__device__ __forceinline__ uint32_t top_bound1(uint32_t mine, int n, TopShared<TH>& sh) {
+  if (TH == 32) return __shfl_sync(0xFFFFFFFFu, list_sort(mine), n - 1);
+  constexpr int NW = TH / 32;
+  const int j0 = (n - 1) / NW, warp = (threadIdx.x & (TH - 1)) >> 5;
+  uint32_t v = mine, last = 0;
+  for (int j = 0; j <= j0 + 1; ++j) {
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, v);
+    if ((int)(threadIdx.x & 31) == __ffs(__ballot_sync(0xFFFFFFFFu, v == top)) - 1) v = 0;
+    if (j == j0) last = top;
+    if (j == j0 + 1 && (threadIdx.x & 31) < 2) sh.vals[threadIdx.x & 1][warp] = threadIdx.x & 1 ? top : last;
+  }
+  return 0;
+}
+template <int TH>
+__device__ __forceinline__ uint32_t top_bound2(uint32_t bound, int n, const TopShared<TH>& sh) {
+  if (TH == 32) return bound;
+  constexpr int NW = TH / 32;
+  const int lane = threadIdx.x & 31, j = (n - 1) / NW + 1 + lane / NW;  // threads per warp, lanes below 2 NW
+  const int k = (n + j - 1) / j;                                        // warps needed
+  const uint32_t* vals = sh.vals[lane / NW & 1];
+  const uint32_t v = vals[lane % NW];
+  int reach = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) reach += vals[w] >= v;
+  return __reduce_max_sync(0xFFFFFFFFu, lane < 2 * NW && reach >= k ? v : 0u);
+}
 
+// The candidates through per-warp lists of the 32 largest, each warp with its
+// own hot threads, 32 candidates at a time; any number of candidates.  The
+// group's list goes to sh.cand, zeros after the last.
+template <int TH, typename E>
+__device__ __noinline__ void list_top(const Row<E>& r, int v0, int v1, bool ends, uint32_t mine, uint32_t bound, int n,
+                                      TopShared<TH>& sh) {
+  constexpr int N = Row<E>::kVec, NW = TH / 32;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x & (TH - 1)) >> 5;
   uint64_t list = 0, least = (uint64_t)bound << 32;  // keys below `least` cannot enter
   uint64_t* pend = sh.pending[warp];
   int held = 0;
-  auto flush = [&](int k) {  // sort the first k <= 32 pending keys into the list
+  auto flush = [&]() {  // sorts up to 32 pending keys into the list
     __syncwarp();
-    const uint64_t key = lane < k ? pend[lane] : 0;
+    const uint64_t key = lane < held ? pend[lane] : 0;
     const uint64_t rest = lane + 32 < held ? pend[lane + 32] : 0;
     __syncwarp();
     if (lane + 32 < held) pend[lane] = rest;
     held = held > 32 ? held - 32 : 0;
     list = list_merge(list, list_sort(key));
-    const uint64_t nth = __shfl_sync(0xFFFFFFFFu, list, n - 1);
-    least = max(least, nth);
+    least = max(least, __shfl_sync(0xFFFFFFFFu, list, n - 1));
     __syncwarp();
   };
   auto offer = [&](float x, int id, bool valid) {
@@ -57,17 +112,17 @@ __device__ __forceinline__ uint64_t block_top(const Row<E>& r, int v0, int v1, b
     if (who == 0) return;
     if (in) pend[held + __popc(who & ((1u << lane) - 1))] = key;
     held += __popc(who);
-    if (held >= 32) flush(32);
+    if (held >= 32) flush();
   };
   uint32_t hot = __ballot_sync(0xFFFFFFFFu, mine >= bound);
   while (hot) {
     const int h = __ffs(hot) - 1;
     hot &= hot - 1;
-    for (int i0 = v0 + warp * 32 + h; i0 < v1; i0 += 32 * kLpThreads) {
-      const int i = i0 + lane * kLpThreads;
-      const bool valid = i < v1;
+    for (int i0 = v0 + warp * 32 + h; i0 < v1; i0 += 32 * TH) {
+      const bool valid = lane < (v1 - i0 + TH - 1) / TH;
+      const int i = i0 + (valid ? lane * TH : 0);
       float x[N];
-      unpack(__ldg(r.vec() + (valid ? i : i0)), x);
+      unpack(__ldg(r.vec() + i), x);
 #pragma unroll
       for (int e = 0; e < N; ++e) offer(x[e], r.head + i * N + e, valid);
     }
@@ -77,101 +132,271 @@ __device__ __forceinline__ uint64_t block_top(const Row<E>& r, int v0, int v1, b
     offer(a ? to_f32(r.p[lane]) : 0.0f, lane, a);
     offer(b ? to_f32(r.p[r.tail_start() + lane]) : 0.0f, r.tail_start() + lane, b);
   }
-  if (held) flush(held);
-  return block_list_merge<kLpWarps>(list, sh.lists);
+  if (held) flush();
+#pragma unroll
+  for (int m = NW / 2; m > 0; m >>= 1) {
+    if (warp >= m && warp < 2 * m) sh.lists[warp][lane] = list;
+    group_sync<TH>();
+    if (warp < m) list = list_merge(list, sh.lists[warp + m][lane]);
+  }
+  if (warp == 0) sh.cand[lane] = list;
 }
 
-// One row per cluster of gridDim.x blocks, each a contiguous part of its
-// vectors.  A thread keeps its own running maximum and sums (one pass, no
-// exchange until the end); the parts meet in the cluster's first block through
-// distributed shared memory.
-template <typename E, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(LogprobArgs a) {
-  __shared__ Soft<ENT> red[kLpWarps];
-  __shared__ Soft<ENT> part;
-  __shared__ uint64_t plist[32];
-  const int nb = gridDim.x, rank = blockIdx.x;
-  const int64_t t = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
-  if (t >= a.T) return;  // the whole cluster
-  const E* row = static_cast<const E*>(a.logits) + t * a.ld;
-  const Row<E> r(row, a.V);
-  const int v0 = (int)((int64_t)r.nvec * rank / nb), v1 = (int)((int64_t)r.nvec * (rank + 1) / nb);
-  const float c = a.inv_t * kLog2e;
-  Soft<ENT> acc;
-  const uint4* vec = r.vec();
-  int i = v0 + threadIdx.x;
-  for (; i + (kLpBatch - 1) * kLpThreads < v1; i += kLpBatch * kLpThreads) {
-    uint4 v[kLpBatch];
+// The candidates of the part into sh.cand; returns their number (keys of 0
+// count for nothing).  `mine`: the thread's maximum; slots: those of its runs,
+// each of U << shift vectors; bound1: top_bound1's.  Called by all TH threads
+// after a group_sync that follows top_bound1 and the last use of sh.ncand.
+template <int TH, typename E>
+__device__ __forceinline__ int group_top(const Row<E>& r, int v0, int v1, bool ends, float mine, uint32_t bound1,
+                                         const float* slots, int shift, int n, TopShared<TH>& sh) {
+  constexpr int N = Row<E>::kVec;
+  const int k = threadIdx.x & (TH - 1);
+  const int run = kLpU << shift, used = ((v1 - v0 + TH - 1) / TH + run - 1) / run;  // vectors in a run; runs
+  if (TH == 32 && n > 8) {  // the lanes' maxima bound little: with each lane's second run
+    float a = kLowest, b = kLowest;
+    for (int q = 0; q < used; ++q) {
+      const float x = slots[q * kLpThreads];
+      b = fmaxf(b, fminf(a, x));
+      a = fmaxf(a, x);
+    }
+    bound1 = __shfl_sync(0xFFFFFFFFu, list_merge(list_sort(rank_value(a)), list_sort(rank_value(b))), n - 1);
+  }
+  const uint32_t bound = top_bound2<TH>(bound1, n, sh);
+  const float fb = rank_logit((uint64_t)bound << 32);
+  if (mine >= fb)
+    for (int q = 0; q < used; ++q)
+      if (slots[q * kLpThreads] >= fb) {
+        const int at = atomicAdd(&sh.nhot, 1);
+        if (at < TopShared<TH>::kHot) sh.hot[at] = q << 16 | k;
+      }
+  if (k == 0) sh.ncand = 0;
+  group_sync<TH>();
+  auto offer = [&](float x, int id) {
+    if (x >= fb && x != neg_inf()) {
+      const int at = atomicAdd(&sh.ncand, 1);
+      if (at < TopShared<TH>::kCap) sh.cand[at] = rank_key(x, (uint32_t)id);
+    }
+  };
+  const int nhot = sh.nhot;
+  if (nhot <= TopShared<TH>::kHot) {
+    const int items = nhot * run;
+#pragma unroll 4
+    for (int q = k; q < items; q += TH) {
+      const int who = sh.hot[q / kLpU >> shift];
+      const int i = v0 + (who & 0xFFFF) + ((who >> 16) * run + (q & (run - 1))) * TH;
+      if (i < v1) {
+        float x[N];
+        unpack(__ldg(r.vec() + i), x);
+        uint32_t in = 0;
 #pragma unroll
-    for (int u = 0; u < kLpBatch; ++u) v[u] = TOP ? __ldg(vec + i + u * kLpThreads) : __ldcs(vec + i + u * kLpThreads);
-    acc.add_batch(v, c, E());
-  }
-  for (; i < v1; i += kLpThreads) {
-    const uint4 v[1] = {__ldg(vec + i)};
-    acc.add_batch(v, c, E());
-  }
-  if (rank == 0) {
-    if ((int)threadIdx.x < r.head) {
-      const float x[1] = {to_f32(row[threadIdx.x])};
-      acc.add(x, c);
-    }
-    if ((int)threadIdx.x < r.tail) {
-      const float x[1] = {to_f32(row[r.tail_start() + threadIdx.x])};
-      acc.add(x, c);
-    }
-  }
-  const float tmax = acc.m;
-  acc.template block_merge<kLpWarps>(c, red);
-  uint64_t list = 0;
-  if (TOP) {
-    __shared__ TopShared<E> top;
-    if (finite_max(acc.m) && acc.s > 0.0f) list = block_top(r, v0, v1, rank == 0, tmax, a.n_top, top);
-  }
-  if (nb > 1) {
-    if (threadIdx.x == 0) part = acc;
-    if (TOP && threadIdx.x < 32) plist[threadIdx.x] = list;
-    cluster_arrive();
-    cluster_wait();
-    if (rank == 0 && threadIdx.x < 32) {
-      for (int b = 1; b < nb; ++b) {
-        Soft<ENT> o;
-        o.m = cluster_load_f32(&part.m, b);
-        o.s = cluster_load_f32(&part.s, b);
-        if (ENT) o.e = cluster_load_f32(&part.e, b);
-        acc.merge(o, c);
-        if (TOP) {
-          const uint32_t* p = reinterpret_cast<const uint32_t*>(&plist[threadIdx.x]);
-          const uint64_t lo = cluster_load(p, b), hi = cluster_load(p + 1, b);
-          list = list_merge(list, lo | (hi << 32));
+        for (int e = 0; e < N; ++e) in |= (x[e] >= fb ? 1u : 0u) << e;
+        if (in) {
+          int at = atomicAdd(&sh.ncand, __popc(in));
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (in >> e & 1) {
+              if (at < TopShared<TH>::kCap) sh.cand[at] = rank_key(x[e], (uint32_t)(r.head + i * N + e));
+              ++at;
+            }
         }
       }
     }
-    cluster_arrive();  // the other blocks' shared memory is read no more
-    cluster_wait();
-  }
-  if (rank != 0 || threadIdx.x >= 32) return;
-  const bool bad = !finite_max(acc.m), none = acc.s == 0.0f;
-  const float l = logf(acc.s), nan = quiet_nan();
-  if (threadIdx.x == 0) {
-    if (bad) set_status(a.status, MOE_STATUS_NONFINITE_LOGITS);
-    if (a.logprob) {
-      const int y = a.targets[t];
-      if (y >= a.V) set_status(a.status, MOE_STATUS_BAD_TOKEN);
-      float lp = 0.0f;
-      if (y >= 0 && y < a.V) lp = bad ? nan : none ? neg_inf() : (to_f32(row[y]) - acc.m) * a.inv_t - l;
-      a.logprob[t] = lp;
-    }
-    if (ENT) a.entropy[t] = bad ? nan : none ? 0.0f : l - a.inv_t * (acc.e / acc.s);
-    if (a.stats) {
-      a.stats[2 * t] = bad ? nan : none ? neg_inf() : acc.m;
-      a.stats[2 * t + 1] = bad ? nan : none ? 0.0f : l;
+    if (ends) {
+      if (k < r.head) offer(to_f32(r.p[k]), k);
+      if (k < r.tail) offer(to_f32(r.p[r.tail_start() + k]), r.tail_start() + k);
     }
   }
-  if (TOP && (int)threadIdx.x < a.n_top) {
-    if (bad) list = 0;
-    a.top_ids[t * a.n_top + threadIdx.x] = list ? rank_id(list) : -1;
-    a.top_logprob[t * a.n_top + threadIdx.x] =
-        bad ? nan : list ? (rank_logit(list) - acc.m) * a.inv_t - l : neg_inf();
+  group_sync<TH>();
+  const int c = sh.ncand;
+  if (k == 0) sh.nhot = 0;
+  if (nhot <= TopShared<TH>::kHot && c <= TopShared<TH>::kCap) return c;
+  list_top<TH>(r, v0, v1, ends, rank_value(mine), bound, n, sh);
+  group_sync<TH>();
+  return 32;
+}
+
+// put(place, key) for each of the n largest of the keys cand[0..c) of a group.
+template <int TH, typename F>
+__device__ __forceinline__ void place_top(const uint64_t* cand, int c, int n, F put) {
+  for (int q = threadIdx.x & (TH - 1); q < c; q += TH) {
+    const uint64_t key = cand[q];
+    int larger = 0;
+    for (int j = 0; j < c; j += 8) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) larger += cand[j + u] > key && j + u < c;  // the array is a multiple of 8
+    }
+    if (key != 0 && larger < n) put(larger, key);
+  }
+}
+
+// TH threads per row (or, for a cluster of nb = gridDim.x blocks, per part of
+// a row), the blocks taking rows in turn.  A thread keeps its own running
+// maximum and sums over its vectors; the threads meet at the row's end while
+// the next row's vectors are on their way.  The parts of a cluster meet in its
+// first block through distributed shared memory.
+template <typename E, bool ENT, bool TOP, int TH>
+__global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_kernel(LogprobArgs a) {
+  constexpr int NW = TH / 32, NG = kLpThreads / TH;
+  extern __shared__ uint4 ring[];
+  __shared__ Run<ENT> red[2][kLpThreads / 32];
+  __shared__ Run<ENT> cpart;
+  __shared__ uint64_t clist[32];
+  __shared__ TopShared<TH> tops[TOP ? NG : 1];
+  const int nb = TH < kLpThreads ? 1 : gridDim.x, rank = TH < kLpThreads ? 0 : blockIdx.x;
+  const int group = threadIdx.x / TH, k = threadIdx.x & (TH - 1), lane = threadIdx.x & 31;
+  TopShared<TH>& top = tops[TOP ? group : 0];
+  const int64_t t0 = (int64_t)blockIdx.y * NG + group, step = (int64_t)gridDim.y * NG;
+  const float c = a.inv_t * kLog2e;
+  const E* logits = static_cast<const E*>(a.logits);
+  auto part = [&](int64_t t) {
+    const Row<E> r(logits + t * a.ld, a.V);
+    const int v0 = (int)((int64_t)r.nvec * rank / nb), v1 = (int)((int64_t)r.nvec * (rank + 1) / nb);
+    return Part{r.vec() + v0, v1 - v0};
+  };
+  if (TOP && k == 0) top.nhot = 0;
+  // Runs of 2^shift groups per slot, enough for the longest part.
+  float* slots = reinterpret_cast<float*>(ring + kLpThreads * kLpU * kLpD<TOP>) + threadIdx.x;
+  const int groups = (a.V / Row<E>::kVec / nb + kLpU * TH) / (kLpU * TH), runs = (groups + kLpSlots - 1) / kLpSlots;
+  const int shift = runs <= 1 ? 0 : 32 - __clz(runs - 1);
+  Stream<TH, kLpU, kLpD<TOP>, E, decltype(part)> stream(part, ring + threadIdx.x, kLpThreads, k, t0, step, a.T);
+  int odd = 0, ynext = a.logprob && k == 0 && rank == 0 && t0 < a.T ? a.targets[t0] : -1;
+  for (int64_t t = t0; t < a.T; t += step, odd ^= 1) {
+    const E* row = logits + t * a.ld;
+    const Row<E> r(row, a.V);
+    const int v0 = (int)((int64_t)r.nvec * rank / nb), v1 = (int)((int64_t)r.nvec * (rank + 1) / nb);
+    // the target's logit, needed at the end, and the next row's target
+    const int y = ynext;
+    const float xy = y >= 0 && y < a.V ? to_f32(row[y]) : 0.0f;
+    if (a.logprob && k == 0 && rank == 0 && t + step < a.T) ynext = a.targets[t + step];
+    Run<ENT> acc;
+    int slot = 0, left = 1 << shift;
+    float high = kLowest;
+    stream.row(v1 - v0, [&](const auto& v, int) {
+      const float mx = acc.add(v, c, E());
+      if (TOP) {
+        high = fmaxf(high, mx);
+        slots[slot * kLpThreads] = high;
+        if (--left == 0) ++slot, left = 1 << shift, high = kLowest;
+      }
+    });
+    if (rank == 0) {
+      if (k < r.head) {
+        const float x[1] = {to_f32(row[k])};
+        acc.add(x, c);
+      }
+      if (k < r.tail) {
+        const float x[1] = {to_f32(row[r.tail_start() + k])};
+        acc.add(x, c);
+      }
+    }
+    const float mine = acc.m;
+    uint32_t bound1 = 0;
+    if (TOP && (TH > 32 || a.n_top <= 8)) bound1 = top_bound1<TH>(rank_value(mine), a.n_top, top);
+    acc.template warp_merge<32>();
+    if (NW > 1) {
+      if (lane == 0) red[odd][threadIdx.x >> 5] = acc;
+      group_sync<TH>();
+      Run<ENT> b;
+      if (lane < NW) b = red[odd][group * NW + lane];
+      b.template warp_merge<NW>();
+      // lanes of one result: NW is a power of two below 32, lanes 0 .. NW - 1 hold it
+      acc.m = b.m, acc.M = b.M;
+      acc.s = __shfl_sync(0xFFFFFFFFu, b.s, 0);
+      if (ENT) acc.e = __shfl_sync(0xFFFFFFFFu, b.e, 0);
+    }
+    int found = 0;
+    if (TOP) {
+      if (NW == 1) __syncwarp();
+      if (finite_max(acc.m)) found = group_top<TH>(r, v0, v1, rank == 0, mine, bound1, slots, shift, a.n_top, top);
+    }
+    if (nb > 1) {
+      if (threadIdx.x == 0) cpart = acc;
+      if (TOP) {
+        if (threadIdx.x < 32) clist[threadIdx.x] = 0;
+        __syncthreads();
+        place_top<TH>(top.cand, found, a.n_top, [&](int at, uint64_t key) { clist[at] = key; });
+      }
+      cluster_arrive();
+      cluster_wait();
+      if (rank == 0) {
+        Run<ENT> b;
+        if (lane < nb) {
+          b.m = cluster_load_f32(&cpart.m, lane);
+          b.M = cluster_load_f32(&cpart.M, lane);
+          b.s = cluster_load_f32(&cpart.s, lane);
+          if (ENT) b.e = cluster_load_f32(&cpart.e, lane);
+        }
+        b.template warp_merge<8>();
+        acc.m = b.m, acc.M = b.M;
+        acc.s = __shfl_sync(0xFFFFFFFFu, b.s, 0);
+        if (ENT) acc.e = __shfl_sync(0xFFFFFFFFu, b.e, 0);
+        if (TOP) {  // the parts' lists, all threads done with this block's own candidates
+          found = finite_max(acc.m) ? nb * 32 : 0;
+          if ((int)threadIdx.x < found) {
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(&clist[lane]);
+            const uint64_t lo = cluster_load(p, threadIdx.x >> 5), hi = cluster_load(p + 1, threadIdx.x >> 5);
+            top.cand[threadIdx.x] = lo | (hi << 32);
+          }
+        }
+      }
+      cluster_arrive();  // the other blocks' shared memory is read no more
+      cluster_wait();
+      if (rank != 0) continue;
+      if (TOP) __syncthreads();
+    }
+    // ln-sum about the maximum, and entropy, of the row
+    const bool bad = !finite_max(acc.m);
+    bool none = false;
+    const float log2s = log2f(acc.s);
+    float l = kLn2 * (log2s - fmaf(acc.m, c, -acc.M));
+    float H = ENT ? kLn2 * (log2s - acc.e / acc.s) : 0.0f;
+    if (!bad && !acc.shift_ok(c)) {  // beyond the shift's range, or nothing but masks: differences first
+      Soft<ENT> all;
+      for (int i = k; i < a.V; i += TH) {
+        const float x[1] = {to_f32(row[i])};
+        all.add(x, c);
+      }
+      all.warp_merge(c);
+      if (NW > 1) {
+        __shared__ Soft<ENT> sred[kLpThreads / 32];
+        if (lane == 0) sred[threadIdx.x >> 5] = all;
+        group_sync<TH>();
+        all = Soft<ENT>();
+        if (lane < NW) all = sred[group * NW + lane];
+        all.warp_merge(c);
+        group_sync<TH>();
+      }
+      none = all.s == 0.0f;
+      l = logf(all.s);
+      if (ENT) H = l - a.inv_t * (all.e / all.s);
+    }
+    const float nan = quiet_nan();
+    auto logp = [&](float x) { return (x - acc.m) * a.inv_t - l; };
+    if (k == 0) {
+      if (bad) set_status(a.status, MOE_STATUS_NONFINITE_LOGITS);
+      if (a.logprob) {
+        if (y >= a.V) set_status(a.status, MOE_STATUS_BAD_TOKEN);
+        a.logprob[t] = y < 0 || y >= a.V ? 0.0f : bad ? nan : none ? neg_inf() : logp(xy);
+      }
+      if (ENT) a.entropy[t] = bad ? nan : none ? 0.0f : H;
+      if (a.stats) {
+        a.stats[2 * t] = bad ? nan : none ? neg_inf() : acc.m;
+        a.stats[2 * t + 1] = bad ? nan : none ? 0.0f : l;
+      }
+    }
+    if (TOP) {
+      int32_t* ids = a.top_ids + t * a.n_top;
+      float* lps = a.top_logprob + t * a.n_top;
+      if (found <= 32 || nb > 1) {  // places that may stay empty
+        for (int q = k; q < a.n_top; q += TH) ids[q] = -1, lps[q] = bad ? nan : neg_inf();
+        group_sync<TH>();
+      }
+      place_top<TH>(top.cand, found, a.n_top, [&](int at, uint64_t key) {
+        ids[at] = rank_id(key);
+        lps[at] = logp(rank_logit(key));
+      });
+      group_sync<TH>();  // the candidates are read no more
+    }
   }
 }
 
@@ -250,17 +475,37 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_backward_kernel(Log
 }
 
 // host launchers
+template <typename E, int TH>
+static void (*token_logprobs_of(bool ent, bool top))(LogprobArgs) {
+  return ent ? (top ? token_logprobs_kernel<E, true, true, TH> : token_logprobs_kernel<E, true, false, TH>)
+             : (top ? token_logprobs_kernel<E, false, true, TH> : token_logprobs_kernel<E, false, false, TH>);
+}
+template <typename E>
+static void (*token_logprobs_of(int th, bool ent, bool top))(LogprobArgs) {
+  return th == 32    ? token_logprobs_of<E, 32>(ent, top)
+         : th == 128 ? token_logprobs_of<E, 128>(ent, top)
+                     : token_logprobs_of<E, kLpThreads>(ent, top);
+}
 int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
-  // Blocks per row: one where the rows alone fill two blocks per SM, else as
-  // many (up to 8, a portable cluster) as do, while each keeps a batch of
-  // loads per thread.
-  const int64_t nvec = (int64_t)a.V * (a.dtype == MOE_DTYPE_BF16 ? 2 : 4) / 16;
+  const bool bf = a.dtype == MOE_DTYPE_BF16, ent = a.entropy != nullptr, top = a.n_top > 0;
+  const int64_t nvec = (int64_t)a.V * (bf ? 2 : 4) / 16;
+  const int most = kLpBlocksPerSm * gemm_num_ctas();  // resident blocks
+  // Threads per row.  With enough rows to fill the GPU, as few as hide the
+  // row's end (sums, alternatives) behind other rows: a warp for short rows,
+  // four for long ones (4000 x 8192 BF16: 16, 19 and 29 us with 32, 128 and
+  // 256 threads; 4000 x 50000: 67, 62 and 73 us).  Else blocks, and clusters of
+  // up to 8 of them while they fill the GPU and each thread keeps two vectors.
+  const int th = nvec <= 1024 && (a.T >= 304 || nvec <= 128) ? 32 : a.T >= 304 ? 128 : kLpThreads;
   int nb = 1;
-  while (nb < 8 && (int64_t)a.T * nb < 304 && nvec / (nb * 2) >= kLpThreads) nb *= 2;
-  const unsigned gy = a.T < 65535 ? a.T : 65535, gz = (a.T + gy - 1) / gy;
+  if (th == kLpThreads)
+    while (nb < 8 && (int64_t)a.T * nb * 2 <= most && nvec / (nb * 2) >= 2 * kLpThreads) nb *= 2;
+  const int64_t per = kLpThreads / th, want = (a.T + per - 1) / per;
+  const int64_t grid = nb > 1 ? most / nb : (int64_t)most * kLpTurns;
+  const int smem = top ? kLpSmem<true> : kLpSmem<false>;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(nb, gy, gz);
+  cfg.gridDim = dim3(nb, (unsigned)(want < grid ? want : grid));
   cfg.blockDim = dim3(kLpThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -268,14 +513,8 @@ int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = nb > 1 ? 1 : 0;
-  const bool ent = a.entropy != nullptr, top = a.n_top > 0;
-  void (*f)(LogprobArgs);
-  if (a.dtype == MOE_DTYPE_BF16)
-    f = ent ? (top ? token_logprobs_kernel<uint16_t, true, true> : token_logprobs_kernel<uint16_t, true, false>)
-            : (top ? token_logprobs_kernel<uint16_t, false, true> : token_logprobs_kernel<uint16_t, false, false>);
-  else
-    f = ent ? (top ? token_logprobs_kernel<float, true, true> : token_logprobs_kernel<float, true, false>)
-            : (top ? token_logprobs_kernel<float, false, true> : token_logprobs_kernel<float, false, false>);
+  auto f = bf ? token_logprobs_of<uint16_t>(th, ent, top) : token_logprobs_of<float>(th, ent, top);
+  if (!allow_smem((const void*)f, smem)) return -1;
   return cudaLaunchKernelEx(&cfg, f, a) == cudaSuccess ? 0 : -1;
 }
 int launch_token_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t s) {

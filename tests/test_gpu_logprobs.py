@@ -52,7 +52,7 @@ def near(got, ref, tol):
 
 
 SHAPES = [(1, 1), (6, 1), (7, 2), (6, 5), (9, 8), (6, 31), (40, 257), (7, 1000), (6, 4096), (11, 12345), (6, 50001),
-          (1, 131072), (3, 131071), (300, 2048), (1, 262147)]
+          (1, 131072), (3, 131071), (300, 2048), (1, 262147), (4000, 65), (600, 17000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
