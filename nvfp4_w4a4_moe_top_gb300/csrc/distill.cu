@@ -3,162 +3,543 @@
 
 namespace moe {
 
-constexpr int kDsThreads = 512, kDsWarps = kDsThreads / 32;
+constexpr int kDsU = 4, kDsD = 3;  // vectors per group of copies, groups in flight
+constexpr int kDsMaxThreads = 1024;
+#ifndef DSTURNS
+#define DSTURNS 4
+#endif
 
-// The teacher's entry of one thread (j = threadIdx.x < K): id < 0 where there
-// is none.
-struct Entry {
-  int id;
-  float a;
-};
-
-// Row scalars of the teacher.
-struct Teacher {
-  float q, lq;  // this thread's entry (q = 0 where there is none)
-  float r, Q;   // mass off the list; total mass
-};
-
-// Reads entry j of row t and drops bad ids and repeats (the first stays).
-// ids: shared, MOE_DISTILL_MAX_K ints.
-__device__ __forceinline__ Entry load_entry(const DistillArgs& a, int64_t t, int* ids) {
-  Entry en = {-1, 0.0f};
-  const int j = threadIdx.x;
-  if (j < a.K) {
-    en.id = a.teacher_ids[t * a.K + j];
-    en.a = a.teacher_logits[t * a.K + j];
-    ids[j] = en.id;
-  }
-  __syncthreads();
-  if (j < a.K && en.id >= 0) {
-    bool ok = en.id < a.V;
-    for (int i = 0; i < j && ok; ++i) ok = ids[i] != en.id;
-    if (!ok) {
-      set_status(a.status, MOE_STATUS_BAD_TOKEN);
-      en.id = -1;
-    } else if (!(en.a <= 3.402823466e+38f)) {
-      set_status(a.status, MOE_STATUS_NONFINITE_LOGITS);
-      en.a = quiet_nan();
-    }
-  }
-  return en;
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
 }
 
-template <int NW>
-__device__ __forceinline__ Teacher teacher_mass(const DistillArgs& a, int64_t t, const Entry& en, float* red,
-                                                Soft<false>* sred) {
+// The row's list in shared memory: ids (-1: no entry), the teacher's logits,
+// the student's logits.
+struct DsList {
+  int id[MOE_DISTILL_MAX_K];
+  float a[MOE_DISTILL_MAX_K];
+  float x[MOE_DISTILL_MAX_K];
+};
+
+// The teacher's side of a row, by one warp: ln q_j = (a_j - base) inv_t - shift
+// (q = 0 where there is no entry), r its mass off the list, Q = sum q + r.
+struct Teacher {
+  float base, shift, r, Q;
+  __device__ __forceinline__ float lq(float a, float inv_t) const { return (a - base) * inv_t - shift; }
+};
+__device__ __forceinline__ Teacher teacher_side(const DsList& li, int K, float inv_t, const float* lse, int64_t t,
+                                                int* status) {
+  const int lane = threadIdx.x & 31;
   Teacher T;
-  const bool live = en.id >= 0;
-  if (a.teacher_lse) {
-    const float L = a.teacher_lse[t];
-    if (!(fabsf(L) <= 3.402823466e+38f) && threadIdx.x == 0) set_status(a.status, MOE_STATUS_NONFINITE_LOGITS);
-    T.lq = en.a * a.inv_t - L;
-    T.q = live ? expf(T.lq) : 0.0f;
-    const float sum = block_sum<NW>(T.q, red);
+  bool bad = false;
+  if (lse) {
+    T.base = 0.0f;
+    T.shift = lse[t];
+    bad = !(fabsf(T.shift) <= 3.402823466e+38f);
+    float sum = 0.0f;
+    for (int j = lane; j < K; j += 32)
+      if (li.id[j] >= 0) {
+        bad |= !(li.a[j] <= 3.402823466e+38f);
+        sum += expf(T.lq(li.a[j], inv_t));
+      }
+    sum = warp_sum(sum);
     T.r = max_nan(1.0f - sum, 0.0f);
     T.Q = T.r > 0.0f ? 1.0f : sum;
   } else {
-    const float c = a.inv_t * kLog2e;
-    Soft<false> acc;
-    if (live) {
-      const float x[1] = {en.a};
-      acc.add(x, c);
-    }
-    acc.template block_merge<NW>(c, sred);
-    T.lq = (en.a - acc.m) * a.inv_t - logf(acc.s);
-    T.q = live && acc.s > 0.0f ? expf(T.lq) : 0.0f;
-    if (live && !(acc.m <= 3.402823466e+38f)) T.q = T.lq = quiet_nan();
+    float m = kLowest;
+    for (int j = lane; j < K; j += 32)
+      if (li.id[j] >= 0) {
+        bad |= !(li.a[j] <= 3.402823466e+38f);
+        m = max_nan(m, li.a[j]);
+      }
+    m = warp_max_nan(m);
+    float sum = 0.0f;
+    for (int j = lane; j < K; j += 32)
+      if (li.id[j] >= 0) sum += expf((li.a[j] - m) * inv_t);
+    sum = warp_sum(sum);
+    T.base = m;
+    T.shift = logf(sum);
     T.r = 0.0f;
-    T.Q = acc.s > 0.0f || !(acc.m <= 3.402823466e+38f) ? 1.0f : 0.0f;
+    T.Q = sum == 0.0f ? 0.0f : 1.0f;
   }
+  if (bad) set_status(status, MOE_STATUS_NONFINITE_LOGITS);
+  if (__any_sync(0xFFFFFFFFu, bad)) T.shift = T.Q = quiet_nan();
   return T;
 }
+__device__ __forceinline__ float teacher_q(const Teacher& T, const DsList& li, int j, float inv_t) {
+  return li.id[j] < 0 || T.Q == 0.0f ? 0.0f : expf(T.lq(li.a[j], inv_t));
+}
 
-struct DsShared {
-  int ids[MOE_DISTILL_MAX_K];
-  Soft<false> sred[kDsWarps];
-  float red[kDsWarps];
-};
+// The 16-byte vector with its listed elements replaced by -inf; bit e of
+// `bits`: element e.
+__device__ __forceinline__ void drop_listed(uint4& v, uint32_t bits, uint16_t) {
+  auto word = [&](uint32_t x, uint32_t b) {
+    const uint32_t m = (b & 1u) * 0xFFFFu | (b >> 1 & 1u) * 0xFFFF0000u;
+    return (x & ~m) | (m & 0xFF80FF80u);
+  };
+  v = make_uint4(word(v.x, bits), word(v.y, bits >> 2), word(v.z, bits >> 4), word(v.w, bits >> 6));
+}
+__device__ __forceinline__ void drop_listed(uint4& v, uint32_t bits, float) {
+  if (bits & 1u) v.x = 0xFF800000u;
+  if (bits & 2u) v.y = 0xFF800000u;
+  if (bits & 4u) v.z = 0xFF800000u;
+  if (bits & 8u) v.w = 0xFF800000u;
+}
+// Bits of the listed elements of vector i of the row (kVec bits each, vector 0
+// after a place for the elements before it).
+__device__ __forceinline__ uint32_t listed_bits(const uint32_t* bits, int i, uint16_t) {
+  return reinterpret_cast<const uint8_t*>(bits)[i + 1];
+}
+__device__ __forceinline__ uint32_t listed_bits(const uint32_t* bits, int i, float) {
+  return reinterpret_cast<const uint8_t*>(bits)[(i + 1) >> 1] >> ((i + 1 & 1) * 4) & 15u;
+}
 
-// LOSS: the statistics and the loss; GRAD: the gradient, from the statistics
-// just computed or (without LOSS) the stored ones.
-template <typename E, bool LOSS, bool GRAD>
-__global__ void __launch_bounds__(kDsThreads) distill_kernel(DistillArgs a) {
-  extern __shared__ uint32_t listed[];  // one bit per id of the row
-  __shared__ DsShared sh;
-  const int64_t t = blockIdx.x;
-  const E* row = static_cast<const E*>(a.logits) + t * a.ld;
+// The loss, and with GRAD the gradient, of rows in turn, TH threads (one
+// block) per row or, in a cluster of gridDim.x blocks, per part of a row.  A
+// bit per id marks the listed ones, whose elements leave the stream, so that
+// the mass off the list is summed by itself.  With GRAD a part of at most
+// (kDsD - 1) groups stays in the ring's slots between the sums and the
+// gradient: the logits are read from memory once.  Longer parts are read again.
+template <typename E, bool GRAD, int TH>
+__global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(DistillArgs a) {
+  constexpr int N = Row<E>::kVec, NW = TH / 32;
+  extern __shared__ uint4 ring[];
+  __shared__ DsList list;
+  __shared__ Run<false> red[NW];
+  __shared__ Run<false> cpart;
+  __shared__ Soft<false> sred[NW];
+  __shared__ float coef[4];  // weight of the part off the list, its shift (or maximum), whether slow
+  __shared__ int dup;
+  const int nb = gridDim.x, rank = blockIdx.x, k = threadIdx.x, lane = k & 31;
+  const int64_t t0 = blockIdx.y, step = gridDim.y;
   const float c = a.inv_t * kLog2e;
-  for (int i = threadIdx.x; i < (a.V + 31) / 32; i += kDsThreads) listed[i] = 0;
-  const Entry en = load_entry(a, t, sh.ids);
-  const bool live = en.id >= 0;
-  if (live) atomicOr(&listed[en.id >> 5], 1u << (en.id & 31));
-  const float xs = live ? to_f32(row[en.id]) : 0.0f;
-  const Teacher T = teacher_mass<kDsWarps>(a, t, en, sh.red, sh.sred);
+  const E* logits = static_cast<const E*>(a.logits);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(ring + TH * kDsU * kDsD);
+  for (int i = k; i < (a.V + 2 * N + 31) / 32; i += TH) bits[i] = 0u;
+  if (k == 0) dup = 0;
+  auto part = [&](int64_t t) {
+    const Row<E> r(logits + t * a.ld, a.V);
+    const int v0 = (int)((int64_t)r.nvec * rank / nb), v1 = (int)((int64_t)r.nvec * (rank + 1) / nb);
+    return Part{r.vec() + v0, v1 - v0};
+  };
+  using S = Stream<TH, kDsU, kDsD, E, decltype(part)>;
+  S stream(part, ring + k, TH, k, t0, step, a.T);
   __syncthreads();
-
-  float m, l, mt, lt;
-  if (LOSS) {
-    Soft<false> tail;
-    for (int i = threadIdx.x; i < a.V; i += kDsThreads)
-      if (!(listed[i >> 5] >> (i & 31) & 1)) {
-        const float x[1] = {to_f32(row[i])};
-        tail.add(x, c);
+  // the next row's entry of this thread (all of them where TH >= K)
+  int nid = -1;
+  float na = 0.0f;
+  if (k < a.K && t0 < a.T) nid = a.teacher_ids[t0 * a.K + k], na = a.teacher_logits[t0 * a.K + k];
+  for (int64_t t = t0; t < a.T; t += step) {
+    const E* row = logits + t * a.ld;
+    const Row<E> r(row, a.V);
+    const int v0 = (int)((int64_t)r.nvec * rank / nb), v1 = (int)((int64_t)r.nvec * (rank + 1) / nb), count = v1 - v0;
+    auto bit_of = [&](int id) { return id - r.head + N; };
+    // ---- the list: range, repeats (the first stays), bits ----
+    float xs = 0.0f;
+    for (int j = k; j < a.K; j += TH) {
+      int id = j == k ? nid : a.teacher_ids[t * a.K + j];
+      list.a[j] = j == k ? na : a.teacher_logits[t * a.K + j];
+      if (id >= a.V) {
+        set_status(a.status, MOE_STATUS_BAD_TOKEN);
+        id = -1;
       }
-    Soft<false> all;
-    if (live) {
-      const float x[1] = {xs};
-      all.add(x, c);
+      list.id[j] = id;
+      if (id >= 0) {
+        const float x = to_f32(row[id]);
+        if (j == k) xs = x;
+        else list.x[j] = x;
+        const int b = bit_of(id);
+        if (atomicOr(&bits[b >> 5], 1u << (b & 31)) >> (b & 31) & 1u) dup = 1;
+      }
     }
-    tail.template block_merge<kDsWarps>(c, sh.sred);
-    all.template block_merge<kDsWarps>(c, sh.sred);
-    all.merge(tail, c);
-    m = all.m, mt = tail.m;
-    l = logf(all.s), lt = logf(tail.s);
-    if (all.s == 0.0f) m = neg_inf(), l = 0.0f;
-    if (tail.s == 0.0f) mt = neg_inf(), lt = 0.0f;
-    if (!(all.m <= 3.402823466e+38f)) {
-      m = l = mt = lt = quiet_nan();
-      if (threadIdx.x == 0) set_status(a.status, MOE_STATUS_NONFINITE_LOGITS);
+    __syncthreads();
+    if (dup) {  // rare: every repeat loses its entry
+      bool again[MOE_DISTILL_MAX_K / 32];
+#pragma unroll
+      for (int e = 0; e < MOE_DISTILL_MAX_K / 32; ++e) {
+        const int j = k + e * TH;
+        again[e] = false;
+        if (j < a.K && list.id[j] >= 0)
+          for (int i = 0; i < j; ++i) again[e] |= list.id[i] == list.id[j];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < MOE_DISTILL_MAX_K / 32; ++e) {
+        if (again[e]) {
+          set_status(a.status, MOE_STATUS_BAD_TOKEN);
+          list.id[k + e * TH] = -1;
+        }
+      }
+      if (k == 0) dup = 0;
     }
-  } else {
-    const float4 st = *reinterpret_cast<const float4*>(a.stats + 4 * t);
-    m = st.x, l = st.y, mt = st.z, lt = st.w;
+    // ---- the sums off the list ----
+    Run<false> acc;
+    auto take = [&](uint4 (&v)[kDsU], int g) {
+      const int i = v0 + g * kDsU * TH + k;
+      uint32_t b[kDsU], any = 0;
+#pragma unroll
+      for (int u = 0; u < kDsU; ++u) {
+        b[u] = i + u * TH < v1 ? listed_bits(bits, i + u * TH, E()) : 0u;
+        any |= b[u];
+      }
+      if (any) {
+#pragma unroll
+        for (int u = 0; u < kDsU; ++u) drop_listed(v[u], b[u], E());
+      }
+      acc.add(v, c, E());
+    };
+    const int groups = S::groups(count);
+    const bool keep = GRAD && groups < kDsD;
+    if (keep) {
+      for (int g = 0; g < groups; ++g) {
+        stream.wait();
+        uint4 v[kDsU];
+        stream.read(g, count, v);
+        take(v, g);
+        stream.hold();
+      }
+    } else {
+      stream.row(count, [&](uint4 (&v)[kDsU], int g) { take(v, g); });
+    }
+    auto listed = [&](int i) { return (bits[bit_of(i) >> 5] >> (bit_of(i) & 31) & 1u) != 0u; };
+    const int edge = k < r.head ? k : r.tail_start() + k - r.head;  // this thread's element outside the vectors
+    const bool has_edge = rank == 0 && k < r.head + r.tail;
+    if (has_edge && !listed(edge)) {
+      const float x[1] = {to_f32(row[edge])};
+      acc.add(x, c);
+    }
+    if (k < a.K) list.x[k] = xs;
+    acc.template warp_merge<32>();
+    if (lane == 0) red[k >> 5] = acc;
+    __syncthreads();
+    acc = Run<false>();
+    if (lane < NW) acc = red[lane];
+    acc.template warp_merge<32>();
+    acc.s = __shfl_sync(0xFFFFFFFFu, acc.s, 0);
+    if (nb > 1) {
+      if (k == 0) cpart = acc;
+      cluster_arrive();
+      cluster_wait();
+      acc = Run<false>();
+      if (lane < nb) {
+        acc.m = cluster_load_f32(&cpart.m, lane);
+        acc.M = cluster_load_f32(&cpart.M, lane);
+        acc.s = cluster_load_f32(&cpart.s, lane);
+      }
+      acc.template warp_merge<32>();
+      acc.s = __shfl_sync(0xFFFFFFFFu, acc.s, 0);
+      cluster_arrive();  // this block has read the others' parts; waited for before cpart is written again
+    }
+    // ---- masks at extreme values, or nothing off the list: differences first ----
+    float mt = acc.m, lt = kLn2 * (log2f(acc.s) - fmaf(acc.m, c, -acc.M));
+    bool empty = false;
+    const bool tail_bad = !(acc.m <= 3.402823466e+38f), slow = !tail_bad && !acc.shift_ok(c);
+    if (slow) {
+      Soft<false> all;
+      for (int i = k; i < a.V; i += TH)
+        if (!listed(i)) {
+          const float x[1] = {to_f32(row[i])};
+          all.add(x, c);
+        }
+      all.warp_merge(c);
+      if (lane == 0) sred[k >> 5] = all;
+      __syncthreads();
+      all = Soft<false>();
+      if (lane < NW) all = sred[lane];
+      all.warp_merge(c);
+      mt = all.m;
+      lt = logf(all.s);
+      empty = all.s == 0.0f;
+      if (empty) mt = neg_inf(), lt = 0.0f;
+      if (nb > 1) {  // no block writes (dlogits may be the logits) before all have read the row
+        cluster_wait();
+        cluster_arrive();
+        cluster_wait();
+        cluster_arrive();
+      }
+      __syncthreads();
+    }
+    // ---- one warp: the list, the loss, the gradient on the list ----
+    if (k < 32) {
+      const Teacher T = teacher_side(list, a.K, a.inv_t, a.teacher_lse, t, rank == 0 ? a.status : nullptr);
+      float m = empty ? kLowest : mt;
+      bool any = !empty;
+      for (int j = lane; j < a.K; j += 32)
+        if (list.id[j] >= 0) {
+          m = max_nan(m, list.x[j]);
+          any |= list.x[j] != neg_inf();
+        }
+      m = warp_max_nan(m);
+      any = __any_sync(0xFFFFFFFFu, any);
+      float s = 0.0f;
+      for (int j = lane; j < a.K; j += 32)
+        if (list.id[j] >= 0) s += exp2_fast((list.x[j] - m) * c);
+      s = warp_sum(s);
+      if (!empty) s += slow ? exp2_fast((mt - m) * c) * expf(lt) : acc.s * exp2_fast(-fmaf(m, c, -acc.M));
+      const bool bad = !(m <= 3.402823466e+38f), none = !any;
+      float l = logf(s);
+      if (none) m = neg_inf(), l = 0.0f;
+      if (bad) m = l = mt = lt = quiet_nan();
+      const float ls = empty ? neg_inf() : (mt - m) * a.inv_t + lt - l;  // ln of the mass off the list
+      float part = 0.0f;
+      const float g = GRAD ? a.g[t] * a.inv_t : 0.0f;
+      for (int j = lane; j < a.K; j += 32) {
+        const float q = teacher_q(T, list, j, a.inv_t), lp = (list.x[j] - m) * a.inv_t - l;
+        if (list.id[j] >= 0 && !(q == 0.0f)) part += none ? -neg_inf() : q * (T.lq(list.a[j], a.inv_t) - lp);
+        if (GRAD) list.a[j] = none ? 0.0f : g * (expf(lp) * T.Q - q);  // the gradient at this id
+      }
+      part = warp_sum(part);
+      if (!(T.r == 0.0f)) part += none ? -neg_inf() : T.r * (logf(T.r) - ls);
+      if (bad || T.Q != T.Q) part = quiet_nan();
+      if (lane == 0) {
+        if (rank == 0) {
+          if (bad) set_status(a.status, MOE_STATUS_NONFINITE_LOGITS);
+          a.loss[t] = part;
+          if (a.stats_out) *reinterpret_cast<float4*>(a.stats_out + 4 * t) = make_float4(m, l, mt, lt);
+        }
+        if (GRAD) {
+          const float off = empty ? 0.0f : g * (expf(ls) * T.Q - T.r);
+          coef[0] = slow ? off * expf(-lt) : off / acc.s;
+          coef[1] = slow ? mt : acc.M;
+          if (bad) coef[0] = quiet_nan();
+        }
+      }
+    }
+    // the bits of this row go; the next row's entry comes
+    const int64_t tn = t + step;
+    if (k < a.K && tn < a.T) nid = a.teacher_ids[tn * a.K + k], na = a.teacher_logits[tn * a.K + k];
+    __syncthreads();
+    for (int j = k; j < a.K; j += TH)
+      if (list.id[j] >= 0) bits[bit_of(list.id[j]) >> 5] = 0u;
+    if (GRAD) {
+      const float w = coef[0], shift = coef[1];
+      E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
+      const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+      auto grad = [&](float x) {
+        if (!slow) return w * exp2_fast(fmaf(x, c, -shift));
+        return w == 0.0f ? 0.0f : w * exp2_fast((x - shift) * c);
+      };
+      auto put = [&](const uint4& v, int i) {  // vector i of the row
+        float x[N];
+        unpack(v, x);
+        if (slow) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) x[e] = grad(x[e]);
+        } else {
+          const uint64_t c2 = f32x2_pack(c, c), s2 = f32x2_pack(-shift, -shift), w2 = f32x2_pack(w, w);
+#pragma unroll
+          for (int e = 0; e < N; e += 2) {
+            float lo, hi;
+            unpack2(fma_f32x2(f32x2_pack(x[e], x[e + 1]), c2, s2), lo, hi);
+            unpack2(mul_f32x2(f32x2_pack(exp2_fast(lo), exp2_fast(hi)), w2), x[e], x[e + 1]);
+          }
+        }
+        if (same) {
+          __stcs(reinterpret_cast<uint4*>(out + r.head) + i, pack(x));
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e) from_f32(x[e], out[r.head + (int64_t)i * N + e]);
+        }
+      };
+      if (keep) {
+        for (int g = 0; g < groups; ++g) {
+          uint4 v[kDsU];
+          stream.read(g, count, v);
+#pragma unroll
+          for (int u = 0; u < kDsU; ++u) {
+            const int i = g * kDsU * TH + u * TH + k;
+            if (i < count) put(v[u], v0 + i);
+          }
+          stream.fetch();
+        }
+        stream.advance(groups);
+      } else {
+        for (int i = v0 + k; i < v1; i += TH) put(__ldcs(r.vec() + i), i);
+      }
+      if (has_edge) from_f32(grad(to_f32(row[edge])), out[edge]);
+      __syncthreads();
+      // ids of this block's part, over what the stream wrote there
+      const int lo = rank == 0 ? 0 : r.head + v0 * N, hi = rank == nb - 1 ? r.tail_start() : r.head + v1 * N;
+      for (int j = k; j < a.K; j += TH) {
+        const int id = list.id[j];
+        if (id >= 0 && ((id >= lo && id < hi) || (rank == 0 && id >= r.tail_start()))) from_f32(list.a[j], out[id]);
+      }
+    }
+    if (nb > 1) cluster_wait();
+    __syncthreads();
   }
-  const bool none = m == neg_inf();
-  const float lp = (xs - m) * a.inv_t - l;                                             // ln p of this entry
-  const float ls = mt == neg_inf() ? neg_inf() : (mt - m) * a.inv_t + lt - l;  // ln of the mass off the list
-  if (LOSS) {
-    float part = 0.0f;
-    if (live && !(T.q == 0.0f)) part = none ? -neg_inf() : T.q * (T.lq - lp);
-    float loss = block_sum<kDsWarps>(part, sh.red);
-    if (!(T.r == 0.0f)) loss += none ? -neg_inf() : T.r * (logf(T.r) - ls);
-    if (threadIdx.x == 0) {
-      a.loss[t] = m == m ? loss : quiet_nan();
-      if (a.stats_out) *reinterpret_cast<float4*>(a.stats_out + 4 * t) = make_float4(m, l, mt, lt);
+}
+
+// The gradient from stored statistics; blockIdx.x a part of the row.  Warp 0
+// works out the teacher's side while the others' loads are on their way; the
+// block overwrites its listed ids at the end.
+constexpr int kDbThreads = 256, kDbBatch = 4;
+
+template <typename E>
+__global__ void __launch_bounds__(kDbThreads) distill_backward_kernel(DistillArgs a) {
+  constexpr int N = Row<E>::kVec;
+  __shared__ DsList list;
+  __shared__ float coef[2];
+  const int64_t t = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+  if (t >= a.T) return;
+  const int k = threadIdx.x, nb = gridDim.x, b = blockIdx.x;
+  const E* row = static_cast<const E*>(a.logits) + t * a.ld;
+  E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
+  const Row<E> r(row, a.V);
+  const float c = a.inv_t * kLog2e;
+  const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+  const int v0 = (int)((int64_t)r.nvec * b / nb), v1 = (int)((int64_t)r.nvec * (b + 1) / nb);
+  const int lo = b == 0 ? 0 : r.head + v0 * N, hi = r.head + v1 * N;  // ids of this block (and the tail's, block 0)
+  auto own = [&](int id) { return (id >= lo && id < hi) || (b == 0 && id >= r.tail_start()); };
+  if (k < a.K) {  // K <= kDbThreads
+    int id = a.teacher_ids[t * a.K + k];
+    if (id >= a.V) {
+      if (b == 0) set_status(a.status, MOE_STATUS_BAD_TOKEN);
+      id = -1;
     }
+    list.id[k] = id;
+    list.a[k] = a.teacher_logits[t * a.K + k];
+    list.x[k] = id >= 0 && own(id) ? to_f32(row[id]) : 0.0f;
   }
-  if (GRAD) {
-    E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
+  int i = v0 + k;
+  uint4 v[kDbBatch];
+#pragma unroll
+  for (int u = 0; u < kDbBatch; ++u)
+    if (i + u * kDbThreads < v1) v[u] = __ldcs(r.vec() + i + u * kDbThreads);
+  __syncthreads();
+  bool again = false;  // a repeat: the first of its id stays
+  if (k < a.K && list.id[k] >= 0) {
+    const int id = list.id[k];
+    for (int j = 0; j < k; ++j) again |= list.id[j] == id;
+  }
+  __syncthreads();
+  if (again) {
+    if (b == 0) set_status(a.status, MOE_STATUS_BAD_TOKEN);
+    list.id[k] = -1;
+  }
+  __syncthreads();
+  const float4 st = *reinterpret_cast<const float4*>(a.stats + 4 * t);
+  const float m = st.x, l = st.y, mt = st.z, lt = st.w;
+  const bool none = m == neg_inf(), empty = mt == neg_inf();
+  if (k < 32) {
+    const Teacher T = teacher_side(list, a.K, a.inv_t, a.teacher_lse, t, b == 0 ? a.status : nullptr);
     const float g = a.g[t] * a.inv_t;
-    const float off = mt == neg_inf() ? 0.0f : g * (expf(ls) * T.Q - T.r);
-    for (int i = threadIdx.x; i < a.V; i += kDsThreads) {
-      const float x = to_f32(row[i]);
-      if (listed[i >> 5] >> (i & 31) & 1) continue;
-      from_f32(none || mt == neg_inf() ? 0.0f : off * expf((x - mt) * a.inv_t - lt), out[i]);
+    for (int j = k; j < a.K; j += 32) {
+      const float lp = (list.x[j] - m) * a.inv_t - l;
+      list.a[j] = none ? 0.0f : g * (expf(lp) * T.Q - teacher_q(T, list, j, a.inv_t));
     }
-    if (live) from_f32(none ? 0.0f : g * (expf(lp) * T.Q - T.q), out[en.id]);
+    if (k == 0) {
+      const float ls = (mt - m) * a.inv_t + lt - l;
+      coef[0] = empty || none ? 0.0f : g * (expf(ls) * T.Q - T.r) * expf(-lt);
+    }
   }
+  __syncthreads();
+  const float w = coef[0];
+  auto grad = [&](float x) { return w * exp2_fast((x - mt) * c); };
+  auto put = [&](const uint4& q, int at) {
+    float x[N];
+    unpack(q, x);
+    if (empty || none) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[e] = 0.0f;
+    } else {
+      const uint64_t m2 = f32x2_pack(-mt, -mt), c2 = f32x2_pack(c, c), w2 = f32x2_pack(w, w);
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        float p, q2;
+        unpack2(mul_f32x2(add_f32x2(f32x2_pack(x[e], x[e + 1]), m2), c2), p, q2);
+        unpack2(mul_f32x2(f32x2_pack(exp2_fast(p), exp2_fast(q2)), w2), x[e], x[e + 1]);
+      }
+    }
+    if (same) {
+      __stcs(reinterpret_cast<uint4*>(out + r.head) + at, pack(x));
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) from_f32(x[e], out[r.head + (int64_t)at * N + e]);
+    }
+  };
+  while (i < v1) {
+    const int next = i + kDbBatch * kDbThreads;
+    uint4 nv[kDbBatch];
+#pragma unroll
+    for (int u = 0; u < kDbBatch; ++u)
+      if (next + u * kDbThreads < v1) nv[u] = __ldcs(r.vec() + next + u * kDbThreads);
+#pragma unroll
+    for (int u = 0; u < kDbBatch; ++u)
+      if (i + u * kDbThreads < v1) put(v[u], i + u * kDbThreads);
+#pragma unroll
+    for (int u = 0; u < kDbBatch; ++u) v[u] = nv[u];
+    i = next;
+  }
+  if (b == 0 && k < r.head + r.tail) {
+    const int e = k < r.head ? k : r.tail_start() + k - r.head;
+    from_f32(empty || none ? 0.0f : grad(to_f32(row[e])), out[e]);
+  }
+  __syncthreads();
+  if (k < a.K && list.id[k] >= 0 && own(list.id[k])) from_f32(list.a[k], out[list.id[k]]);
 }
 
 // host launchers
+template <typename E, bool GRAD>
+static void (*distill_of(int th))(DistillArgs) {
+  return th == 32     ? distill_kernel<E, GRAD, 32>
+         : th == 128  ? distill_kernel<E, GRAD, 128>
+         : th == 256  ? distill_kernel<E, GRAD, 256>
+         : th == 512  ? distill_kernel<E, GRAD, 512>
+                      : distill_kernel<E, GRAD, 1024>;
+}
 template <typename E>
 static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
-  const int smem = (a.V + 31) / 32 * 4;
-  void (*f)(DistillArgs) = a.loss ? (a.dlogits ? distill_kernel<E, true, true> : distill_kernel<E, true, false>)
-                                  : distill_kernel<E, false, true>;
-  if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
-  f<<<dim3((unsigned)a.T), kDsThreads, smem, s>>>(a);
-  return 0;
+  const int64_t nvec = (int64_t)a.V / Row<E>::kVec;
+  const unsigned gy = a.T < 65535 ? a.T : 65535;
+  if (!a.loss) {
+    const int64_t per = kDbThreads * kDbBatch * 2;
+    const dim3 grid((unsigned)(nvec < per ? 1 : (nvec + per - 1) / per), gy, (a.T + gy - 1) / gy);
+    distill_backward_kernel<E><<<grid, kDbThreads, 0, s>>>(a);
+    return 0;
+  }
+  const bool grad = a.dlogits != nullptr;
+  const int sms = gemm_num_ctas(), bits = (a.V + 2 * Row<E>::kVec + 31) / 32 * 4;
+  const int64_t stay = (kDsD - 1) * kDsU;  // vectors per thread that a part may keep
+  const int slots = kDsU * kDsD * 16;      // ring bytes per thread
+  const int most = bits <= 28 * 1024 ? 1024 : bits <= 100 * 1024 ? 512 : 256;  // threads whose ring fits beside the bits
+  // Few rows: blocks of a cluster per row until there is one for each SM.
+  int nb = 1, th = 32;
+  while (nb < 8 && (int64_t)a.T * nb < sms && nvec / (nb * 2) >= 512) nb *= 2;
+  if (grad) {  // the fewest threads that keep their parts
+    while (nb < 8 && (nvec + nb - 1) / nb > stay * most) nb *= 2;
+    while (th < most && (nvec + nb - 1) / nb > stay * th) th = th == 32 ? 128 : th * 2;
+  } else if (nvec / nb > 1024) {
+    th = 128;
+  }
+  if ((int64_t)a.T * nb <= 2 * sms)
+    while (th < 512 && th < most && nvec / nb > 2 * th) th = th == 32 ? 128 : th * 2;
+  const int smem = th * slots + bits;
+  int fit = 227 * 1024 / (smem + 5 * 1024);
+  if (fit > kDsMaxThreads / th) fit = kDsMaxThreads / th;
+  if (fit < 1) fit = 1;
+  const int64_t grid = (int64_t)sms * fit / nb * DSTURNS;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(nb, (unsigned)(a.T < grid ? a.T : grid));
+  cfg.blockDim = dim3(th);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = nb;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = nb > 1 ? 1 : 0;
+  auto f = grad ? distill_of<E, true>(th) : distill_of<E, false>(th);
+  if (!allow_smem((const void*)f, smem)) return -1;
+  return cudaLaunchKernelEx(&cfg, f, a) == cudaSuccess ? 0 : -1;
 }
 int launch_distill(const DistillArgs& a, cudaStream_t s) {
   return a.dtype == MOE_DTYPE_BF16 ? launch_distill_of<uint16_t>(a, s) : launch_distill_of<float>(a, s);

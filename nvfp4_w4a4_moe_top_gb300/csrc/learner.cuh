@@ -448,22 +448,45 @@ struct Stream {
     }
     cp_async_commit();
   }
-  // The vectors of the next row part (of `count`) in groups: f(v, g), g = 0, 1,
-  // ..  Places past the end hold -inf; an empty part is one group of such.
+  // Groups of a part of `count` vectors; an empty part has one, of -inf.
+  static __device__ __forceinline__ int groups(int count) { return count > U * TH ? (count + U * TH - 1) / (U * TH) : 1; }
+  // Waits for the current part's next group.  Each group looked at is followed
+  // by one commit, a fetch() into its slots or hold() where they are kept: the
+  // D - 1 latest commits then never include the group waited for.
+  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory"); }
+  __device__ __forceinline__ void hold() { cp_async_commit(); }
+  // Group g of the current part (of `count` vectors), from its slots.  Places
+  // past the end hold -inf.
+  __device__ __forceinline__ void read(int g, int count, uint4 (&v)[U]) const {
+    const int s = use + g;
+    const uint4* slot = ring + (s >= D ? s - D : s) * U * stride;
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = slot[u * stride];
+    const int j = g * U * TH + k;
+    if ((g + 1) * U * TH > count) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j + u * TH >= count) v[u] = none(E());
+    }
+  }
+  // The part is done with: n of its groups' slots were freed by fetches.
+  __device__ __forceinline__ void advance(int n) { use = (use + n) % D; }
+  // All groups of the next part in turn: f(v, g), each slot refilled after it.
   template <typename F>
   __device__ __forceinline__ void row(int count, F f) {
-    int g = 0;
-    for (int j = 0; j == 0 || j < count; j += U * TH, ++g) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+    const int n = groups(count);
+    for (int g = 0; g < n; ++g) {
+      wait();
+      uint4 v[U];
       const uint4* slot = ring + use * U * stride;
       use = use + 1 == D ? 0 : use + 1;
-      uint4 v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) v[u] = slot[u * stride];
-      if (j + U * TH > count) {
+      const int j = g * U * TH + k;
+      if ((g + 1) * U * TH > count) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (j + u * TH + k >= count) v[u] = none(E());
+          if (j + u * TH >= count) v[u] = none(E());
       }
       f(v, g);
       fetch();  // into the slots just read

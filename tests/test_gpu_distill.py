@@ -128,7 +128,7 @@ def check(z, dtype, ids, a, lse, inv_t, g, pad=0, lead=0, dpad=None, dlead=0):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,V,K", [(1, 1, 1), (6, 2, 2), (7, 9, 4), (8, 33, 40), (6, 1000, 16), (9, 4097, 64), (7, 30011, 256),
-                                   (2, 131072, 64), (64, 2048, 8), (1, 262145, 33), (200, 8190, 3)])
+                                   (2, 131072, 64), (64, 2048, 8), (1, 262145, 33), (200, 8190, 3), (330, 66000, 16)])
 def test_loss_and_gradient(T, V, K, dtype):
     rng = np.random.default_rng(T * 31 + V + K)
     for inv_t, tail, pad, lead, dpad, dlead in [(1.0, True, 0, 0, None, 0), (0.5, False, 3, 1, 3, 1),
