@@ -77,20 +77,13 @@ __device__ __forceinline__ float teacher_q(const Teacher& T, const DsList& li, i
   return li.id[j] < 0 || T.Q == 0.0f ? 0.0f : expf(T.lq(li.a[j], inv_t));
 }
 
-// The 16-byte vector with its listed elements replaced by -inf; bit e of
+// The listed elements of a vector in shared memory become -inf; bit e of
 // `bits`: element e.
-__device__ __forceinline__ void drop_listed(uint4& v, uint32_t bits, uint16_t) {
-  auto word = [&](uint32_t x, uint32_t b) {
-    const uint32_t m = (b & 1u) * 0xFFFFu | (b >> 1 & 1u) * 0xFFFF0000u;
-    return (x & ~m) | (m & 0xFF80FF80u);
-  };
-  v = make_uint4(word(v.x, bits), word(v.y, bits >> 2), word(v.z, bits >> 4), word(v.w, bits >> 6));
+__device__ __forceinline__ void drop_listed(uint4* v, uint32_t bits, uint16_t) {
+  for (; bits; bits &= bits - 1) reinterpret_cast<uint16_t*>(v)[__ffs(bits) - 1] = 0xFF80u;
 }
-__device__ __forceinline__ void drop_listed(uint4& v, uint32_t bits, float) {
-  if (bits & 1u) v.x = 0xFF800000u;
-  if (bits & 2u) v.y = 0xFF800000u;
-  if (bits & 4u) v.z = 0xFF800000u;
-  if (bits & 8u) v.w = 0xFF800000u;
+__device__ __forceinline__ void drop_listed(uint4* v, uint32_t bits, float) {
+  for (; bits; bits &= bits - 1) reinterpret_cast<uint32_t*>(v)[__ffs(bits) - 1] = 0xFF800000u;
 }
 // Bits of the listed elements of vector i of the row (kVec bits each, vector 0
 // after a place for the elements before it).
@@ -115,9 +108,10 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
   __shared__ Run<false> red[NW];
   __shared__ Run<false> cpart;
   __shared__ Soft<false> sred[NW];
-  __shared__ float coef[4];  // weight of the part off the list, its shift (or maximum), whether slow
+  __shared__ float coef[2];
+  __shared__ bool slow;
   __shared__ int dup;
-  const int nb = gridDim.x, rank = blockIdx.x, k = threadIdx.x, lane = k & 31;
+  const int nb = gridDim.x, lg = 31 - __clz(nb), rank = blockIdx.x, k = threadIdx.x, lane = k & 31;  // nb: a power of two
   const int64_t t0 = blockIdx.y, step = gridDim.y;
   const float c = a.inv_t * kLog2e;
   const E* logits = static_cast<const E*>(a.logits);
@@ -126,7 +120,7 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
   if (k == 0) dup = 0;
   auto part = [&](int64_t t) {
     const Row<E> r(logits + t * a.ld, a.V);
-    const int v0 = (int)((int64_t)r.nvec * rank / nb), v1 = (int)((int64_t)r.nvec * (rank + 1) / nb);
+    const int v0 = r.part(rank, lg), v1 = r.part(rank + 1, lg);
     return Part{r.vec() + v0, v1 - v0};
   };
   using S = Stream<TH, kDsU, kDsD, E, decltype(part)>;
@@ -139,7 +133,7 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
   for (int64_t t = t0; t < a.T; t += step) {
     const E* row = logits + t * a.ld;
     const Row<E> r(row, a.V);
-    const int v0 = (int)((int64_t)r.nvec * rank / nb), v1 = (int)((int64_t)r.nvec * (rank + 1) / nb), count = v1 - v0;
+    const int v0 = r.part(rank, lg), v1 = r.part(rank + 1, lg), count = v1 - v0;
     auto bit_of = [&](int id) { return id - r.head + N; };
     // ---- the list: range, repeats (the first stays), bits ----
     float xs = 0.0f;
@@ -181,32 +175,33 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
     }
     // ---- the sums off the list ----
     Run<false> acc;
-    auto take = [&](uint4 (&v)[kDsU], int g) {
-      const int i = v0 + g * kDsU * TH + k;
+    // the listed elements of a group (in the thread's own slots) leave it
+    auto drop = [&](uint4* slot, int g) {
+      const int i = g * kDsU * TH + k;
       uint32_t b[kDsU], any = 0;
 #pragma unroll
       for (int u = 0; u < kDsU; ++u) {
-        b[u] = i + u * TH < v1 ? listed_bits(bits, i + u * TH, E()) : 0u;
+        b[u] = i + u * TH < count ? listed_bits(bits, v0 + i + u * TH, E()) : 0u;
         any |= b[u];
       }
       if (any) {
 #pragma unroll
-        for (int u = 0; u < kDsU; ++u) drop_listed(v[u], b[u], E());
+        for (int u = 0; u < kDsU; ++u) drop_listed(slot + u * TH, b[u], E());
       }
-      acc.add(v, c, E());
     };
     const int groups = S::groups(count);
     const bool keep = GRAD && groups < kDsD;
     if (keep) {
       for (int g = 0; g < groups; ++g) {
         stream.wait();
+        drop(stream.slot(g), g);
         uint4 v[kDsU];
         stream.read(g, count, v);
-        take(v, g);
+        acc.add(v, c, E());
         stream.hold();
       }
     } else {
-      stream.row(count, [&](uint4 (&v)[kDsU], int g) { take(v, g); });
+      stream.row(count, drop, [&](const uint4 (&v)[kDsU], int) { acc.add(v, c, E()); });
     }
     auto listed = [&](int i) { return (bits[bit_of(i) >> 5] >> (bit_of(i) & 31) & 1u) != 0u; };
     const int edge = k < r.head ? k : r.tail_start() + k - r.head;  // this thread's element outside the vectors
@@ -219,55 +214,10 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
     acc.template warp_merge<32>();
     if (lane == 0) red[k >> 5] = acc;
     __syncthreads();
-    acc = Run<false>();
-    if (lane < NW) acc = red[lane];
-    acc.template warp_merge<32>();
-    acc.s = __shfl_sync(0xFFFFFFFFu, acc.s, 0);
-    if (nb > 1) {
-      if (k == 0) cpart = acc;
-      cluster_arrive();
-      cluster_wait();
-      acc = Run<false>();
-      if (lane < nb) {
-        acc.m = cluster_load_f32(&cpart.m, lane);
-        acc.M = cluster_load_f32(&cpart.M, lane);
-        acc.s = cluster_load_f32(&cpart.s, lane);
-      }
-      acc.template warp_merge<32>();
-      acc.s = __shfl_sync(0xFFFFFFFFu, acc.s, 0);
-      cluster_arrive();  // this block has read the others' parts; waited for before cpart is written again
-    }
-    // ---- masks at extreme values, or nothing off the list: differences first ----
-    float mt = acc.m, lt = kLn2 * (log2f(acc.s) - fmaf(acc.m, c, -acc.M));
-    bool empty = false;
-    const bool tail_bad = !(acc.m <= 3.402823466e+38f), slow = !tail_bad && !acc.shift_ok(c);
-    if (slow) {
-      Soft<false> all;
-      for (int i = k; i < a.V; i += TH)
-        if (!listed(i)) {
-          const float x[1] = {to_f32(row[i])};
-          all.add(x, c);
-        }
-      all.warp_merge(c);
-      if (lane == 0) sred[k >> 5] = all;
-      __syncthreads();
-      all = Soft<false>();
-      if (lane < NW) all = sred[lane];
-      all.warp_merge(c);
-      mt = all.m;
-      lt = logf(all.s);
-      empty = all.s == 0.0f;
-      if (empty) mt = neg_inf(), lt = 0.0f;
-      if (nb > 1) {  // no block writes (dlogits may be the logits) before all have read the row
-        cluster_wait();
-        cluster_arrive();
-        cluster_wait();
-        cluster_arrive();
-      }
-      __syncthreads();
-    }
-    // ---- one warp: the list, the loss, the gradient on the list ----
-    if (k < 32) {
+    // ---- one warp: the parts, the list, the loss, the gradient on the list ----
+    // mt, lt: maximum and ln-sum off the list; the gradient there is coef[0]
+    // times 2^(x c - shift), or 2^((x - shift) c) after the slow path
+    auto finish = [&](float mt, float lt, bool empty, float rescale, float shift) {
       const Teacher T = teacher_side(list, a.K, a.inv_t, a.teacher_lse, t, rank == 0 ? a.status : nullptr);
       float m = empty ? kLowest : mt;
       bool any = !empty;
@@ -282,7 +232,7 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
       for (int j = lane; j < a.K; j += 32)
         if (list.id[j] >= 0) s += exp2_fast((list.x[j] - m) * c);
       s = warp_sum(s);
-      if (!empty) s += slow ? exp2_fast((mt - m) * c) * expf(lt) : acc.s * exp2_fast(-fmaf(m, c, -acc.M));
+      if (!empty) s += exp2_fast((mt - m) * c) * expf(lt);
       const bool bad = !(m <= 3.402823466e+38f), none = !any;
       float l = logf(s);
       if (none) m = neg_inf(), l = 0.0f;
@@ -304,32 +254,82 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
           a.loss[t] = part;
           if (a.stats_out) *reinterpret_cast<float4*>(a.stats_out + 4 * t) = make_float4(m, l, mt, lt);
         }
-        if (GRAD) {
-          const float off = empty ? 0.0f : g * (expf(ls) * T.Q - T.r);
-          coef[0] = slow ? off * expf(-lt) : off / acc.s;
-          coef[1] = slow ? mt : acc.M;
-          if (bad) coef[0] = quiet_nan();
-        }
+        coef[0] = empty ? 0.0f : bad ? quiet_nan() : g * (expf(ls) * T.Q - T.r) * rescale;
+        coef[1] = shift;
       }
+    };
+    if (k < 32) {
+      acc = Run<false>();
+      if (lane < NW) acc = red[lane];
+      acc.template warp_merge<32>();
+      if (lane == 0) cpart = acc;
+    }
+    if (nb > 1) {
+      cluster_arrive();
+      cluster_wait();
+      if (k < 32) {
+        acc = Run<false>();
+        if (lane < nb) {
+          acc.m = cluster_load_f32(&cpart.m, lane);
+          acc.M = cluster_load_f32(&cpart.M, lane);
+          acc.s = cluster_load_f32(&cpart.s, lane);
+        }
+        acc.template warp_merge<32>();
+      }
+      cluster_arrive();  // this block has read the others' parts; waited for before cpart is written again
+    }
+    if (k < 32) {
+      acc.s = __shfl_sync(0xFFFFFFFFu, acc.s, 0);
+      const bool differ = acc.m <= 3.402823466e+38f && !acc.shift_ok(c);
+      if (lane == 0) slow = differ;
+      if (!differ)
+        finish(acc.m, kLn2 * (log2f(acc.s) - fmaf(acc.m, c, -acc.M)), false, 1.0f / acc.s, acc.M);
+    }
+    __syncthreads();
+    if (slow) {  // masks at extreme values, or nothing off the list: differences first
+      Soft<false> all;
+      for (int i = k; i < a.V; i += TH)
+        if (!listed(i)) {
+          const float x[1] = {to_f32(row[i])};
+          all.add(x, c);
+        }
+      all.warp_merge(c);
+      if (lane == 0) sred[k >> 5] = all;
+      if (nb > 1) {  // no block writes (dlogits may be the logits) before all have read the row
+        cluster_wait();
+        cluster_arrive();
+        cluster_wait();
+        cluster_arrive();
+      }
+      __syncthreads();
+      if (k < 32) {
+        all = Soft<false>();
+        if (lane < NW) all = sred[lane];
+        all.warp_merge(c);
+        const bool empty = all.s == 0.0f;
+        const float lt = empty ? 0.0f : logf(all.s);
+        finish(empty ? neg_inf() : all.m, lt, empty, expf(-lt), all.m);
+      }
+      __syncthreads();
     }
     // the bits of this row go; the next row's entry comes
     const int64_t tn = t + step;
     if (k < a.K && tn < a.T) nid = a.teacher_ids[tn * a.K + k], na = a.teacher_logits[tn * a.K + k];
-    __syncthreads();
     for (int j = k; j < a.K; j += TH)
       if (list.id[j] >= 0) bits[bit_of(list.id[j]) >> 5] = 0u;
     if (GRAD) {
       const float w = coef[0], shift = coef[1];
+      const bool diff = slow;
       E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
       const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
       auto grad = [&](float x) {
-        if (!slow) return w * exp2_fast(fmaf(x, c, -shift));
+        if (!diff) return w * exp2_fast(fmaf(x, c, -shift));
         return w == 0.0f ? 0.0f : w * exp2_fast((x - shift) * c);
       };
       auto put = [&](const uint4& v, int i) {  // vector i of the row
         float x[N];
         unpack(v, x);
-        if (slow) {
+        if (diff) {
 #pragma unroll
           for (int e = 0; e < N; ++e) x[e] = grad(x[e]);
         } else {
@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
 // works out the teacher's side while the others' loads are on their way; the
 // block overwrites its listed ids at the end.
 constexpr int kDbThreads = 256, kDbBatch = 4;
+constexpr int kDbPart = kDbThreads * kDbBatch * 2;  // vectors of a block
 
 template <typename E>
 __global__ void __launch_bounds__(kDbThreads) distill_backward_kernel(DistillArgs a) {
@@ -389,13 +390,13 @@ __global__ void __launch_bounds__(kDbThreads) distill_backward_kernel(DistillArg
   __shared__ float coef[2];
   const int64_t t = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
   if (t >= a.T) return;
-  const int k = threadIdx.x, nb = gridDim.x, b = blockIdx.x;
+  const int k = threadIdx.x, b = blockIdx.x;
   const E* row = static_cast<const E*>(a.logits) + t * a.ld;
   E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
   const Row<E> r(row, a.V);
   const float c = a.inv_t * kLog2e;
   const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
-  const int v0 = (int)((int64_t)r.nvec * b / nb), v1 = (int)((int64_t)r.nvec * (b + 1) / nb);
+  const int v0 = min(b * kDbPart, r.nvec), v1 = min(v0 + kDbPart, r.nvec);
   const int lo = b == 0 ? 0 : r.head + v0 * N, hi = r.head + v1 * N;  // ids of this block (and the tail's, block 0)
   auto own = [&](int id) { return (id >= lo && id < hi) || (b == 0 && id >= r.tail_start()); };
   if (k < a.K) {  // K <= kDbThreads
@@ -500,8 +501,7 @@ static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
   const int64_t nvec = (int64_t)a.V / Row<E>::kVec;
   const unsigned gy = a.T < 65535 ? a.T : 65535;
   if (!a.loss) {
-    const int64_t per = kDbThreads * kDbBatch * 2;
-    const dim3 grid((unsigned)(nvec < per ? 1 : (nvec + per - 1) / per), gy, (a.T + gy - 1) / gy);
+    const dim3 grid((unsigned)(nvec <= kDbPart ? 1 : (nvec + kDbPart - 1) / kDbPart), gy, (a.T + gy - 1) / gy);
     distill_backward_kernel<E><<<grid, kDbThreads, 0, s>>>(a);
     return 0;
   }

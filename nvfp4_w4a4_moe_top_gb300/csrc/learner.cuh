@@ -165,6 +165,11 @@ struct Row {
     return reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p + head) & ~(uintptr_t)15);
   }
   __device__ __forceinline__ int tail_start() const { return head + nvec * kVec; }
+  // First vector of part `rank` of 2^shift parts; part 2^shift is the end.
+  __device__ __forceinline__ int part(int rank, int shift) const {
+    const int per = (nvec >> shift) + ((nvec & ((1 << shift) - 1)) != 0);
+    return min(rank * per, nvec);
+  }
 };
 
 __device__ __forceinline__ float to_f32(uint16_t b) { return bf16_bits_to_f32(b); }
@@ -180,8 +185,13 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
 __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
   x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
 }
+__device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
 __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  return make_uint4(bf16x2_rn(x[0], x[1]), bf16x2_rn(x[2], x[3]), bf16x2_rn(x[4], x[5]), bf16x2_rn(x[6], x[7]));
 }
 __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
   return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
@@ -455,13 +465,17 @@ struct Stream {
   // D - 1 latest commits then never include the group waited for.
   __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory"); }
   __device__ __forceinline__ void hold() { cp_async_commit(); }
+  // This thread's first slot of group g of the current part.
+  __device__ __forceinline__ uint4* slot(int g) const {
+    const int s = use + g;
+    return ring + (s >= D ? s - D : s) * U * stride;
+  }
   // Group g of the current part (of `count` vectors), from its slots.  Places
   // past the end hold -inf.
   __device__ __forceinline__ void read(int g, int count, uint4 (&v)[U]) const {
-    const int s = use + g;
-    const uint4* slot = ring + (s >= D ? s - D : s) * U * stride;
+    const uint4* p = slot(g);
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = slot[u * stride];
+    for (int u = 0; u < U; ++u) v[u] = p[u * stride];
     const int j = g * U * TH + k;
     if ((g + 1) * U * TH > count) {
 #pragma unroll
@@ -471,17 +485,18 @@ struct Stream {
   }
   // The part is done with: n of its groups' slots were freed by fetches.
   __device__ __forceinline__ void advance(int n) { use = (use + n) % D; }
-  // All groups of the next part in turn: f(v, g), each slot refilled after it.
-  template <typename F>
-  __device__ __forceinline__ void row(int count, F f) {
+  // All groups of the next part in turn, each slot refilled after it:
+  // pre(slot, g) on the slots, then f(v, g).
+  template <typename P2, typename F>
+  __device__ __forceinline__ void row(int count, P2 pre, F f) {
     const int n = groups(count);
     for (int g = 0; g < n; ++g) {
       wait();
+      pre(slot(0), g);
       uint4 v[U];
-      const uint4* slot = ring + use * U * stride;
-      use = use + 1 == D ? 0 : use + 1;
+      const uint4* p = slot(0);
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = slot[u * stride];
+      for (int u = 0; u < U; ++u) v[u] = p[u * stride];
       const int j = g * U * TH + k;
       if ((g + 1) * U * TH > count) {
 #pragma unroll
@@ -489,6 +504,7 @@ struct Stream {
           if (j + u * TH >= count) v[u] = none(E());
       }
       f(v, g);
+      use = use + 1 == D ? 0 : use + 1;
       fetch();  // into the slots just read
     }
   }

@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_ker
   __shared__ uint64_t clist[32];
   __shared__ TopShared<TH> tops[TOP ? NG : 1];
   const int nb = TH < kLpThreads ? 1 : gridDim.x, rank = TH < kLpThreads ? 0 : blockIdx.x;
+  const int lg = TH < kLpThreads ? 0 : 31 - __clz(nb);  // nb is a power of two
   const int group = threadIdx.x / TH, k = threadIdx.x & (TH - 1), lane = threadIdx.x & 31;
   TopShared<TH>& top = tops[TOP ? group : 0];
   const int64_t t0 = (int64_t)blockIdx.y * NG + group, step = (int64_t)gridDim.y * NG;
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_ker
   const E* logits = static_cast<const E*>(a.logits);
   auto part = [&](int64_t t) {
     const Row<E> r(logits + t * a.ld, a.V);
-    const int v0 = (int)((int64_t)r.nvec * rank / nb), v1 = (int)((int64_t)r.nvec * (rank + 1) / nb);
+    const int v0 = r.part(rank, lg), v1 = r.part(rank + 1, lg);
     return Part{r.vec() + v0, v1 - v0};
   };
   if (TOP && k == 0) top.nhot = 0;
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_ker
   for (int64_t t = t0; t < a.T; t += step, odd ^= 1) {
     const E* row = logits + t * a.ld;
     const Row<E> r(row, a.V);
-    const int v0 = (int)((int64_t)r.nvec * rank / nb), v1 = (int)((int64_t)r.nvec * (rank + 1) / nb);
+    const int v0 = r.part(rank, lg), v1 = r.part(rank + 1, lg);
     // the target's logit, needed at the end, and the next row's target
     const int y = ynext;
     const float xy = y >= 0 && y < a.V ? to_f32(row[y]) : 0.0f;
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_ker
     Run<ENT> acc;
     int slot = 0, left = 1 << shift;
     float high = kLowest;
-    stream.row(v1 - v0, [&](const auto& v, int) {
+    stream.row(v1 - v0, [](uint4*, int) {}, [&](const auto& v, int) {
       const float mx = acc.add(v, c, E());
       if (TOP) {
         high = fmaxf(high, mx);
@@ -404,6 +405,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_ker
 // blockIdx.x a part of the row.
 constexpr int kLbThreads = 256;
 constexpr int kLbBatch = 4;
+constexpr int kLbPart = kLbThreads * kLbBatch * 2;  // vectors of a block
 
 template <typename E>
 __global__ void __launch_bounds__(kLbThreads) token_logprobs_backward_kernel(LogprobBwdArgs a) {
@@ -427,8 +429,7 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_backward_kernel(Log
   };
   const Row<E> r(row, a.V);
   if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0) {
-    const int nb = gridDim.x, b = blockIdx.x;
-    const int v0 = (int)((int64_t)r.nvec * b / nb), v1 = (int)((int64_t)r.nvec * (b + 1) / nb);
+    const int b = blockIdx.x, v0 = b * kLbPart, v1 = min(v0 + kLbPart, r.nvec);
     uint4* ov = reinterpret_cast<uint4*>(out + r.head);
     const int yv = has && y >= r.head ? (y - r.head) / N : -1, ye = (y - r.head) % N;
     auto store = [&](const uint4& v, int i) {
@@ -519,8 +520,7 @@ int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
 }
 int launch_token_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t s) {
   const int64_t nvec = (int64_t)a.V * (a.dtype == MOE_DTYPE_BF16 ? 2 : 4) / 16;
-  const int64_t per = kLbThreads * kLbBatch * 2;
-  const unsigned nb = (unsigned)(nvec < per ? 1 : (nvec + per - 1) / per);
+  const unsigned nb = (unsigned)(nvec <= kLbPart ? 1 : (nvec + kLbPart - 1) / kLbPart);
   const unsigned gy = a.T < 65535 ? a.T : 65535, gz = (a.T + gy - 1) / gy;
   const dim3 grid(nb, gy, gz);
   if (a.dtype == MOE_DTYPE_BF16) token_logprobs_backward_kernel<uint16_t><<<grid, kLbThreads, 0, s>>>(a);
