@@ -3,7 +3,13 @@
 
 namespace moe {
 
-constexpr int kDsU = 4, kDsD = 3;  // vectors per group of copies, groups in flight
+#ifndef DSD
+#define DSD 2
+#define DSU 4
+#define DSMOST 512
+#define DSPER 16
+#endif
+constexpr int kDsU = DSU, kDsD = DSD;  // vectors per group of copies, groups in flight
 constexpr int kDsMaxThreads = 1024;
 #ifndef DSTURNS
 #define DSTURNS 4
@@ -34,14 +40,14 @@ struct Teacher {
   float base, shift, r, Q;
   __device__ __forceinline__ float lq(float a, float inv_t) const { return (a - base) * inv_t - shift; }
 };
-__device__ __forceinline__ Teacher teacher_side(const DsList& li, int K, float inv_t, const float* lse, int64_t t,
+__device__ __forceinline__ Teacher teacher_side(const DsList& li, int K, float inv_t, bool has_lse, float lse,
                                                 int* status) {
   const int lane = threadIdx.x & 31;
   Teacher T;
   bool bad = false;
-  if (lse) {
+  if (has_lse) {
     T.base = 0.0f;
-    T.shift = lse[t];
+    T.shift = lse;
     bad = !(fabsf(T.shift) <= 3.402823466e+38f);
     float sum = 0.0f;
     for (int j = lane; j < K; j += 32)
@@ -97,9 +103,9 @@ __device__ __forceinline__ uint32_t listed_bits(const uint32_t* bits, int i, flo
 // The loss, and with GRAD the gradient, of rows in turn, TH threads (one
 // block) per row or, in a cluster of gridDim.x blocks, per part of a row.  A
 // bit per id marks the listed ones, whose elements leave the stream, so that
-// the mass off the list is summed by itself.  With GRAD a part of at most
-// (kDsD - 1) groups stays in the ring's slots between the sums and the
-// gradient: the logits are read from memory once.  Longer parts are read again.
+// the mass off the list is summed by itself.  With GRAD the stream brings each
+// part twice, for the sums and for the gradient; the second time it comes from
+// L2, which holds the rows that the resident blocks work on.
 template <typename E, bool GRAD, int TH>
 __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(DistillArgs a) {
   constexpr int N = Row<E>::kVec, NW = TH / 32;
@@ -123,8 +129,7 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
     const int v0 = r.part(rank, lg), v1 = r.part(rank + 1, lg);
     return Part{r.vec() + v0, v1 - v0};
   };
-  using S = Stream<TH, kDsU, kDsD, E, decltype(part)>;
-  S stream(part, ring + k, TH, k, t0, step, a.T);
+  Stream<TH, kDsU, kDsD, GRAD ? 2 : 1, E, decltype(part)> stream(part, ring + k, TH, k, t0, step, a.T);
   __syncthreads();
   // the next row's entry of this thread (all of them where TH >= K)
   int nid = -1;
@@ -135,6 +140,7 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
     const Row<E> r(row, a.V);
     const int v0 = r.part(rank, lg), v1 = r.part(rank + 1, lg), count = v1 - v0;
     auto bit_of = [&](int id) { return id - r.head + N; };
+    const float g_row = GRAD && k < 32 ? a.g[t] : 0.0f, lse_row = a.teacher_lse && k < 32 ? a.teacher_lse[t] : 0.0f;
     // ---- the list: range, repeats (the first stays), bits ----
     float xs = 0.0f;
     for (int j = k; j < a.K; j += TH) {
@@ -189,20 +195,7 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
         for (int u = 0; u < kDsU; ++u) drop_listed(slot + u * TH, b[u], E());
       }
     };
-    const int groups = S::groups(count);
-    const bool keep = GRAD && groups < kDsD;
-    if (keep) {
-      for (int g = 0; g < groups; ++g) {
-        stream.wait();
-        drop(stream.slot(g), g);
-        uint4 v[kDsU];
-        stream.read(g, count, v);
-        acc.add(v, c, E());
-        stream.hold();
-      }
-    } else {
-      stream.row(count, drop, [&](const uint4 (&v)[kDsU], int) { acc.add(v, c, E()); });
-    }
+    stream.row(count, drop, [&](const uint4 (&v)[kDsU], int) { acc.add(v, c, E()); });
     auto listed = [&](int i) { return (bits[bit_of(i) >> 5] >> (bit_of(i) & 31) & 1u) != 0u; };
     const int edge = k < r.head ? k : r.tail_start() + k - r.head;  // this thread's element outside the vectors
     const bool has_edge = rank == 0 && k < r.head + r.tail;
@@ -218,7 +211,7 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
     // mt, lt: maximum and ln-sum off the list; the gradient there is coef[0]
     // times 2^(x c - shift), or 2^((x - shift) c) after the slow path
     auto finish = [&](float mt, float lt, bool empty, float rescale, float shift) {
-      const Teacher T = teacher_side(list, a.K, a.inv_t, a.teacher_lse, t, rank == 0 ? a.status : nullptr);
+      const Teacher T = teacher_side(list, a.K, a.inv_t, a.teacher_lse != nullptr, lse_row, rank == 0 ? a.status : nullptr);
       float m = empty ? kLowest : mt;
       bool any = !empty;
       for (int j = lane; j < a.K; j += 32)
@@ -239,7 +232,7 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
       if (bad) m = l = mt = lt = quiet_nan();
       const float ls = empty ? neg_inf() : (mt - m) * a.inv_t + lt - l;  // ln of the mass off the list
       float part = 0.0f;
-      const float g = GRAD ? a.g[t] * a.inv_t : 0.0f;
+      const float g = g_row * a.inv_t;
       for (int j = lane; j < a.K; j += 32) {
         const float q = teacher_q(T, list, j, a.inv_t), lp = (list.x[j] - m) * a.inv_t - l;
         if (list.id[j] >= 0 && !(q == 0.0f)) part += none ? -neg_inf() : q * (T.lq(list.a[j], a.inv_t) - lp);
@@ -348,21 +341,13 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
           for (int e = 0; e < N; ++e) from_f32(x[e], out[r.head + (int64_t)i * N + e]);
         }
       };
-      if (keep) {
-        for (int g = 0; g < groups; ++g) {
-          uint4 v[kDsU];
-          stream.read(g, count, v);
+      stream.row(count, [](uint4*, int) {}, [&](const uint4 (&v)[kDsU], int g) {
 #pragma unroll
-          for (int u = 0; u < kDsU; ++u) {
-            const int i = g * kDsU * TH + u * TH + k;
-            if (i < count) put(v[u], v0 + i);
-          }
-          stream.fetch();
+        for (int u = 0; u < kDsU; ++u) {
+          const int i = g * kDsU * TH + u * TH + k;
+          if (i < count) put(v[u], v0 + i);
         }
-        stream.advance(groups);
-      } else {
-        for (int i = v0 + k; i < v1; i += TH) put(__ldcs(r.vec() + i), i);
-      }
+      });
       if (has_edge) from_f32(grad(to_f32(row[edge])), out[edge]);
       __syncthreads();
       // ids of this block's part, over what the stream wrote there
@@ -409,6 +394,8 @@ __global__ void __launch_bounds__(kDbThreads) distill_backward_kernel(DistillArg
     list.a[k] = a.teacher_logits[t * a.K + k];
     list.x[k] = id >= 0 && own(id) ? to_f32(row[id]) : 0.0f;
   }
+  const float4 st = *reinterpret_cast<const float4*>(a.stats + 4 * t);
+  const float lse_row = a.teacher_lse ? a.teacher_lse[t] : 0.0f, g_row = a.g[t];
   int i = v0 + k;
   uint4 v[kDbBatch];
 #pragma unroll
@@ -426,12 +413,11 @@ __global__ void __launch_bounds__(kDbThreads) distill_backward_kernel(DistillArg
     list.id[k] = -1;
   }
   __syncthreads();
-  const float4 st = *reinterpret_cast<const float4*>(a.stats + 4 * t);
   const float m = st.x, l = st.y, mt = st.z, lt = st.w;
   const bool none = m == neg_inf(), empty = mt == neg_inf();
   if (k < 32) {
-    const Teacher T = teacher_side(list, a.K, a.inv_t, a.teacher_lse, t, b == 0 ? a.status : nullptr);
-    const float g = a.g[t] * a.inv_t;
+    const Teacher T = teacher_side(list, a.K, a.inv_t, a.teacher_lse != nullptr, lse_row, b == 0 ? a.status : nullptr);
+    const float g = g_row * a.inv_t;
     for (int j = k; j < a.K; j += 32) {
       const float lp = (list.x[j] - m) * a.inv_t - l;
       list.a[j] = none ? 0.0f : g * (expf(lp) * T.Q - teacher_q(T, list, j, a.inv_t));
@@ -507,15 +493,13 @@ static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
   }
   const bool grad = a.dlogits != nullptr;
   const int sms = gemm_num_ctas(), bits = (a.V + 2 * Row<E>::kVec + 31) / 32 * 4;
-  const int64_t stay = (kDsD - 1) * kDsU;  // vectors per thread that a part may keep
   const int slots = kDsU * kDsD * 16;      // ring bytes per thread
-  const int most = bits <= 28 * 1024 ? 1024 : bits <= 100 * 1024 ? 512 : 256;  // threads whose ring fits beside the bits
+  const int most = DSMOST;
   // Few rows: blocks of a cluster per row until there is one for each SM.
   int nb = 1, th = 32;
   while (nb < 8 && (int64_t)a.T * nb < sms && nvec / (nb * 2) >= 512) nb *= 2;
-  if (grad) {  // the fewest threads that keep their parts
-    while (nb < 8 && (nvec + nb - 1) / nb > stay * most) nb *= 2;
-    while (th < most && (nvec + nb - 1) / nb > stay * th) th = th == 32 ? 128 : th * 2;
+  if (grad) {
+    while (th < most && (nvec + nb - 1) / nb > DSPER * th) th = th == 32 ? 128 : th * 2;
   } else if (nvec / nb > 1024) {
     th = 128;
   }

@@ -414,21 +414,21 @@ struct Part {
 // A sequence of row parts read by TH threads (thread k takes the vectors k, k
 // + TH, ..) through a ring of slots of the thread's own in shared memory: D
 // groups of U asynchronous 16-byte copies in flight, across the ends of rows,
-// and no barrier between threads.  part(t) names row t's part.
-template <int TH, int U, int D, typename E, typename P>
+// and no barrier between threads.  part(t) names row t's part; each part comes
+// PASSES times before the next.
+template <int TH, int U, int D, int PASSES, typename E, typename P>
 struct Stream {
-  static constexpr int kBytesPerThread = U * D * 16;
   P part;
-  uint4* ring;  // this thread's first slot; slots kStride apart
+  uint4* ring;  // this thread's first slot; slots `stride` apart
   int stride, k;
   int64_t T, step;
-  // next group to fetch: of row t, from vector i (this thread's)
+  // next group to fetch: of row t, from vector i
   int64_t t;
   Part cur;
-  int i, fill, use;
+  int i, pass, fill, use;
 
   __device__ __forceinline__ Stream(P p, uint4* ring_, int stride_, int k_, int64_t t0, int64_t step_, int64_t T_)
-      : part(p), ring(ring_), stride(stride_), k(k_), T(T_), step(step_), t(t0), i(0), fill(0), use(0) {
+      : part(p), ring(ring_), stride(stride_), k(k_), T(T_), step(step_), t(t0), i(0), pass(0), fill(0), use(0) {
     if (t < T) cur = part(t);
 #pragma unroll
     for (int g = 0; g < D; ++g) fetch();
@@ -452,51 +452,31 @@ struct Stream {
       i += U * TH;
       if (i >= cur.count) {
         i = 0;
-        t += step;
-        if (t < T) cur = part(t);
+        if (PASSES > 1 && pass + 1 < PASSES) {
+          ++pass;
+        } else {
+          pass = 0;
+          t += step;
+          if (t < T) cur = part(t);
+        }
       }
     }
     cp_async_commit();
   }
-  // Groups of a part of `count` vectors; an empty part has one, of -inf.
-  static __device__ __forceinline__ int groups(int count) { return count > U * TH ? (count + U * TH - 1) / (U * TH) : 1; }
-  // Waits for the current part's next group.  Each group looked at is followed
-  // by one commit, a fetch() into its slots or hold() where they are kept: the
-  // D - 1 latest commits then never include the group waited for.
-  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory"); }
-  __device__ __forceinline__ void hold() { cp_async_commit(); }
-  // This thread's first slot of group g of the current part.
-  __device__ __forceinline__ uint4* slot(int g) const {
-    const int s = use + g;
-    return ring + (s >= D ? s - D : s) * U * stride;
-  }
-  // Group g of the current part (of `count` vectors), from its slots.  Places
-  // past the end hold -inf.
-  __device__ __forceinline__ void read(int g, int count, uint4 (&v)[U]) const {
-    const uint4* p = slot(g);
-#pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = p[u * stride];
-    const int j = g * U * TH + k;
-    if ((g + 1) * U * TH > count) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (j + u * TH >= count) v[u] = none(E());
-    }
-  }
-  // The part is done with: n of its groups' slots were freed by fetches.
-  __device__ __forceinline__ void advance(int n) { use = (use + n) % D; }
-  // All groups of the next part in turn, each slot refilled after it:
-  // pre(slot, g) on the slots, then f(v, g).
+  // The next pass over a part of `count` vectors in groups of U: pre(slot, g)
+  // on the group's slots, then f(v, g) on its vectors; each slot refilled after
+  // it.  Places past the end hold -inf; an empty part is one group of such.
   template <typename P2, typename F>
   __device__ __forceinline__ void row(int count, P2 pre, F f) {
-    const int n = groups(count);
+    const int n = count > U * TH ? (count + U * TH - 1) / (U * TH) : 1;
     for (int g = 0; g < n; ++g) {
-      wait();
-      pre(slot(0), g);
+      asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+      uint4* slot = ring + use * U * stride;
+      use = use + 1 == D ? 0 : use + 1;
+      pre(slot, g);
       uint4 v[U];
-      const uint4* p = slot(0);
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = p[u * stride];
+      for (int u = 0; u < U; ++u) v[u] = slot[u * stride];
       const int j = g * U * TH + k;
       if ((g + 1) * U * TH > count) {
 #pragma unroll
@@ -504,7 +484,6 @@ struct Stream {
           if (j + u * TH >= count) v[u] = none(E());
       }
       f(v, g);
-      use = use + 1 == D ? 0 : use + 1;
       fetch();  // into the slots just read
     }
   }

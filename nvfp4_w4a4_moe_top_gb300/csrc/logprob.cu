@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_ker
   float* slots = reinterpret_cast<float*>(ring + kLpThreads * kLpU * kLpD<TOP>) + threadIdx.x;
   const int groups = (a.V / Row<E>::kVec / nb + kLpU * TH) / (kLpU * TH), runs = (groups + kLpSlots - 1) / kLpSlots;
   const int shift = runs <= 1 ? 0 : 32 - __clz(runs - 1);
-  Stream<TH, kLpU, kLpD<TOP>, E, decltype(part)> stream(part, ring + threadIdx.x, kLpThreads, k, t0, step, a.T);
+  Stream<TH, kLpU, kLpD<TOP>, 1, E, decltype(part)> stream(part, ring + threadIdx.x, kLpThreads, k, t0, step, a.T);
   int odd = 0, ynext = a.logprob && k == 0 && rank == 0 && t0 < a.T ? a.targets[t0] : -1;
   for (int64_t t = t0; t < a.T; t += step, odd ^= 1) {
     const E* row = logits + t * a.ld;
