@@ -3,17 +3,9 @@
 
 namespace moe {
 
-#ifndef DSD
-#define DSD 2
-#define DSU 4
-#define DSMOST 512
-#define DSPER 16
-#endif
-constexpr int kDsU = DSU, kDsD = DSD;  // vectors per group of copies, groups in flight
+constexpr int kDsU = 4, kDsD = 2;  // vectors per group of copies, groups in flight
 constexpr int kDsMaxThreads = 1024;
-#ifndef DSTURNS
-#define DSTURNS 4
-#endif
+constexpr int kDsTurns = 4;  // resident grids of rows per launch at most (see kLpTurns)
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -100,13 +92,14 @@ __device__ __forceinline__ uint32_t listed_bits(const uint32_t* bits, int i, flo
   return reinterpret_cast<const uint8_t*>(bits)[(i + 1) >> 1] >> ((i + 1 & 1) * 4) & 15u;
 }
 
-// The loss, and with GRAD the gradient, of rows in turn, TH threads (one
-// block) per row or, in a cluster of gridDim.x blocks, per part of a row.  A
-// bit per id marks the listed ones, whose elements leave the stream, so that
-// the mass off the list is summed by itself.  With GRAD the stream brings each
-// part twice, for the sums and for the gradient; the second time it comes from
+// Rows in turn, TH threads (one block) per row, or per part of a row: of
+// gridDim.x parts, which with SUMS form a cluster.  SUMS: the row's sums,
+// loss and statistics; GRAD: its gradient, from the sums or (without SUMS) the
+// stored statistics.  A bit per id marks the listed ones, whose elements leave
+// the stream of the sums, so that the mass off the list is summed by itself.
+// With both, the stream brings each part twice; the second time it comes from
 // L2, which holds the rows that the resident blocks work on.
-template <typename E, bool GRAD, int TH>
+template <typename E, bool SUMS, bool GRAD, int TH>
 __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(DistillArgs a) {
   constexpr int N = Row<E>::kVec, NW = TH / 32;
   extern __shared__ uint4 ring[];
@@ -115,7 +108,7 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
   __shared__ Run<false> cpart;
   __shared__ Soft<false> sred[NW];
   __shared__ float coef[2];
-  __shared__ bool slow;
+  __shared__ bool diff;
   __shared__ int dup;
   const int nb = gridDim.x, lg = 31 - __clz(nb), rank = blockIdx.x, k = threadIdx.x, lane = k & 31;  // nb: a power of two
   const int64_t t0 = blockIdx.y, step = gridDim.y;
@@ -129,7 +122,7 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
     const int v0 = r.part(rank, lg), v1 = r.part(rank + 1, lg);
     return Part{r.vec() + v0, v1 - v0};
   };
-  Stream<TH, kDsU, kDsD, GRAD ? 2 : 1, E, decltype(part)> stream(part, ring + k, TH, k, t0, step, a.T);
+  Stream<TH, kDsU, kDsD, SUMS && GRAD ? 2 : 1, E, decltype(part)> stream(part, ring + k, TH, k, t0, step, a.T);
   __syncthreads();
   // the next row's entry of this thread (all of them where TH >= K)
   int nid = -1;
@@ -141,6 +134,8 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
     const int v0 = r.part(rank, lg), v1 = r.part(rank + 1, lg), count = v1 - v0;
     auto bit_of = [&](int id) { return id - r.head + N; };
     const float g_row = GRAD && k < 32 ? a.g[t] : 0.0f, lse_row = a.teacher_lse && k < 32 ? a.teacher_lse[t] : 0.0f;
+    float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!SUMS && k < 32) st = *reinterpret_cast<const float4*>(a.stats + 4 * t);
     // ---- the list: range, repeats (the first stays), bits ----
     float xs = 0.0f;
     for (int j = k; j < a.K; j += TH) {
@@ -179,129 +174,149 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
       }
       if (k == 0) dup = 0;
     }
-    // ---- the sums off the list ----
-    Run<false> acc;
-    // the listed elements of a group (in the thread's own slots) leave it
-    auto drop = [&](uint4* slot, int g) {
-      const int i = g * kDsU * TH + k;
-      uint32_t b[kDsU], any = 0;
-#pragma unroll
-      for (int u = 0; u < kDsU; ++u) {
-        b[u] = i + u * TH < count ? listed_bits(bits, v0 + i + u * TH, E()) : 0u;
-        any |= b[u];
-      }
-      if (any) {
-#pragma unroll
-        for (int u = 0; u < kDsU; ++u) drop_listed(slot + u * TH, b[u], E());
-      }
-    };
-    stream.row(count, drop, [&](const uint4 (&v)[kDsU], int) { acc.add(v, c, E()); });
     auto listed = [&](int i) { return (bits[bit_of(i) >> 5] >> (bit_of(i) & 31) & 1u) != 0u; };
     const int edge = k < r.head ? k : r.tail_start() + k - r.head;  // this thread's element outside the vectors
     const bool has_edge = rank == 0 && k < r.head + r.tail;
-    if (has_edge && !listed(edge)) {
-      const float x[1] = {to_f32(row[edge])};
-      acc.add(x, c);
-    }
-    if (k < a.K) list.x[k] = xs;
-    acc.template warp_merge<32>();
-    if (lane == 0) red[k >> 5] = acc;
-    __syncthreads();
-    // ---- one warp: the parts, the list, the loss, the gradient on the list ----
-    // mt, lt: maximum and ln-sum off the list; the gradient there is coef[0]
-    // times 2^(x c - shift), or 2^((x - shift) c) after the slow path
-    auto finish = [&](float mt, float lt, bool empty, float rescale, float shift) {
-      const Teacher T = teacher_side(list, a.K, a.inv_t, a.teacher_lse != nullptr, lse_row, rank == 0 ? a.status : nullptr);
-      float m = empty ? kLowest : mt;
-      bool any = !empty;
-      for (int j = lane; j < a.K; j += 32)
-        if (list.id[j] >= 0) {
-          m = max_nan(m, list.x[j]);
-          any |= list.x[j] != neg_inf();
-        }
-      m = warp_max_nan(m);
-      any = __any_sync(0xFFFFFFFFu, any);
-      float s = 0.0f;
-      for (int j = lane; j < a.K; j += 32)
-        if (list.id[j] >= 0) s += exp2_fast((list.x[j] - m) * c);
-      s = warp_sum(s);
-      if (!empty) s += exp2_fast((mt - m) * c) * expf(lt);
-      const bool bad = !(m <= 3.402823466e+38f), none = !any;
-      float l = logf(s);
-      if (none) m = neg_inf(), l = 0.0f;
-      if (bad) m = l = mt = lt = quiet_nan();
-      const float ls = empty ? neg_inf() : (mt - m) * a.inv_t + lt - l;  // ln of the mass off the list
-      float part = 0.0f;
+    // By one warp, from the maxima and ln-sums of the row (m, l) and of its part
+    // off the list (mt, lt): the gradient on the list, and off it coef[0] times
+    // 2^(x c - shift), or 2^((x - shift) c) with `diff`.
+    auto gradient = [&](const Teacher& T, float m, float l, float mt, float lt, float rescale, float shift) {
       const float g = g_row * a.inv_t;
       for (int j = lane; j < a.K; j += 32) {
-        const float q = teacher_q(T, list, j, a.inv_t), lp = (list.x[j] - m) * a.inv_t - l;
-        if (list.id[j] >= 0 && !(q == 0.0f)) part += none ? -neg_inf() : q * (T.lq(list.a[j], a.inv_t) - lp);
-        if (GRAD) list.a[j] = none ? 0.0f : g * (expf(lp) * T.Q - q);  // the gradient at this id
+        const float lp = (list.x[j] - m) * a.inv_t - l;
+        list.a[j] = m == neg_inf() ? 0.0f : g * (expf(lp) * T.Q - teacher_q(T, list, j, a.inv_t));
       }
-      part = warp_sum(part);
-      if (!(T.r == 0.0f)) part += none ? -neg_inf() : T.r * (logf(T.r) - ls);
-      if (bad || T.Q != T.Q) part = quiet_nan();
       if (lane == 0) {
-        if (rank == 0) {
+        const float ls = (mt - m) * a.inv_t + lt - l;  // ln of the mass off the list
+        coef[0] = mt == neg_inf() ? 0.0f : g * (expf(ls) * T.Q - T.r) * rescale;
+        coef[1] = shift;
+      }
+    };
+    auto teacher = [&]() {
+      return teacher_side(list, a.K, a.inv_t, a.teacher_lse != nullptr, lse_row, rank == 0 ? a.status : nullptr);
+    };
+    if (SUMS) {
+      Run<false> acc;
+      // the listed elements of a group (in the thread's own slots) leave it
+      auto drop = [&](uint4* slot, int g) {
+        const int i = g * kDsU * TH + k;
+        uint32_t b[kDsU], any = 0;
+#pragma unroll
+        for (int u = 0; u < kDsU; ++u) {
+          b[u] = i + u * TH < count ? listed_bits(bits, v0 + i + u * TH, E()) : 0u;
+          any |= b[u];
+        }
+        if (any) {
+#pragma unroll
+          for (int u = 0; u < kDsU; ++u) drop_listed(slot + u * TH, b[u], E());
+        }
+      };
+      stream.row(count, drop, [&](const uint4 (&v)[kDsU], int) { acc.add(v, c, E()); });
+      if (has_edge && !listed(edge)) {
+        const float x[1] = {to_f32(row[edge])};
+        acc.add(x, c);
+      }
+      if (k < a.K) list.x[k] = xs;
+      acc.template warp_merge<32>();
+      if (lane == 0) red[k >> 5] = acc;
+      __syncthreads();
+      // By one warp, from the part off the list: the row's statistics, the loss
+      // and the gradient.
+      auto finish = [&](float mt, float lt, float rescale, float shift) {
+        const bool empty = mt == neg_inf();
+        const Teacher T = teacher();
+        float m = empty ? kLowest : mt;
+        bool any = !empty;
+        for (int j = lane; j < a.K; j += 32)
+          if (list.id[j] >= 0) {
+            m = max_nan(m, list.x[j]);
+            any |= list.x[j] != neg_inf();
+          }
+        m = warp_max_nan(m);
+        any = __any_sync(0xFFFFFFFFu, any);
+        float s = 0.0f;
+        for (int j = lane; j < a.K; j += 32)
+          if (list.id[j] >= 0) s += exp2_fast((list.x[j] - m) * c);
+        s = warp_sum(s);
+        if (!empty) s += exp2_fast((mt - m) * c) * expf(lt);
+        const bool bad = !(m <= 3.402823466e+38f), none = !any;
+        float l = logf(s);
+        if (none) m = neg_inf(), l = 0.0f;
+        if (bad) m = l = mt = lt = quiet_nan();
+        float part = 0.0f;
+        for (int j = lane; j < a.K; j += 32) {
+          const float q = teacher_q(T, list, j, a.inv_t), lp = (list.x[j] - m) * a.inv_t - l;
+          if (list.id[j] >= 0 && !(q == 0.0f)) part += none ? -neg_inf() : q * (T.lq(list.a[j], a.inv_t) - lp);
+        }
+        part = warp_sum(part);
+        const float ls = empty ? neg_inf() : (mt - m) * a.inv_t + lt - l;
+        if (!(T.r == 0.0f)) part += none ? -neg_inf() : T.r * (logf(T.r) - ls);
+        if (bad || T.Q != T.Q) part = quiet_nan();
+        if (GRAD) gradient(T, m, l, mt, lt, rescale, shift);
+        if (lane == 0 && rank == 0) {
           if (bad) set_status(a.status, MOE_STATUS_NONFINITE_LOGITS);
           a.loss[t] = part;
           if (a.stats_out) *reinterpret_cast<float4*>(a.stats_out + 4 * t) = make_float4(m, l, mt, lt);
         }
-        coef[0] = empty ? 0.0f : bad ? quiet_nan() : g * (expf(ls) * T.Q - T.r) * rescale;
-        coef[1] = shift;
-      }
-    };
-    if (k < 32) {
-      acc = Run<false>();
-      if (lane < NW) acc = red[lane];
-      acc.template warp_merge<32>();
-      if (lane == 0) cpart = acc;
-    }
-    if (nb > 1) {
-      cluster_arrive();
-      cluster_wait();
+      };
       if (k < 32) {
         acc = Run<false>();
-        if (lane < nb) {
-          acc.m = cluster_load_f32(&cpart.m, lane);
-          acc.M = cluster_load_f32(&cpart.M, lane);
-          acc.s = cluster_load_f32(&cpart.s, lane);
-        }
+        if (lane < NW) acc = red[lane];
         acc.template warp_merge<32>();
+        if (lane == 0) cpart = acc;
       }
-      cluster_arrive();  // this block has read the others' parts; waited for before cpart is written again
-    }
-    if (k < 32) {
-      acc.s = __shfl_sync(0xFFFFFFFFu, acc.s, 0);
-      const bool differ = acc.m <= 3.402823466e+38f && !acc.shift_ok(c);
-      if (lane == 0) slow = differ;
-      if (!differ)
-        finish(acc.m, kLn2 * (log2f(acc.s) - fmaf(acc.m, c, -acc.M)), false, 1.0f / acc.s, acc.M);
-    }
-    __syncthreads();
-    if (slow) {  // masks at extreme values, or nothing off the list: differences first
-      Soft<false> all;
-      for (int i = k; i < a.V; i += TH)
-        if (!listed(i)) {
-          const float x[1] = {to_f32(row[i])};
-          all.add(x, c);
+      if (nb > 1) {
+        cluster_arrive();
+        cluster_wait();
+        if (k < 32) {
+          acc = Run<false>();
+          if (lane < nb) {
+            acc.m = cluster_load_f32(&cpart.m, lane);
+            acc.M = cluster_load_f32(&cpart.M, lane);
+            acc.s = cluster_load_f32(&cpart.s, lane);
+          }
+          acc.template warp_merge<32>();
         }
-      all.warp_merge(c);
-      if (lane == 0) sred[k >> 5] = all;
-      if (nb > 1) {  // no block writes (dlogits may be the logits) before all have read the row
-        cluster_wait();
-        cluster_arrive();
-        cluster_wait();
-        cluster_arrive();
+        cluster_arrive();  // this block has read the others' parts; waited for before cpart is written again
+      }
+      if (k < 32) {
+        acc.s = __shfl_sync(0xFFFFFFFFu, acc.s, 0);
+        const bool differ = acc.m <= 3.402823466e+38f && !acc.shift_ok(c);
+        if (lane == 0) diff = differ;
+        if (!differ) finish(acc.m, kLn2 * (log2f(acc.s) - fmaf(acc.m, c, -acc.M)), 1.0f / acc.s, acc.M);
       }
       __syncthreads();
-      if (k < 32) {
-        all = Soft<false>();
-        if (lane < NW) all = sred[lane];
+      if (diff) {  // masks at extreme values, or nothing off the list: differences first
+        Soft<false> all;
+        for (int i = k; i < a.V; i += TH)
+          if (!listed(i)) {
+            const float x[1] = {to_f32(row[i])};
+            all.add(x, c);
+          }
         all.warp_merge(c);
-        const bool empty = all.s == 0.0f;
-        const float lt = empty ? 0.0f : logf(all.s);
-        finish(empty ? neg_inf() : all.m, lt, empty, expf(-lt), all.m);
+        if (lane == 0) sred[k >> 5] = all;
+        if (nb > 1) {  // no block writes (dlogits may be the logits) before all have read the row
+          cluster_wait();
+          cluster_arrive();
+          cluster_wait();
+          cluster_arrive();
+        }
+        __syncthreads();
+        if (k < 32) {
+          all = Soft<false>();
+          if (lane < NW) all = sred[lane];
+          all.warp_merge(c);
+          const float lt = all.s == 0.0f ? 0.0f : logf(all.s);
+          finish(all.s == 0.0f ? neg_inf() : all.m, lt, expf(-lt), all.m);
+        }
+        __syncthreads();
+      }
+    } else {
+      if (k < a.K) list.x[k] = xs;
+      __syncthreads();
+      if (k < 32) {
+        if (lane == 0) diff = true;
+        gradient(teacher(), st.x, st.y, st.z, st.w, expf(-st.w), st.z);
       }
       __syncthreads();
     }
@@ -312,27 +327,26 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
       if (list.id[j] >= 0) bits[bit_of(list.id[j]) >> 5] = 0u;
     if (GRAD) {
       const float w = coef[0], shift = coef[1];
-      const bool diff = slow;
+      const bool by_diff = diff;
       E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
       const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
       auto grad = [&](float x) {
-        if (!diff) return w * exp2_fast(fmaf(x, c, -shift));
-        return w == 0.0f ? 0.0f : w * exp2_fast((x - shift) * c);
+        return w == 0.0f ? 0.0f : w * exp2_fast(by_diff ? (x - shift) * c : fmaf(x, c, -shift));
       };
+      const uint64_t c2 = f32x2_pack(c, c), s2 = f32x2_pack(-shift, -shift), w2 = f32x2_pack(w, w);
       auto put = [&](const uint4& v, int i) {  // vector i of the row
         float x[N];
         unpack(v, x);
-        if (diff) {
 #pragma unroll
-          for (int e = 0; e < N; ++e) x[e] = grad(x[e]);
-        } else {
-          const uint64_t c2 = f32x2_pack(c, c), s2 = f32x2_pack(-shift, -shift), w2 = f32x2_pack(w, w);
+        for (int e = 0; e < N; e += 2) {
+          const uint64_t xe = f32x2_pack(x[e], x[e + 1]);
+          float lo, hi;
+          unpack2(by_diff ? mul_f32x2(add_f32x2(xe, s2), c2) : fma_f32x2(xe, c2, s2), lo, hi);
+          unpack2(mul_f32x2(f32x2_pack(exp2_fast(lo), exp2_fast(hi)), w2), x[e], x[e + 1]);
+        }
+        if (w == 0.0f) {  // also where nothing is off the list, and the shift no number
 #pragma unroll
-          for (int e = 0; e < N; e += 2) {
-            float lo, hi;
-            unpack2(fma_f32x2(f32x2_pack(x[e], x[e + 1]), c2, s2), lo, hi);
-            unpack2(mul_f32x2(f32x2_pack(exp2_fast(lo), exp2_fast(hi)), w2), x[e], x[e + 1]);
-          }
+          for (int e = 0; e < N; ++e) x[e] = 0.0f;
         }
         if (same) {
           __stcs(reinterpret_cast<uint4*>(out + r.head) + i, pack(x));
@@ -357,159 +371,45 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
         if (id >= 0 && ((id >= lo && id < hi) || (rank == 0 && id >= r.tail_start()))) from_f32(list.a[j], out[id]);
       }
     }
-    if (nb > 1) cluster_wait();
+    if (SUMS && nb > 1) cluster_wait();
     __syncthreads();
   }
 }
 
-// The gradient from stored statistics; blockIdx.x a part of the row.  Warp 0
-// works out the teacher's side while the others' loads are on their way; the
-// block overwrites its listed ids at the end.
-constexpr int kDbThreads = 256, kDbBatch = 4;
-constexpr int kDbPart = kDbThreads * kDbBatch * 2;  // vectors of a block
-
-template <typename E>
-__global__ void __launch_bounds__(kDbThreads) distill_backward_kernel(DistillArgs a) {
-  constexpr int N = Row<E>::kVec;
-  __shared__ DsList list;
-  __shared__ float coef[2];
-  const int64_t t = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
-  if (t >= a.T) return;
-  const int k = threadIdx.x, b = blockIdx.x;
-  const E* row = static_cast<const E*>(a.logits) + t * a.ld;
-  E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
-  const Row<E> r(row, a.V);
-  const float c = a.inv_t * kLog2e;
-  const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
-  const int v0 = min(b * kDbPart, r.nvec), v1 = min(v0 + kDbPart, r.nvec);
-  const int lo = b == 0 ? 0 : r.head + v0 * N, hi = r.head + v1 * N;  // ids of this block (and the tail's, block 0)
-  auto own = [&](int id) { return (id >= lo && id < hi) || (b == 0 && id >= r.tail_start()); };
-  if (k < a.K) {  // K <= kDbThreads
-    int id = a.teacher_ids[t * a.K + k];
-    if (id >= a.V) {
-      if (b == 0) set_status(a.status, MOE_STATUS_BAD_TOKEN);
-      id = -1;
-    }
-    list.id[k] = id;
-    list.a[k] = a.teacher_logits[t * a.K + k];
-    list.x[k] = id >= 0 && own(id) ? to_f32(row[id]) : 0.0f;
-  }
-  const float4 st = *reinterpret_cast<const float4*>(a.stats + 4 * t);
-  const float lse_row = a.teacher_lse ? a.teacher_lse[t] : 0.0f, g_row = a.g[t];
-  int i = v0 + k;
-  uint4 v[kDbBatch];
-#pragma unroll
-  for (int u = 0; u < kDbBatch; ++u)
-    if (i + u * kDbThreads < v1) v[u] = __ldcs(r.vec() + i + u * kDbThreads);
-  __syncthreads();
-  bool again = false;  // a repeat: the first of its id stays
-  if (k < a.K && list.id[k] >= 0) {
-    const int id = list.id[k];
-    for (int j = 0; j < k; ++j) again |= list.id[j] == id;
-  }
-  __syncthreads();
-  if (again) {
-    if (b == 0) set_status(a.status, MOE_STATUS_BAD_TOKEN);
-    list.id[k] = -1;
-  }
-  __syncthreads();
-  const float m = st.x, l = st.y, mt = st.z, lt = st.w;
-  const bool none = m == neg_inf(), empty = mt == neg_inf();
-  if (k < 32) {
-    const Teacher T = teacher_side(list, a.K, a.inv_t, a.teacher_lse != nullptr, lse_row, b == 0 ? a.status : nullptr);
-    const float g = g_row * a.inv_t;
-    for (int j = k; j < a.K; j += 32) {
-      const float lp = (list.x[j] - m) * a.inv_t - l;
-      list.a[j] = none ? 0.0f : g * (expf(lp) * T.Q - teacher_q(T, list, j, a.inv_t));
-    }
-    if (k == 0) {
-      const float ls = (mt - m) * a.inv_t + lt - l;
-      coef[0] = empty || none ? 0.0f : g * (expf(ls) * T.Q - T.r) * expf(-lt);
-    }
-  }
-  __syncthreads();
-  const float w = coef[0];
-  auto grad = [&](float x) { return w * exp2_fast((x - mt) * c); };
-  auto put = [&](const uint4& q, int at) {
-    float x[N];
-    unpack(q, x);
-    if (empty || none) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) x[e] = 0.0f;
-    } else {
-      const uint64_t m2 = f32x2_pack(-mt, -mt), c2 = f32x2_pack(c, c), w2 = f32x2_pack(w, w);
-#pragma unroll
-      for (int e = 0; e < N; e += 2) {
-        float p, q2;
-        unpack2(mul_f32x2(add_f32x2(f32x2_pack(x[e], x[e + 1]), m2), c2), p, q2);
-        unpack2(mul_f32x2(f32x2_pack(exp2_fast(p), exp2_fast(q2)), w2), x[e], x[e + 1]);
-      }
-    }
-    if (same) {
-      __stcs(reinterpret_cast<uint4*>(out + r.head) + at, pack(x));
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e) from_f32(x[e], out[r.head + (int64_t)at * N + e]);
-    }
-  };
-  while (i < v1) {
-    const int next = i + kDbBatch * kDbThreads;
-    uint4 nv[kDbBatch];
-#pragma unroll
-    for (int u = 0; u < kDbBatch; ++u)
-      if (next + u * kDbThreads < v1) nv[u] = __ldcs(r.vec() + next + u * kDbThreads);
-#pragma unroll
-    for (int u = 0; u < kDbBatch; ++u)
-      if (i + u * kDbThreads < v1) put(v[u], i + u * kDbThreads);
-#pragma unroll
-    for (int u = 0; u < kDbBatch; ++u) v[u] = nv[u];
-    i = next;
-  }
-  if (b == 0 && k < r.head + r.tail) {
-    const int e = k < r.head ? k : r.tail_start() + k - r.head;
-    from_f32(empty || none ? 0.0f : grad(to_f32(row[e])), out[e]);
-  }
-  __syncthreads();
-  if (k < a.K && list.id[k] >= 0 && own(list.id[k])) from_f32(list.a[k], out[list.id[k]]);
-}
-
 // host launchers
-template <typename E, bool GRAD>
+template <typename E, bool SUMS, bool GRAD>
 static void (*distill_of(int th))(DistillArgs) {
-  return th == 32     ? distill_kernel<E, GRAD, 32>
-         : th == 128  ? distill_kernel<E, GRAD, 128>
-         : th == 256  ? distill_kernel<E, GRAD, 256>
-         : th == 512  ? distill_kernel<E, GRAD, 512>
-                      : distill_kernel<E, GRAD, 1024>;
+  return th == 32     ? distill_kernel<E, SUMS, GRAD, 32>
+         : th == 128  ? distill_kernel<E, SUMS, GRAD, 128>
+         : th == 256  ? distill_kernel<E, SUMS, GRAD, 256>
+         : th == 512  ? distill_kernel<E, SUMS, GRAD, 512>
+                      : distill_kernel<E, SUMS, GRAD, SUMS && GRAD ? 1024 : 512>;
 }
 template <typename E>
 static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
   const int64_t nvec = (int64_t)a.V / Row<E>::kVec;
-  const unsigned gy = a.T < 65535 ? a.T : 65535;
-  if (!a.loss) {
-    const dim3 grid((unsigned)(nvec <= kDbPart ? 1 : (nvec + kDbPart - 1) / kDbPart), gy, (a.T + gy - 1) / gy);
-    distill_backward_kernel<E><<<grid, kDbThreads, 0, s>>>(a);
-    return 0;
-  }
-  const bool grad = a.dlogits != nullptr;
+  const bool sums = a.loss != nullptr, grad = a.dlogits != nullptr;
   const int sms = gemm_num_ctas(), bits = (a.V + 2 * Row<E>::kVec + 31) / 32 * 4;
-  const int slots = kDsU * kDsD * 16;      // ring bytes per thread
-  const int most = DSMOST;
-  // Few rows: blocks of a cluster per row until there is one for each SM.
-  int nb = 1, th = 32;
+  const int most = bits <= 80 * 1024 ? 1024 : 512;  // threads whose ring fits beside the bits
+  // Few rows: more blocks per row until there is one for each SM.
+  int nb = 1;
   while (nb < 8 && (int64_t)a.T * nb < sms && nvec / (nb * 2) >= 512) nb *= 2;
-  if (grad) {
-    while (th < most && (nvec + nb - 1) / nb > DSPER * th) th = th == 32 ? 128 : th * 2;
-  } else if (nvec / nb > 1024) {
-    th = 128;
-  }
+  // Threads per row.  A warp for short rows; 128 while they hide a row's ends
+  // behind others, else 256 (the loss of 16384 x 32768 BF16: 175 us with 128,
+  // 213 with 256; of 4096 x 131072: 166 and 153).  The step's 1024 threads per
+  // SM work on rows that L2 has to hold between the passes: 80 MB of it.
+  const int64_t part = nvec / nb;
+  int th = part <= 1024 ? 32 : part <= 8192 ? 128 : 256;
+  if (sums && grad && th > 32) th = part <= 8192 ? 256 : part <= 16384 ? 512 : 1024;
+  if (bits > 40 * 1024 && th < 256) th = 256;
   if ((int64_t)a.T * nb <= 2 * sms)
-    while (th < 512 && th < most && nvec / nb > 2 * th) th = th == 32 ? 128 : th * 2;
-  const int smem = th * slots + bits;
+    while (th < 512 && part > 2 * th) th = th == 32 ? 128 : th * 2;
+  if (th > most) th = most;
+  const int smem = th * kDsU * kDsD * 16 + bits;
   int fit = 227 * 1024 / (smem + 5 * 1024);
   if (fit > kDsMaxThreads / th) fit = kDsMaxThreads / th;
   if (fit < 1) fit = 1;
-  const int64_t grid = (int64_t)sms * fit / nb * DSTURNS;
+  const int64_t grid = (int64_t)sms * fit / nb * kDsTurns;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nb, (unsigned)(a.T < grid ? a.T : grid));
   cfg.blockDim = dim3(th);
@@ -520,8 +420,8 @@ static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
   at[0].val.clusterDim.x = nb;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = nb > 1 ? 1 : 0;
-  auto f = grad ? distill_of<E, true>(th) : distill_of<E, false>(th);
+  cfg.numAttrs = sums && nb > 1 ? 1 : 0;
+  auto f = sums ? (grad ? distill_of<E, true, true>(th) : distill_of<E, true, false>(th)) : distill_of<E, false, true>(th);
   if (!allow_smem((const void*)f, smem)) return -1;
   return cudaLaunchKernelEx(&cfg, f, a) == cudaSuccess ? 0 : -1;
 }

@@ -411,6 +411,13 @@ struct Part {
   int count;
 };
 
+// cp_async16 with an L2 cache policy.
+__device__ __forceinline__ void cp_async16_hint(uint32_t dst, const void* src, bool valid, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0), "l"(policy)
+               : "memory");
+}
+
 // A sequence of row parts read by TH threads (thread k takes the vectors k, k
 // + TH, ..) through a ring of slots of the thread's own in shared memory: D
 // groups of U asynchronous 16-byte copies in flight, across the ends of rows,
@@ -426,9 +433,11 @@ struct Stream {
   int64_t t;
   Part cur;
   int i, pass, fill, use;
+  uint64_t keep, drop;  // L2 policies of a pass that comes again, and of the last
 
   __device__ __forceinline__ Stream(P p, uint4* ring_, int stride_, int k_, int64_t t0, int64_t step_, int64_t T_)
       : part(p), ring(ring_), stride(stride_), k(k_), T(T_), step(step_), t(t0), i(0), pass(0), fill(0), use(0) {
+    if (PASSES > 1) keep = l2_evict_last(), drop = l2_evict_first();
     if (t < T) cur = part(t);
 #pragma unroll
     for (int g = 0; g < D; ++g) fetch();
@@ -446,7 +455,10 @@ struct Stream {
       for (int u = 0; u < U; ++u) {
         const int at = i + u * TH + k;
         const bool in = at < cur.count;
-        cp_async16(smem_u32(slot + u * stride), cur.vec + (in ? at : 0), in);
+        if (PASSES > 1)
+          cp_async16_hint(smem_u32(slot + u * stride), cur.vec + (in ? at : 0), in, pass + 1 < PASSES ? keep : drop);
+        else
+          cp_async16(smem_u32(slot + u * stride), cur.vec + (in ? at : 0), in);
       }
       fill = fill + 1 == D ? 0 : fill + 1;
       i += U * TH;
