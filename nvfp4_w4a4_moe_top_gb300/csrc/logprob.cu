@@ -215,18 +215,52 @@ __device__ __forceinline__ int group_top(const Row<E>& r, int v0, int v1, bool e
   return 32;
 }
 
-// put(place, key) for each of the n largest of the keys cand[0..c) of a group.
+// put(place, key) for each of the n largest of the keys cand[0..c) of a group:
+// a key's place is the number of larger ones.
 template <int TH, typename F>
 __device__ __forceinline__ void place_top(const uint64_t* cand, int c, int n, F put) {
-  for (int q = threadIdx.x & (TH - 1); q < c; q += TH) {
-    const uint64_t key = cand[q];
-    int larger = 0;
-    for (int j = 0; j < c; j += 8) {
+  constexpr int KC = TopShared<TH>::kCap / TH;  // keys of a thread at most
+  const int k = threadIdx.x & (TH - 1);
+  uint64_t key[KC];
+  int larger[KC];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) larger += cand[j + u] > key && j + u < c;  // the array is a multiple of 8
-    }
-    if (key != 0 && larger < n) put(larger, key);
+  for (int q = 0; q < KC; ++q) key[q] = k + q * TH < c ? cand[k + q * TH] : 0, larger[q] = 0;
+  for (int j = 0; j < c; j += 8) {  // the array is a multiple of 8
+    uint64_t o[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) o[u] = j + u < c ? cand[j + u] : 0;
+#pragma unroll
+    for (int q = 0; q < KC; ++q)
+      if (q == 0 || c > q * TH) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) larger[q] += o[u] > key[q];
+      }
   }
+#pragma unroll
+  for (int q = 0; q < KC; ++q)
+    if (key[q] != 0 && larger[q] < n) put(larger[q], key[q]);
+}
+
+// The same from nb sorted lists of 32, list b at lists + 32 b (zeros after the
+// last key): thread 32 b + i places the i-th key of list b, by its place there
+// and a binary search of each other list.
+template <typename F>
+__device__ __forceinline__ void place_lists(const uint64_t* lists, int nb, int n, F put) {
+  const int b = threadIdx.x >> 5, i = threadIdx.x & 31;
+  if (b >= nb || i >= n) return;
+  const uint64_t key = lists[32 * b + i];
+  int larger = i;
+#pragma unroll
+  for (int o = 0; o < 8; ++o) {  // nb <= 8
+    if (o < nb && o != b) {
+      int at = 0;  // keys of list o known to be larger
+#pragma unroll
+      for (int w = 32; w > 0; w >>= 1)
+        if (at + w <= 32 && lists[32 * o + at + w - 1] > key) at += w;
+      larger += at;
+    }
+  }
+  if (key != 0 && larger < n) put(larger, key);
 }
 
 // TH threads per row (or, for a cluster of nb = gridDim.x blocks, per part of
@@ -392,10 +426,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_ker
         for (int q = k; q < a.n_top; q += TH) ids[q] = -1, lps[q] = bad ? nan : neg_inf();
         group_sync<TH>();
       }
-      place_top<TH>(top.cand, found, a.n_top, [&](int at, uint64_t key) {
+      auto put = [&](int at, uint64_t key) {
         ids[at] = rank_id(key);
         lps[at] = logp(rank_logit(key));
-      });
+      };
+      if (nb > 1) place_lists(top.cand, found / 32, a.n_top, put);
+      else place_top<TH>(top.cand, found, a.n_top, put);
       group_sync<TH>();  // the candidates are read no more
     }
   }

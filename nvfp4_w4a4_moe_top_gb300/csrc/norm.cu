@@ -271,10 +271,11 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a
     fetch(t0 + D * step, g);  // into the slots just read
     g = g + 1 == D ? 0 : g + 1;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sum of the parts may be set up
   if (!a.dw) return;
   // the groups' parts of dw, added in order, make the block's
-  float* sum = reinterpret_cast<float*>(ring);
-  if (GROUPS) {
+  if constexpr (GROUPS) {
+    float* sum = reinterpret_cast<float*>(ring);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
 #pragma unroll
@@ -286,15 +287,15 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a
       for (int g2 = 1; g2 < groups; ++g2) s += sum[g2 * a.d + c];
       a.part[(int64_t)blockIdx.x * a.d + c] = s;
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = k + v * nt;
-    if (c < n) {
-      float4* p = reinterpret_cast<float4*>(a.part + (int64_t)blockIdx.x * a.d + c * 8);
-      p[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
-      p[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+    for (int v = 0; v < NV; ++v) {
+      const int c = k + v * nt;
+      if (c < n) {
+        float4* p = reinterpret_cast<float4*>(a.part + (int64_t)blockIdx.x * a.d + c * 8);
+        p[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+        p[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+      }
     }
   }
 }
@@ -304,6 +305,8 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a
 __global__ void __launch_bounds__(1024) add_rmsnorm_dw_kernel(const float* __restrict__ part, int nb, int d, float* dw) {
   __shared__ float sh[32][33];
   const int i = blockIdx.x * 32 + threadIdx.x;
+  // launched while the parts are still being made; they are complete after this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float s = 0.0f;
   if (i < d)
 #pragma unroll 8
@@ -365,9 +368,18 @@ int launch_add_rmsnorm_backward(const NormBwdArgs& a, cudaStream_t s) {
                           : add_rmsnorm_backward_kernel<1, 2, 2, false>;
   if (!allow_smem((const void*)f, p.smem)) return -1;
   f<<<dim3((unsigned)p.blocks), p.threads * p.groups, p.smem, s>>>(a, p.threads);
-  if (a.dw)
-    add_rmsnorm_dw_kernel<<<dim3((unsigned)((a.d + 31) / 32)), dim3(32, 32), 0, s>>>(a.part, p.blocks, a.d, a.dw);
-  return 0;
+  if (!a.dw) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.d + 31) / 32));
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its start overlaps the first launch's end
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const float* part = a.part;
+  return cudaLaunchKernelEx(&cfg, add_rmsnorm_dw_kernel, part, p.blocks, a.d, a.dw) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace moe
