@@ -394,18 +394,14 @@ static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
   // Few rows: more blocks per row until there is one for each SM.
   int nb = 1;
   while (nb < 8 && (int64_t)a.T * nb < sms && nvec / (nb * 2) >= 512) nb *= 2;
-  // Threads per row.  A warp for short rows; 128 while they hide a row's ends
-  // behind others, else 256 (the loss of 16384 x 32768 BF16: 175 us with 128,
-  // 213 with 256; of 4096 x 131072: 166 and 153).  The step's 1024 threads per
-  // SM work on rows that L2 has to hold between the passes: 80 MB of it.
-  // The gradient alone exchanges nothing: parts of 2048 vectors or more until
-  // the last of 16 rounds per SM weighs little (1024 x 100003 BF16: 72 -> 68 us;
-  // 500 x 100000 FP32: 76 -> 65).
-  if (!sums)
-    while (nb < 8 && (int64_t)a.T * nb < 16 * sms && nvec / (nb * 2) >= 2048) nb *= 2;
-  const int64_t part = nvec / nb;
-  int th = part <= 1024 ? 32 : part <= 8192 ? 128 : 256;
-  if (sums && grad && th > 32) th = part <= 8192 ? 256 : part <= 16384 ? 512 : 1024;
+  // Threads per row: as few as hide a row's ends (list, sums, loss) behind
+  // other rows.  Loss, BF16: 4000 x 10000 25 us with 32 and 30 with 128; 16384 x
+  // 32768 175 with 128 and 213 with 256; 4096 x 131072 166 and 153.  Gradient:
+  // 4000 x 10000 40 with 32 and 33 with 128.  The step's 1024 threads per SM
+  // work on rows that L2 has to hold between the passes: 80 MB of it (4096 x
+  // 131072: 372 with 512, 455 with 256).
+  int th = part <= (sums ? 2048 : 1024) ? 32 : part <= 8192 ? 128 : 256;
+  if (sums && grad && th > 32) th = part <= 3072 ? 128 : part <= 8192 ? 256 : part <= 16384 ? 512 : 1024;
   if (bits > 40 * 1024 && th < 256) th = 256;
   if ((int64_t)a.T * nb <= 2 * sms)
     while (th < 512 && part > 2 * th) th = th == 32 ? 128 : th * 2;

@@ -438,20 +438,21 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_ker
 }
 
 // d_v = inv_t (p_v (A - g_ent ln p_v) + g 1[v = target]), A = -g - g_ent H.
-// blockIdx.x a part of the row.
+// TH threads per row; with whole blocks, blockIdx.x is a part of the row.
 constexpr int kLbThreads = 256;
 constexpr int kLbBatch = 4;
 constexpr int kLbPart = kLbThreads * kLbBatch * 2;  // vectors of a block
 
-template <typename E>
+template <typename E, int TH>
 __global__ void __launch_bounds__(kLbThreads) token_logprobs_backward_kernel(LogprobBwdArgs a) {
   constexpr int N = Row<E>::kVec;
-  const int64_t t = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+  const int tid = threadIdx.x % TH;
+  const int64_t t = (blockIdx.y + (int64_t)blockIdx.z * gridDim.y) * (kLbThreads / TH) + threadIdx.x / TH;
   if (t >= a.T) return;
   const E* row = static_cast<const E*>(a.logits) + t * a.ld;
   E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
   const int y = a.targets ? a.targets[t] : -1;
-  if (y >= a.V && threadIdx.x == 0 && blockIdx.x == 0) set_status(a.status, MOE_STATUS_BAD_TOKEN);
+  if (y >= a.V && tid == 0 && blockIdx.x == 0) set_status(a.status, MOE_STATUS_BAD_TOKEN);
   const bool has = y >= 0 && y < a.V;
   const float g = has && a.g_logprob ? a.g_logprob[t] * a.inv_t : 0.0f;
   const float ge = a.g_entropy ? a.g_entropy[t] * a.inv_t : 0.0f;
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_backward_kernel(Log
   };
   const Row<E> r(row, a.V);
   if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0) {
-    const int b = blockIdx.x, v0 = b * kLbPart, v1 = min(v0 + kLbPart, r.nvec);
+    const int b = blockIdx.x, v0 = b * kLbPart, v1 = TH < kLbThreads ? r.nvec : min(v0 + kLbPart, r.nvec);
     uint4* ov = reinterpret_cast<uint4*>(out + r.head);
     const int yv = has && y >= r.head ? (y - r.head) / N : -1, ye = (y - r.head) % N;
     auto store = [&](const uint4& v, int i) {
@@ -480,23 +481,22 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_backward_kernel(Log
       }
       __stcs(ov + i, pack(x));
     };
-    int i = v0 + threadIdx.x;
+    int i = v0 + tid;
     if (zero) {
-      for (; i < v1; i += kLbThreads) __stcs(ov + i, make_uint4(0u, 0u, 0u, 0u));
+      for (; i < v1; i += TH) __stcs(ov + i, make_uint4(0u, 0u, 0u, 0u));
     } else {
-      for (; i + (kLbBatch - 1) * kLbThreads < v1; i += kLbBatch * kLbThreads) {
+      for (; i + (kLbBatch - 1) * TH < v1; i += kLbBatch * TH) {
         uint4 v[kLbBatch];
 #pragma unroll
-        for (int u = 0; u < kLbBatch; ++u) v[u] = __ldcs(r.vec() + i + u * kLbThreads);
+        for (int u = 0; u < kLbBatch; ++u) v[u] = __ldcs(r.vec() + i + u * TH);
 #pragma unroll
-        for (int u = 0; u < kLbBatch; ++u) store(v[u], i + u * kLbThreads);
+        for (int u = 0; u < kLbBatch; ++u) store(v[u], i + u * TH);
       }
-      for (; i < v1; i += kLbThreads) store(__ldcs(r.vec() + i), i);
+      for (; i < v1; i += TH) store(__ldcs(r.vec() + i), i);
     }
     if (b == 0) {
-      const int k = threadIdx.x < (unsigned)r.head ? (int)threadIdx.x
-                                                   : r.tail_start() + (int)threadIdx.x - r.head;
-      if ((int)threadIdx.x < r.head + r.tail) {
+      const int k = tid < r.head ? tid : r.tail_start() + tid - r.head;
+      if (tid < r.head + r.tail) {
         const float v = zero ? 0.0f : grad(to_f32(row[k])) + (k == y ? g : 0.0f);
         from_f32(v, out[k]);
       }
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_backward_kernel(Log
   } else {  // rows of different alignment: element by element
     const int64_t per = (a.V + gridDim.x - 1) / gridDim.x, k0 = per * blockIdx.x;
     const int64_t k1 = k0 + per < a.V ? k0 + per : a.V;
-    for (int64_t k = k0 + threadIdx.x; k < k1; k += kLbThreads) {
+    for (int64_t k = k0 + tid; k < k1; k += TH) {
       const float v = zero ? 0.0f : grad(to_f32(row[k])) + (k == y ? g : 0.0f);
       from_f32(v, out[k]);
     }
@@ -529,10 +529,11 @@ int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
   const int most = kLpBlocksPerSm * gemm_num_ctas();  // resident blocks
   // Threads per row.  With enough rows to fill the GPU, as few as hide the
   // row's end (sums, alternatives) behind other rows: a warp for short rows,
-  // four for long ones (4000 x 8192 BF16: 16, 19 and 29 us with 32, 128 and
-  // 256 threads; 4000 x 50000: 67, 62 and 73 us).  Else blocks, and clusters of
-  // up to 8 of them while they fill the GPU and each thread keeps two vectors.
-  const int th = nvec <= 1024 && (a.T >= 304 || nvec <= 128) ? 32 : a.T >= 304 ? 128 : kLpThreads;
+  // four for long ones (BF16, no alternatives: 4000 x 8192 16, 19 and 29 us with
+  // 32, 128 and 256 threads; 2000 x 20000 17, 19 and 25; 4000 x 50000 67, 62 and
+  // 73).  Else blocks, and clusters of up to 8 of them while they fill the GPU
+  // and each thread keeps two vectors (2 x 131072: 18 us with one, 14 with 8).
+  const int th = (nvec <= 1024 && (a.T >= 304 || nvec <= 128)) || (nvec <= 3072 && a.T >= 1000) ? 32 : a.T >= 304 ? 128 : kLpThreads;
   int nb = 1;
   if (th == kLpThreads)
     while (nb < 8 && (int64_t)a.T * nb * 2 <= most && nvec / (nb * 2) >= 2 * kLpThreads) nb *= 2;
@@ -556,11 +557,18 @@ int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
 }
 int launch_token_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t s) {
   const int64_t nvec = (int64_t)a.V * (a.dtype == MOE_DTYPE_BF16 ? 2 : 4) / 16;
-  const unsigned nb = (unsigned)(nvec <= kLbPart ? 1 : (nvec + kLbPart - 1) / kLbPart);
-  const unsigned gy = a.T < 65535 ? a.T : 65535, gz = (a.T + gy - 1) / gy;
+  // A warp per row where a row is too short for a block (40000 x 2000 BF16: 89
+  // us with blocks, 53 with warps).
+  const bool small = nvec <= 512 && a.T >= 1024;
+  const int rows = small ? (a.T + kLbThreads / 32 - 1) / (kLbThreads / 32) : a.T;
+  const unsigned nb = (unsigned)(small || nvec <= kLbPart ? 1 : (nvec + kLbPart - 1) / kLbPart);
+  const unsigned gy = rows < 65535 ? rows : 65535, gz = (rows + gy - 1) / gy;
   const dim3 grid(nb, gy, gz);
-  if (a.dtype == MOE_DTYPE_BF16) token_logprobs_backward_kernel<uint16_t><<<grid, kLbThreads, 0, s>>>(a);
-  else token_logprobs_backward_kernel<float><<<grid, kLbThreads, 0, s>>>(a);
+  auto f = a.dtype == MOE_DTYPE_BF16 ? (small ? token_logprobs_backward_kernel<uint16_t, 32>
+                                              : token_logprobs_backward_kernel<uint16_t, kLbThreads>)
+                                     : (small ? token_logprobs_backward_kernel<float, 32>
+                                              : token_logprobs_backward_kernel<float, kLbThreads>);
+  f<<<grid, kLbThreads, 0, s>>>(a);
   return 0;
 }
 
