@@ -531,9 +531,11 @@ int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
   // row's end (sums, alternatives) behind other rows: a warp for short rows,
   // four for long ones (BF16, no alternatives: 4000 x 8192 16, 19 and 29 us with
   // 32, 128 and 256 threads; 2000 x 20000 17, 19 and 25; 4000 x 50000 67, 62 and
-  // 73).  Else blocks, and clusters of up to 8 of them while they fill the GPU
+  // 73).  With alternatives L2 should still hold a row at its end: 256 threads
+  // from 160 KB on (4096 x 131072 with 20: 247 us with 128, 191 with 256; 8000 x
+  // 65536: 212 and 218).  Else blocks, and clusters of up to 8 of them while they fill the GPU
   // and each thread keeps two vectors (2 x 131072: 18 us with one, 14 with 8).
-  const int th = (nvec <= 1024 && (a.T >= 304 || nvec <= 128)) || (nvec <= 3072 && a.T >= 1000) ? 32 : a.T >= 304 ? 128 : kLpThreads;
+  const int th = (nvec <= 1024 && (a.T >= 304 || nvec <= 128)) || (nvec <= 3072 && a.T >= 1000) ? 32 : a.T >= 304 && !(top && nvec > 10240) ? 128 : kLpThreads;
   int nb = 1;
   if (th == kLpThreads)
     while (nb < 8 && (int64_t)a.T * nb * 2 <= most && nvec / (nb * 2) >= 2 * kLpThreads) nb *= 2;
