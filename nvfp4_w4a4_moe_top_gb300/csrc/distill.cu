@@ -100,7 +100,7 @@ __device__ __forceinline__ uint32_t listed_bits(const uint32_t* bits, int i, flo
 // With both, the stream brings each part twice; the second time it comes from
 // L2, which holds the rows that the resident blocks work on.
 template <typename E, bool SUMS, bool GRAD, int TH>
-__global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(DistillArgs a) {
+__global__ void __launch_bounds__(TH, TH == 32 ? 24 : kDsMaxThreads / TH) distill_kernel(DistillArgs a) {
   constexpr int N = Row<E>::kVec, NW = TH / 32;
   extern __shared__ uint4 ring[];
   __shared__ DsList list;
@@ -173,27 +173,26 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
         }
       }
       if (k == 0) dup = 0;
+      __syncthreads();
     }
     auto listed = [&](int i) { return (bits[bit_of(i) >> 5] >> (bit_of(i) & 31) & 1u) != 0u; };
     const int edge = k < r.head ? k : r.tail_start() + k - r.head;  // this thread's element outside the vectors
     const bool has_edge = rank == 0 && k < r.head + r.tail;
-    // By one warp, from the maxima and ln-sums of the row (m, l) and of its part
-    // off the list (mt, lt): the gradient on the list, and off it coef[0] times
-    // 2^(x c - shift), or 2^((x - shift) c) with `diff`.
-    auto gradient = [&](const Teacher& T, float m, float l, float mt, float lt, float rescale, float shift) {
-      const float g = g_row * a.inv_t;
-      for (int j = lane; j < a.K; j += 32) {
-        const float lp = (list.x[j] - m) * a.inv_t - l;
-        list.a[j] = m == neg_inf() ? 0.0f : g * (expf(lp) * T.Q - teacher_q(T, list, j, a.inv_t));
-      }
+    // One warp works on the list: the teacher's side now, the row's statistics
+    // (maximum and ln-sum of the row, m, l, and off the list, mt, lt) where the
+    // sums end, and the loss and the gradient on the list beside the gradient
+    // off it, which is coef[0] times 2^(x c - coef[1]), or 2^((x - coef[1]) c)
+    // with `diff`.
+    Teacher T;
+    float m = 0.0f, l = 0.0f, mt = 0.0f, lt = 0.0f;
+    if (k < 32)
+      T = teacher_side(list, a.K, a.inv_t, a.teacher_lse != nullptr, lse_row, rank == 0 ? a.status : nullptr);
+    auto weights = [&](float rescale, float shift) {
+      const float ls = (mt - m) * a.inv_t + lt - l;  // ln of the mass off the list
       if (lane == 0) {
-        const float ls = (mt - m) * a.inv_t + lt - l;  // ln of the mass off the list
-        coef[0] = mt == neg_inf() ? 0.0f : g * (expf(ls) * T.Q - T.r) * rescale;
+        coef[0] = mt == neg_inf() ? 0.0f : g_row * a.inv_t * (expf(ls) * T.Q - T.r) * rescale;
         coef[1] = shift;
       }
-    };
-    auto teacher = [&]() {
-      return teacher_side(list, a.K, a.inv_t, a.teacher_lse != nullptr, lse_row, rank == 0 ? a.status : nullptr);
     };
     if (SUMS) {
       Run<false> acc;
@@ -220,12 +219,11 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
       acc.template warp_merge<32>();
       if (lane == 0) red[k >> 5] = acc;
       __syncthreads();
-      // By one warp, from the part off the list: the row's statistics, the loss
-      // and the gradient.
-      auto finish = [&](float mt, float lt, float rescale, float shift) {
+      // from the part off the list
+      auto finish = [&](float mt_, float lt_, float rescale, float shift) {
+        mt = mt_, lt = lt_;
         const bool empty = mt == neg_inf();
-        const Teacher T = teacher();
-        float m = empty ? kLowest : mt;
+        m = empty ? kLowest : mt;
         bool any = !empty;
         for (int j = lane; j < a.K; j += 32)
           if (list.id[j] >= 0) {
@@ -239,25 +237,11 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
           if (list.id[j] >= 0) s += exp2_fast((list.x[j] - m) * c);
         s = warp_sum(s);
         if (!empty) s += exp2_fast((mt - m) * c) * expf(lt);
-        const bool bad = !(m <= 3.402823466e+38f), none = !any;
-        float l = logf(s);
-        if (none) m = neg_inf(), l = 0.0f;
+        l = logf(s);
+        const bool bad = !(m <= 3.402823466e+38f);
+        if (!any) m = neg_inf(), l = 0.0f;
         if (bad) m = l = mt = lt = quiet_nan();
-        float part = 0.0f;
-        for (int j = lane; j < a.K; j += 32) {
-          const float q = teacher_q(T, list, j, a.inv_t), lp = (list.x[j] - m) * a.inv_t - l;
-          if (list.id[j] >= 0 && !(q == 0.0f)) part += none ? -neg_inf() : q * (T.lq(list.a[j], a.inv_t) - lp);
-        }
-        part = warp_sum(part);
-        const float ls = empty ? neg_inf() : (mt - m) * a.inv_t + lt - l;
-        if (!(T.r == 0.0f)) part += none ? -neg_inf() : T.r * (logf(T.r) - ls);
-        if (bad || T.Q != T.Q) part = quiet_nan();
-        if (GRAD) gradient(T, m, l, mt, lt, rescale, shift);
-        if (lane == 0 && rank == 0) {
-          if (bad) set_status(a.status, MOE_STATUS_NONFINITE_LOGITS);
-          a.loss[t] = part;
-          if (a.stats_out) *reinterpret_cast<float4*>(a.stats_out + 4 * t) = make_float4(m, l, mt, lt);
-        }
+        if (GRAD) weights(rescale, shift);
       };
       if (k < 32) {
         acc = Run<false>();
@@ -313,12 +297,32 @@ __global__ void __launch_bounds__(TH, kDsMaxThreads / TH) distill_kernel(Distill
       }
     } else {
       if (k < a.K) list.x[k] = xs;
-      __syncthreads();
       if (k < 32) {
+        m = st.x, l = st.y, mt = st.z, lt = st.w;
         if (lane == 0) diff = true;
-        gradient(teacher(), st.x, st.y, st.z, st.w, expf(-st.w), st.z);
+        weights(expf(-lt), mt);
       }
       __syncthreads();
+    }
+    if (k < 32) {
+      const bool none = m == neg_inf(), bad = m != m;
+      float part = 0.0f;
+      for (int j = lane; j < a.K; j += 32) {
+        const float q = teacher_q(T, list, j, a.inv_t), lp = (list.x[j] - m) * a.inv_t - l;
+        if (SUMS && list.id[j] >= 0 && !(q == 0.0f)) part += none ? -neg_inf() : q * (T.lq(list.a[j], a.inv_t) - lp);
+        if (GRAD) list.a[j] = none ? 0.0f : g_row * a.inv_t * (expf(lp) * T.Q - q);
+      }
+      if (SUMS) {
+        part = warp_sum(part);
+        const float ls = mt == neg_inf() ? neg_inf() : (mt - m) * a.inv_t + lt - l;
+        if (!(T.r == 0.0f)) part += none ? -neg_inf() : T.r * (logf(T.r) - ls);
+        if (bad || T.Q != T.Q) part = quiet_nan();
+        if (lane == 0 && rank == 0) {
+          if (bad) set_status(a.status, MOE_STATUS_NONFINITE_LOGITS);
+          a.loss[t] = part;
+          if (a.stats_out) *reinterpret_cast<float4*>(a.stats_out + 4 * t) = make_float4(m, l, mt, lt);
+        }
+      }
     }
     // the bits of this row go; the next row's entry comes
     const int64_t tn = t + step;
