@@ -69,8 +69,9 @@ size_t moe_mx8_sf_bytes(int64_t rows, int d);
  *   rstd  f32 [T] (out), or NULL
  * Needs d % 16 == 0 (y8: d % 128 == 0), 16 <= d <= 16384, ldx, ldr >= d and
  * multiples of 8, eps >= 0 finite.  Non-finite values of h set
- * MOE_STATUS_NONFINITE_X (the row's outputs are then unspecified).  One
- * launch. */
+ * MOE_STATUS_NONFINITE_X (the row's outputs are then unspecified).  The sum of
+ * squares is FP32: rows whose sum exceeds its range (|h| about 1e18 and more)
+ * give y = 0, and a row of zeros with eps = 0 gives NaN.  One launch. */
 int moe_add_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* res,
                     int64_t ldr, const uint16_t* w, float eps, int T, int d,
                     uint16_t* h, uint16_t* y, uint8_t* y8, uint8_t* y8_sf,
@@ -101,7 +102,7 @@ int moe_add_rmsnorm_backward(const uint16_t* dy, const uint16_t* dh,
 /* A logit of -inf (a masked id) has p = 0 and enters no sum.  A row of      */
 /* nothing but -inf has no distribution: see each entry point.  A row with a */
 /* NaN or +inf gives NaN and sets MOE_STATUS_NONFINITE_LOGITS.               */
-/* Needs 1 <= V, ld >= V, 1e-6 <= inv_temperature <= 1e6.                    */
+/* Needs 1 <= V <= 2^30, ld >= V, 1e-6 <= inv_temperature <= 1e6.            */
 /* ---------------------------------------------------------------------- */
 
 /* Log-probabilities of given tokens, entropy and top alternatives, in one

@@ -328,6 +328,10 @@ def _dt():
     return _types
 
 
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
 def _stream(stream):
     return _types.raw_stream(_types.device()) if stream is None else stream.cuda_stream
 
@@ -356,7 +360,7 @@ def moe_add_rmsnorm(x, res, w, eps, h, y, y8=None, y8_sf=None, rstd=None, status
     _check("moe_add_rmsnorm", lib().moe_add_rmsnorm(
         px, ldx, pr, ldr, _tensor(w, b16, (d,), "w"), eps, T, d, _tensor(h, b16, shape, "h"),
         _tensor(y, b16, shape, "y"), _tensor(y8, ty.codes, shape, "y8"),
-        None if y8_sf is None else y8_sf.data_ptr(), _tensor(rstd, ty.f32, (T,), "rstd"), None if status is None else status.data_ptr(),
+        _opt(y8_sf), _tensor(rstd, ty.f32, (T,), "rstd"), _opt(status),
         _stream(stream)))
 
 
@@ -372,8 +376,8 @@ def moe_add_rmsnorm_backward(dy, dh, h, rstd, w, dx, dw, ws, status=None, stream
     _check("moe_add_rmsnorm_backward", lib().moe_add_rmsnorm_backward(
         _tensor(dy, b16, shape, "dy"), _tensor(dh, b16, shape, "dh"), _tensor(h, b16, shape, "h"),
         _tensor(rstd, ty.f32, (T,), "rstd"), _tensor(w, b16, (d,), "w"), T, d, _tensor(dx, b16, shape, "dx"),
-        _tensor(dw, ty.f32, (d,), "dw"), None if ws is None else ws.data_ptr(),
-        0 if ws is None else ws.numel() * ws.element_size(), None if status is None else status.data_ptr(), _stream(stream)))
+        _tensor(dw, ty.f32, (d,), "dw"), _opt(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _opt(status), _stream(stream)))
 
 
 def moe_token_logprobs(logits, targets, inv_temperature, n_top, logprob, entropy, stats, top_ids=None,
@@ -389,7 +393,7 @@ def moe_token_logprobs(logits, targets, inv_temperature, n_top, logprob, entropy
         pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty.i32, (T,), "targets"), inv_temperature,
         n_top, _tensor(logprob, f32, (T,), "logprob"), _tensor(entropy, f32, (T,), "entropy"),
         _tensor(stats, f32, (T, 2), "stats"), _tensor(top_ids, ty.i32, (T, n_top), "top_ids"),
-        _tensor(top_logprob, f32, (T, n_top), "top_logprob"), None if status is None else status.data_ptr(), _stream(stream)))
+        _tensor(top_logprob, f32, (T, n_top), "top_logprob"), _opt(status), _stream(stream)))
 
 
 def moe_token_logprobs_backward(logits, targets, inv_temperature, stats, entropy, g_logprob, g_entropy, dlogits,
@@ -404,7 +408,7 @@ def moe_token_logprobs_backward(logits, targets, inv_temperature, stats, entropy
     _check("moe_token_logprobs_backward", lib().moe_token_logprobs_backward(
         pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty.i32, (T,), "targets"), inv_temperature,
         _tensor(stats, f32, (T, 2), "stats"), _tensor(entropy, f32, (T,), "entropy"),
-        _tensor(g_logprob, f32, (T,), "g_logprob"), _tensor(g_entropy, f32, (T,), "g_entropy"), pd, ldd, None if status is None else status.data_ptr(),
+        _tensor(g_logprob, f32, (T,), "g_logprob"), _tensor(g_entropy, f32, (T,), "g_entropy"), pd, ldd, _opt(status),
         _stream(stream)))
 
 
@@ -429,7 +433,7 @@ def moe_distill_topk(logits, teacher_ids, teacher_logits, teacher_lse, inv_tempe
     T = logits.shape[0]
     a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
     _check("moe_distill_topk", lib().moe_distill_topk(
-        *a, _tensor(loss, ty.f32, (T,), "loss"), _tensor(stats, ty.f32, (T, 4), "stats"), None if status is None else status.data_ptr(),
+        *a, _tensor(loss, ty.f32, (T,), "loss"), _tensor(stats, ty.f32, (T, 4), "stats"), _opt(status),
         _stream(stream)))
 
 
@@ -442,7 +446,7 @@ def moe_distill_topk_backward(logits, teacher_ids, teacher_logits, teacher_lse, 
     a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
     pd, ldd = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
     _check("moe_distill_topk_backward", lib().moe_distill_topk_backward(
-        *a, _tensor(stats, ty.f32, (T, 4), "stats"), _tensor(g, ty.f32, (T,), "g"), pd, ldd, None if status is None else status.data_ptr(),
+        *a, _tensor(stats, ty.f32, (T, 4), "stats"), _tensor(g, ty.f32, (T,), "g"), pd, ldd, _opt(status),
         _stream(stream)))
 
 
@@ -455,7 +459,7 @@ def moe_distill_topk_train(logits, teacher_ids, teacher_logits, teacher_lse, inv
     a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
     pd, ldd = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
     _check("moe_distill_topk_train", lib().moe_distill_topk_train(
-        *a, _tensor(g, ty.f32, (T,), "g"), _tensor(loss, ty.f32, (T,), "loss"), pd, ldd, None if status is None else status.data_ptr(),
+        *a, _tensor(g, ty.f32, (T,), "g"), _tensor(loss, ty.f32, (T,), "loss"), pd, ldd, _opt(status),
         _stream(stream)))
 
 

@@ -1,4 +1,10 @@
-// Distillation from a teacher's top logits: loss and gradient.
+// Distillation from a teacher's top logits: loss and gradient.  With the
+// teacher's q over a list of ids and r off it, the student's p and s = sum of p
+// off the list:
+//   loss = sum q (ln q - ln p) + r (ln r - ln s)
+//   d loss / dz = p - q on the list, p - r p / s off it.
+// p / s = e^(z - lse of the part off the list), so neither s nor the quotient
+// comes from a difference, and both keep their precision when s is small.
 #include "learner.cuh"
 
 namespace moe {
@@ -98,7 +104,14 @@ __device__ __forceinline__ uint32_t listed_bits(const uint32_t* bits, int i, flo
 // stored statistics.  A bit per id marks the listed ones, whose elements leave
 // the stream of the sums, so that the mass off the list is summed by itself.
 // With both, the stream brings each part twice; the second time it comes from
-// L2, which holds the rows that the resident blocks work on.
+// L2, which holds the rows that the resident blocks work on (first pass with
+// the evict-last policy, second with evict-first: 454 -> 372 us).
+// 4096 x 131072 BF16, 64 listed: loss 155 us (1.0 of the measured copy rate),
+// gradient 328 (0.96), both 371 (0.85 of one read and one write; DRAM moves just
+// those, and no exponentials in the second pass change nothing: the third trip
+// between L2 and the SMs is what it waits for).  Parts kept in shared memory
+// between the passes, in clusters of 2 to 8, took 650 to 1120 us: with one row
+// per SM nothing is fetched while a row's sums meet.
 template <typename E, bool SUMS, bool GRAD, int TH>
 __global__ void __launch_bounds__(TH, TH == 32 ? 24 : kDsMaxThreads / TH) distill_kernel(DistillArgs a) {
   constexpr int N = Row<E>::kVec, NW = TH / 32;
@@ -110,7 +123,8 @@ __global__ void __launch_bounds__(TH, TH == 32 ? 24 : kDsMaxThreads / TH) distil
   __shared__ float coef[2];
   __shared__ bool diff;
   __shared__ int dup;
-  const int nb = gridDim.x, lg = 31 - __clz(nb), rank = blockIdx.x, k = threadIdx.x, lane = k & 31;  // nb: a power of two
+  const int nb = gridDim.x, lg = 31 - __clz(nb), rank = blockIdx.x;  // nb: a power of two
+  const int k = threadIdx.x, lane = k & 31;
   const int64_t t0 = blockIdx.y, step = gridDim.y;
   const float c = a.inv_t * kLog2e;
   const E* logits = static_cast<const E*>(a.logits);
@@ -432,7 +446,9 @@ static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = sums && nb > 1 ? 1 : 0;
-  auto f = sums ? (grad ? distill_of<E, true, true>(th) : distill_of<E, true, false>(th)) : distill_of<E, false, true>(th);
+  auto f = !sums  ? distill_of<E, false, true>(th)
+           : grad ? distill_of<E, true, true>(th)
+                  : distill_of<E, true, false>(th);
   if (!allow_smem((const void*)f, smem)) return -1;
   return cudaLaunchKernelEx(&cfg, f, a) == cudaSuccess ? 0 : -1;
 }

@@ -27,7 +27,7 @@ bool norm_shape(int T, int d) { return T >= 0 && d >= 16 && d <= 16384 && d % 16
 // T, V, row strides, type and temperature of a logits call.
 bool logits_shape(int dtype, int64_t ld, int T, int V, float inv_t) {
   if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32) return false;
-  if (T < 0 || V < 1 || !rows_ok(ld, T, V)) return false;
+  if (T < 0 || V < 1 || V > (1 << 30) || !rows_ok(ld, T, V)) return false;
   return inv_t >= 1e-6f && inv_t <= 1e6f;  // false for NaN
 }
 uintptr_t esize(int dtype) { return dtype == MOE_DTYPE_BF16 ? 2 : 4; }
@@ -36,8 +36,8 @@ int distill(const void* logits, int dtype, int64_t ld, int T, int V, const int32
             const float* teacher_logits, const float* teacher_lse, int K, float inv_temperature, float* loss,
             float* stats_out, const float* stats, const float* g, void* dlogits, int64_t ldd, int* status,
             void* stream) {
-  moe::DistillArgs a = {logits, dtype,     ld,    T, V,       teacher_ids, teacher_logits, teacher_lse, K, inv_temperature,
-                        loss,   stats_out, stats, g, dlogits, ldd,         status};
+  moe::DistillArgs a = {logits,          dtype, ld,        T,     V, teacher_ids, teacher_logits, teacher_lse, K,
+                        inv_temperature, loss,  stats_out, stats, g, dlogits,     ldd,            status};
   const int rc = moe::check_device();
   if (rc != MOE_OK) return rc;
   if (T == 0) return MOE_OK;
@@ -66,8 +66,8 @@ size_t moe_mx8_sf_bytes(int64_t rows, int d) {
 int moe_add_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* res, int64_t ldr, const uint16_t* w, float eps,
                     int T, int d, uint16_t* h, uint16_t* y, uint8_t* y8, uint8_t* y8_sf, float* rstd, int* status,
                     void* stream) {
-  if (!norm_shape(T, d) || !rows_ok(ldx, T, d) || ldx % 8 != 0 || (res && (!rows_ok(ldr, T, d) || ldr % 8 != 0)) || !(eps >= 0.0f) ||
-      !(eps <= 1e30f) || (y8 && d % 128 != 0))
+  if (!norm_shape(T, d) || !rows_ok(ldx, T, d) || ldx % 8 != 0 || (res && (!rows_ok(ldr, T, d) || ldr % 8 != 0)) ||
+      !(eps >= 0.0f) || !(eps <= 1e30f) || (y8 && d % 128 != 0))
     return MOE_ERR_SHAPE;
   if (!opt(res, 16) || !opt(h, 16) || !opt(y, 16) || !opt(y8, 16) || !opt(y8_sf, 16) || !opt(rstd, 4) ||
       !opt(status, 4) || (y8 == nullptr) != (y8_sf == nullptr))

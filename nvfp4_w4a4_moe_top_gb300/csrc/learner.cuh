@@ -129,11 +129,6 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 }
 
 // ---- thread-block clusters: a row's blocks exchange their parts ----
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // The 4 bytes at shared address p of block `rank` of the cluster.
@@ -273,18 +268,6 @@ struct Soft {
       }
     }
   }
-  // Merged over the block's NW warps; every thread gets the result.
-  template <int NW>
-  __device__ __forceinline__ void block_merge(float c, Soft* red) {
-    warp_merge(c);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = *this;
-    __syncthreads();
-    Soft b;
-    if ((threadIdx.x & 31) < NW) b = red[threadIdx.x & 31];
-    b.warp_merge(c);
-    *this = b;
-    __syncthreads();
-  }
 };
 
 // Softmax statistics of a stream of logits, in base 2 about an integer shift:
@@ -381,17 +364,9 @@ struct Run {
     take(s2, e2);
     return top;
   }
-  __device__ __forceinline__ void merge(const Run& o) {
-    const float nM = fmaxf(M, o.M);
-    Run b = o;
-    shift(nM);
-    b.shift(nM);
-    m = max_nan(m, o.m);
-    s += b.s;
-    e += b.e;
-  }
-  // Merged over the first 2^k lanes' parts (k from N), every lane gets it:
-  // the largest shift first, so that each part is scaled once.
+  // Merged over lanes 0 .. N - 1, N a power of two (the other lanes' parts are
+  // empty): the largest shift first, so that each part is scaled once.  Every
+  // lane gets m and M, lanes 0 .. N - 1 the sums.
   template <int N>
   __device__ __forceinline__ void warp_merge() {
     const int top = __reduce_max_sync(0xFFFFFFFFu, (int)M);
@@ -501,20 +476,6 @@ struct Stream {
   }
 };
 
-// Sum over the block's NW warps in a fixed order; every thread gets it.
-template <int NW>
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = (threadIdx.x & 31) < NW ? red[threadIdx.x & 31] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  __syncthreads();
-  return v;
-}
-
 // ---- lists of 32 keys held by a warp, lane i the i-th largest ----
 template <typename K>
 __device__ __forceinline__ K order_step(K v, int j, bool desc) {
@@ -537,17 +498,4 @@ __device__ __forceinline__ K list_merge(K a, K b) {
   for (int j = 16; j > 0; j >>= 1) v = order_step(v, j, true);
   return v;
 }
-// The 32 largest of the lists of the block's NW warps; warp 0 gets it.
-template <int NW, typename K>
-__device__ __forceinline__ K block_list_merge(K v, K (*lists)[32]) {
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int n = NW / 2; n > 0; n >>= 1) {
-    if (w >= n && w < 2 * n) lists[w][lane] = v;
-    __syncthreads();
-    if (w < n) v = list_merge(v, lists[w + n][lane]);
-  }
-  return v;
-}
-
 }  // namespace moe

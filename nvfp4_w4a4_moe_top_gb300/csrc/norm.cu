@@ -1,5 +1,10 @@
 // Residual add + RMS norm with BF16 and block-scaled 8-bit outputs, and its
-// gradient.
+// gradient.  Both are bound by HBM: about ten operations per element against
+// eight bytes.
+//   forward   h = x + res, r = 1 / sqrt(mean h^2 + eps), y = h r w
+//   backward  n = h r, a = dy w: dx = r (a - n mean(a n)) + dh, dw = sum dy n
+// Sums are FP32; h is rounded to BF16 first, as the residual stream and the
+// gradient read it, and every output is rounded once.
 #include "learner.cuh"
 
 namespace moe {
@@ -48,8 +53,12 @@ struct Chunk {
 
 // TPR threads per row, each with up to NV chunks of 16 values, c = k, k + TPR,
 // ..; h stays in registers (as BF16) between the sum of squares and the
-// outputs, so x and res are read once.  Two lanes share a block of 32 values of
-// the 8-bit output, eight a word of four scale bytes.
+// outputs, so x and res are read once.  A warp per row needs no barrier; more
+// threads per row where rows are few or long.  Two lanes share a block of 32
+// values of the 8-bit output, eight a word of four scale bytes, so codes leave
+// in 16-byte and scales in 4-byte stores.
+// 65536 x 2048: 159 us, 6.75 TB/s, 0.99 of the measured copy rate; 16384 x 2048
+// with the 8-bit output 48 us, 6.4 TB/s, 0.94.
 template <int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rmsnorm_kernel(NormArgs a) {
   constexpr int kThreads = TPR < 128 ? 128 : TPR, kRows = kThreads / TPR, NW = TPR / 32;
@@ -139,7 +148,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rmsnorm_kernel(Norm
       uint32_t q[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        q[i] = e4m3x2_hw(y[4 * i] * inv, y[4 * i + 1] * inv) | (e4m3x2_hw(y[4 * i + 2] * inv, y[4 * i + 3] * inv) << 16);
+        q[i] = e4m3x2_hw(y[4 * i] * inv, y[4 * i + 1] * inv) |
+               (e4m3x2_hw(y[4 * i + 2] * inv, y[4 * i + 3] * inv) << 16);
       uint32_t word = sb << (8 * (c >> 1 & 3));
       word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
       word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
@@ -156,6 +166,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rmsnorm_kernel(Norm
 // groups.  A group takes R rows at a time (one barrier serves R row sums);
 // each thread fetches its own columns of dy, h and dh D groups of
 // rows ahead, by asynchronous copies into shared memory that only it reads.
+// 65536 x 2048: 160 us, 6.7 TB/s, 0.98 of the measured copy rate (four rows of
+// loads in registers and no ring: 194 us, the loads waited out at each barrier).
 // GROUPS false: one group.
 template <int NV, int R, int D, bool GROUPS>
 __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a, int nt) {
@@ -302,7 +314,8 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a
 
 // dw from the blocks' parts: 32 columns per block, the parts in 32 slices that
 // meet in shared memory; always the same order.
-__global__ void __launch_bounds__(1024) add_rmsnorm_dw_kernel(const float* __restrict__ part, int nb, int d, float* dw) {
+__global__ void __launch_bounds__(1024) add_rmsnorm_dw_kernel(const float* __restrict__ part, int nb, int d,
+                                                              float* dw) {
   __shared__ float sh[32][33];
   const int i = blockIdx.x * 32 + threadIdx.x;
   // launched while the parts are still being made; they are complete after this

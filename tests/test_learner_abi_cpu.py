@@ -75,7 +75,8 @@ def test_add_rmsnorm_backward_refusals(L):
 
 
 LOGITS = dict(logits=FAKE, dtype=0, ld=1000, T=4, V=1000)
-BAD_LOGITS = [dict(dtype=2), dict(dtype=-1), dict(ld=999), dict(V=0), dict(T=-1), dict(ld=1 << 45), dict(inv_t=0.0),
+BAD_LOGITS = [dict(dtype=2), dict(dtype=-1), dict(ld=999), dict(V=0), dict(T=-1), dict(ld=1 << 45),
+              dict(V=(1 << 30) + 1, ld=1 << 31), dict(inv_t=0.0),
               dict(inv_t=-1.0), dict(inv_t=NAN), dict(inv_t=INF), dict(inv_t=1e7)]
 
 
