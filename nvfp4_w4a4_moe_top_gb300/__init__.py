@@ -290,13 +290,15 @@ def _tensor(t, dtypes, shape, what):
 
 
 def _rows(t, dtypes, shape, what):
-    """Pointer and row stride of a 2-D device tensor whose rows are contiguous."""
-    if t.dim() != 2 or (shape is not None and t.shape != shape) or t.dtype not in dtypes or not t.is_cuda or \
-            (t.stride(1) != 1 and t.shape[1] > 1):
+    """Pointer, row stride and shape of a 2-D device tensor whose rows are
+    contiguous."""
+    own, st = t.shape, t.stride()
+    if len(own) != 2 or (shape is not None and own != shape) or t.dtype not in dtypes or not t.is_cuda or \
+            (st[1] != 1 and own[1] > 1):
         raise ValueError("%s: a 2-D CUDA tensor%s of %s with contiguous rows expected, got %s of %s, strides %s"
                          % (what, "" if shape is None else " %s" % (tuple(shape),), " or ".join(map(str, dtypes)),
-                            tuple(t.shape), t.dtype, t.stride()))
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+                            tuple(own), t.dtype, st))
+    return t.data_ptr(), (st[0] if own[0] > 1 else own[1]), own
 
 
 class _Types:
@@ -350,10 +352,9 @@ def moe_add_rmsnorm(x, res, w, eps, h, y, y8=None, y8_sf=None, rstd=None, status
     res [T][d] may have strided rows."""
     ty = _dt()
     b16 = ty.b16
-    px, ldx = _rows(x, b16, None, "x")
-    shape = x.shape
+    px, ldx, shape = _rows(x, b16, None, "x")
     T, d = shape
-    pr, ldr = (None, d) if res is None else _rows(res, b16, shape, "res")
+    pr, ldr, _ = (None, d, None) if res is None else _rows(res, b16, shape, "res")
     if y8_sf is not None and (not y8_sf.is_contiguous() or y8_sf.dtype not in ty.scales or not y8_sf.is_cuda
                               or y8_sf.numel() < (T + 127) // 128 * (d // 128) * 512):
         raise ValueError("y8_sf: at least %d contiguous scale bytes on the GPU expected" % mx8_sf_bytes(T, d))
@@ -387,8 +388,8 @@ def moe_token_logprobs(logits, targets, inv_temperature, n_top, logprob, entropy
     allowed).  Outputs that are None are left out."""
     ty = _dt()
     f32 = ty.f32
-    pl, ld = _rows(logits, ty.logits, None, "logits")
-    T, V = logits.shape
+    pl, ld, shape = _rows(logits, ty.logits, None, "logits")
+    T, V = shape
     _check("moe_token_logprobs", lib().moe_token_logprobs(
         pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty.i32, (T,), "targets"), inv_temperature,
         n_top, _tensor(logprob, f32, (T,), "logprob"), _tensor(entropy, f32, (T,), "entropy"),
@@ -402,9 +403,9 @@ def moe_token_logprobs_backward(logits, targets, inv_temperature, stats, entropy
     be the logits themselves."""
     ty = _dt()
     f32 = ty.f32
-    pl, ld = _rows(logits, ty.logits, None, "logits")
-    T, V = logits.shape
-    pd, ldd = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
+    pl, ld, shape = _rows(logits, ty.logits, None, "logits")
+    T, V = shape
+    pd, ldd, _ = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
     _check("moe_token_logprobs_backward", lib().moe_token_logprobs_backward(
         pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty.i32, (T,), "targets"), inv_temperature,
         _tensor(stats, f32, (T, 2), "stats"), _tensor(entropy, f32, (T,), "entropy"),
@@ -413,8 +414,8 @@ def moe_token_logprobs_backward(logits, targets, inv_temperature, stats, entropy
 
 
 def _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature):
-    pl, ld = _rows(logits, ty.logits, None, "logits")
-    T, V = logits.shape
+    pl, ld, shape = _rows(logits, ty.logits, None, "logits")
+    T, V = shape
     if teacher_ids.dim() != 2:
         raise ValueError("teacher_ids: a 2-D tensor expected, got %s" % (tuple(teacher_ids.shape),))
     K = teacher_ids.shape[1]
@@ -444,7 +445,7 @@ def moe_distill_topk_backward(logits, teacher_ids, teacher_logits, teacher_lse, 
     ty = _dt()
     T = logits.shape[0]
     a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
-    pd, ldd = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
+    pd, ldd, _ = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
     _check("moe_distill_topk_backward", lib().moe_distill_topk_backward(
         *a, _tensor(stats, ty.f32, (T, 4), "stats"), _tensor(g, ty.f32, (T,), "g"), pd, ldd, _opt(status),
         _stream(stream)))
@@ -457,7 +458,7 @@ def moe_distill_topk_train(logits, teacher_ids, teacher_logits, teacher_lse, inv
     ty = _dt()
     T = logits.shape[0]
     a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
-    pd, ldd = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
+    pd, ldd, _ = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
     _check("moe_distill_topk_train", lib().moe_distill_topk_train(
         *a, _tensor(g, ty.f32, (T,), "g"), _tensor(loss, ty.f32, (T,), "loss"), pd, ldd, _opt(status),
         _stream(stream)))
