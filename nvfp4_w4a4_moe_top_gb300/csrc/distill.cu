@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(TH, TH == 32 ? 24 : kDsMaxThreads / TH) distil
   const float c = a.inv_t * kLog2e;
   const E* logits = static_cast<const E*>(a.logits);
   uint32_t* bits = reinterpret_cast<uint32_t*>(ring + TH * kDsU * kDsD);
+  begin_kernel();
   for (int i = k; i < (a.V + 2 * N + 31) / 32; i += TH) bits[i] = 0u;
   if (k == 0) dup = 0;
   auto part = [&](int64_t t) {
@@ -435,22 +436,11 @@ static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
   if (fit > kDsMaxThreads / th) fit = kDsMaxThreads / th;
   if (fit < 1) fit = 1;
   const int64_t grid = (int64_t)sms * fit / nb * kDsTurns;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(nb, (unsigned)(a.T < grid ? a.T : grid));
-  cfg.blockDim = dim3(th);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = nb;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = sums && nb > 1 ? 1 : 0;
   auto f = !sums  ? distill_of<E, false, true>(th)
            : grad ? distill_of<E, true, true>(th)
                   : distill_of<E, true, false>(th);
   if (!allow_smem((const void*)f, smem)) return -1;
-  return cudaLaunchKernelEx(&cfg, f, a) == cudaSuccess ? 0 : -1;
+  return launch_kernel(f, dim3(nb, (unsigned)(a.T < grid ? a.T : grid)), th, smem, sums ? nb : 1, s, a);
 }
 int launch_distill(const DistillArgs& a, cudaStream_t s) {
   return a.dtype == MOE_DTYPE_BF16 ? launch_distill_of<uint16_t>(a, s) : launch_distill_of<float>(a, s);

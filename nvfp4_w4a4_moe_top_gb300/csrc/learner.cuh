@@ -95,6 +95,34 @@ int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s);
 int launch_token_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t s);
 int launch_distill(const DistillArgs& a, cudaStream_t s);
 
+// A launch whose grid may be set up while the stream's kernel before it ends
+// (kernels begin with begin_kernel), in clusters of `cluster` blocks along x.
+template <typename... P, typename... A>
+int launch_kernel(void (*f)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, f, P(args)...) == cudaSuccess ? 0 : -1;
+}
+// First in every kernel, before any access to global memory: lets the next
+// launch be set up once all of this grid runs, and waits until what the stream
+// ran before is complete and visible.  Small calls in a row save most of a
+// launch's latency.
+__device__ __forceinline__ void begin_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 constexpr float kLowest = -3.402823466e+38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 

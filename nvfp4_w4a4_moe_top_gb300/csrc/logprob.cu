@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_ker
   const int lg = TH < kLpThreads ? 0 : 31 - __clz(nb);  // nb is a power of two
   const int group = threadIdx.x / TH, k = threadIdx.x & (TH - 1), lane = threadIdx.x & 31;
   TopShared<TH>& top = tops[TOP ? group : 0];
+  begin_kernel();
   const int64_t t0 = (int64_t)blockIdx.y * NG + group, step = (int64_t)gridDim.y * NG;
   const float c = a.inv_t * kLog2e;
   const E* logits = static_cast<const E*>(a.logits);
@@ -458,6 +459,7 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_backward_kernel(Log
   constexpr int N = Row<E>::kVec;
   const int tid = threadIdx.x % TH;
   const int64_t t = (blockIdx.y + (int64_t)blockIdx.z * gridDim.y) * (kLbThreads / TH) + threadIdx.x / TH;
+  begin_kernel();
   if (t >= a.T) return;
   const E* row = static_cast<const E*>(a.logits) + t * a.ld;
   E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
@@ -554,20 +556,9 @@ int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
   const int64_t per = kLpThreads / th, want = (a.T + per - 1) / per;
   const int64_t grid = nb > 1 ? most / nb : (int64_t)most * kLpTurns;
   const int smem = top ? kLpSmem<true> : kLpSmem<false>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(nb, (unsigned)(want < grid ? want : grid));
-  cfg.blockDim = dim3(kLpThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = nb;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = nb > 1 ? 1 : 0;
   auto f = bf ? token_logprobs_of<uint16_t>(th, ent, top) : token_logprobs_of<float>(th, ent, top);
   if (!allow_smem((const void*)f, smem)) return -1;
-  return cudaLaunchKernelEx(&cfg, f, a) == cudaSuccess ? 0 : -1;
+  return launch_kernel(f, dim3(nb, (unsigned)(want < grid ? want : grid)), kLpThreads, smem, nb, s, a);
 }
 int launch_token_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t s) {
   const int64_t nvec = (int64_t)a.V * (a.dtype == MOE_DTYPE_BF16 ? 2 : 4) / 16;
@@ -577,13 +568,11 @@ int launch_token_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t s) {
   const int rows = small ? (a.T + kLbThreads / 32 - 1) / (kLbThreads / 32) : a.T;
   const unsigned nb = (unsigned)(small || nvec <= kLbPart ? 1 : (nvec + kLbPart - 1) / kLbPart);
   const unsigned gy = rows < 65535 ? rows : 65535, gz = (rows + gy - 1) / gy;
-  const dim3 grid(nb, gy, gz);
   auto f = a.dtype == MOE_DTYPE_BF16 ? (small ? token_logprobs_backward_kernel<uint16_t, 32>
                                               : token_logprobs_backward_kernel<uint16_t, kLbThreads>)
                                      : (small ? token_logprobs_backward_kernel<float, 32>
                                               : token_logprobs_backward_kernel<float, kLbThreads>);
-  f<<<grid, kLbThreads, 0, s>>>(a);
-  return 0;
+  return launch_kernel(f, dim3(nb, gy, gz), kLbThreads, 0, 1, s, a);
 }
 
 }  // namespace moe

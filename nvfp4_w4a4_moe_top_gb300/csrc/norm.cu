@@ -63,6 +63,7 @@ template <int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rmsnorm_kernel(NormArgs a) {
   constexpr int kThreads = TPR < 128 ? 128 : TPR, kRows = kThreads / TPR, NW = TPR / 32;
   __shared__ float red[NW];
+  begin_kernel();
   const int k = threadIdx.x % TPR, n = a.d / 16;
   const int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
   if (TPR == 32 && t >= a.T) return;  // whole warps
@@ -173,6 +174,7 @@ template <int NV, int R, int D, bool GROUPS>
 __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a, int nt) {
   extern __shared__ uint4 ring[];  // [D][R][NV][3][blockDim.x]
   __shared__ float red[2][R][16];
+  begin_kernel();
   const int n = a.d / 8, nb = blockDim.x, groups = GROUPS ? nb / nt : 1;
   const int group = GROUPS ? threadIdx.x / nt : 0, k = threadIdx.x - group * nt;
   const int lane = threadIdx.x & 31, nw = nt >> 5, warp0 = group * nw;  // the group's warps
@@ -283,7 +285,6 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a
     fetch(t0 + D * step, g);  // into the slots just read
     g = g + 1 == D ? 0 : g + 1;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sum of the parts may be set up
   if (!a.dw) return;
   // the groups' parts of dw, added in order, make the block's
   if constexpr (GROUPS) {
@@ -317,9 +318,8 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a
 __global__ void __launch_bounds__(1024) add_rmsnorm_dw_kernel(const float* __restrict__ part, int nb, int d,
                                                               float* dw) {
   __shared__ float sh[32][33];
+  begin_kernel();
   const int i = blockIdx.x * 32 + threadIdx.x;
-  // launched while the parts are still being made; they are complete after this
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   float s = 0.0f;
   if (i < d)
 #pragma unroll 8
@@ -334,20 +334,20 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_dw_kernel(const float* __res
 
 // host launchers
 template <int TPR, int NV>
-static void launch_norm(const NormArgs& a, cudaStream_t s) {
+static int launch_norm(const NormArgs& a, cudaStream_t s) {
   constexpr int rows = TPR < 128 ? 128 / TPR : 1;
-  add_rmsnorm_kernel<TPR, NV><<<dim3((unsigned)((a.T + rows - 1) / rows)), TPR < 128 ? 128 : TPR, 0, s>>>(a);
+  return launch_kernel(add_rmsnorm_kernel<TPR, NV>, dim3((unsigned)((a.T + rows - 1) / rows)), TPR < 128 ? 128 : TPR, 0,
+                       1, s, a);
 }
 int launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
   const int n = a.d / 16;  // chunks
-  if (n <= 32) launch_norm<32, 1>(a, s);
-  else if (n <= 64 && a.T >= 1024) launch_norm<32, 2>(a, s);
-  else if (n <= 128 && a.T >= 1024) launch_norm<32, 4>(a, s);
-  else if (n <= 128) launch_norm<128, 1>(a, s);
-  else if (n <= 256) launch_norm<128, 2>(a, s);
-  else if (n <= 512) launch_norm<256, 2>(a, s);
-  else launch_norm<512, 2>(a, s);
-  return 0;
+  if (n <= 32) return launch_norm<32, 1>(a, s);
+  if (n <= 64 && a.T >= 1024) return launch_norm<32, 2>(a, s);
+  if (n <= 128 && a.T >= 1024) return launch_norm<32, 4>(a, s);
+  if (n <= 128) return launch_norm<128, 1>(a, s);
+  if (n <= 256) return launch_norm<128, 2>(a, s);
+  if (n <= 512) return launch_norm<256, 2>(a, s);
+  return launch_norm<512, 2>(a, s);
 }
 
 // The backward's launch for a size: threads per row, groups of threads per
@@ -380,19 +380,10 @@ int launch_add_rmsnorm_backward(const NormBwdArgs& a, cudaStream_t s) {
            : p.depth == 3 ? add_rmsnorm_backward_kernel<1, 2, 3, false>
                           : add_rmsnorm_backward_kernel<1, 2, 2, false>;
   if (!allow_smem((const void*)f, p.smem)) return -1;
-  f<<<dim3((unsigned)p.blocks), p.threads * p.groups, p.smem, s>>>(a, p.threads);
+  if (launch_kernel(f, dim3((unsigned)p.blocks), p.threads * p.groups, p.smem, 1, s, a, p.threads) != 0) return -1;
   if (!a.dw) return 0;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.d + 31) / 32));
-  cfg.blockDim = dim3(32, 32);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its start overlaps the first launch's end
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const float* part = a.part;
-  return cudaLaunchKernelEx(&cfg, add_rmsnorm_dw_kernel, part, p.blocks, a.d, a.dw) == cudaSuccess ? 0 : -1;
+  return launch_kernel(add_rmsnorm_dw_kernel, dim3((unsigned)((a.d + 31) / 32)), dim3(32, 32), 0, 1, s, a.part, p.blocks,
+                       a.d, a.dw);
 }
 
 }  // namespace moe
