@@ -117,7 +117,9 @@ int launch_kernel(void (*f)(P...), dim3 grid, dim3 block, size_t smem, int clust
 // First in every kernel, before any access to global memory: lets the next
 // launch be set up once all of this grid runs, and waits until what the stream
 // ran before is complete and visible.  Small calls in a row save most of a
-// launch's latency.
+// launch's latency.  What the kernels before may have written is then read by
+// plain loads: a load through the read-only path might be moved ahead of the
+// wait.
 __device__ __forceinline__ void begin_kernel() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -126,7 +126,7 @@ __device__ __noinline__ void list_top(const Row<E>& r, int v0, int v1, bool ends
       const bool valid = lane < (v1 - i0 + TH - 1) / TH;
       const int i = i0 + (valid ? lane * TH : 0);
       float x[N];
-      unpack(__ldg(r.vec() + i), x);
+      unpack(r.vec()[i], x);
 #pragma unroll
       for (int e = 0; e < N; ++e) offer(x[e], r.head + i * N + e, valid);
     }
@@ -190,7 +190,7 @@ __device__ __forceinline__ int group_top(const Row<E>& r, int v0, int v1, bool e
       const int i = v0 + (who & 0xFFFF) + ((who >> 16) * run + (q & (run - 1))) * TH;
       if (i < v1) {
         float x[N];
-        unpack(__ldg(r.vec() + i), x);
+        unpack(r.vec()[i], x);
         uint32_t in = 0;
 #pragma unroll
         for (int e = 0; e < N; ++e) in |= (x[e] >= fb ? 1u : 0u) << e;

@@ -29,8 +29,8 @@ struct Chunk {
     b = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
   }
   __device__ __forceinline__ void load_kept(const uint16_t* p) {
-    a = __ldg(reinterpret_cast<const uint4*>(p));
-    b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    a = *reinterpret_cast<const uint4*>(p);
+    b = reinterpret_cast<const uint4*>(p)[1];
   }
   __device__ __forceinline__ void store(uint16_t* p) const {
     __stcs(reinterpret_cast<uint4*>(p), a);
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = k + v * nt;
-    const uint4 wv = c < n ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4 wv = c < n ? reinterpret_cast<const uint4*>(a.w)[c] : make_uint4(0u, 0u, 0u, 0u);
     unpack(wv, w[v]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a
   };
   auto rstds = [&](int64_t t0) {
 #pragma unroll
-    for (int q = 0; q < R; ++q) rnext[q] = t0 + q < a.T ? __ldg(a.rstd + t0 + q) : 0.0f;
+    for (int q = 0; q < R; ++q) rnext[q] = t0 + q < a.T ? a.rstd[t0 + q] : 0.0f;
   };
   const int64_t first = ((int64_t)blockIdx.x * groups + group) * R;
 #pragma unroll
