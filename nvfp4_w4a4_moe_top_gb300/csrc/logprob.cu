@@ -38,7 +38,10 @@ __device__ __forceinline__ void group_sync() {
 // threads' maxima reach is a lower bound of the n-th largest logit.  Each
 // thread also keeps the maxima of up to kLpSlots runs of its vectors, so that
 // only the runs that reach the bound (little more than n) are read again, from
-// L2, by all threads together.  The few logits at or above the bound (ties
+// L2, by all threads together; a run of nothing but -inf reaches no bound, so
+// rows that leave fewer than n ids unmasked are as fast (2 x 131072 BF16 with 5
+// ids left, 20 alternatives: 7.3 us; 4096 rows 169 us; through the lists below
+// 24 and 764).  The few logits at or above the bound (ties
 // among them) are listed, and each finds its place by counting the larger
 // ones: no sorting, and no order of atomics in the result.  More runs or
 // candidates than fit (long ties) go through sorted lists of 32 per warp
@@ -315,13 +318,13 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_ker
     if (a.logprob && k == 0 && rank == 0 && t + step < a.T) ynext = a.targets[t + step];
     Run<ENT> acc;
     int slot = 0, left = 1 << shift;
-    float high = kLowest;
+    float high = neg_inf();
     stream.row(v1 - v0, [](uint4*, int) {}, [&](const auto& v, int) {
       const float mx = acc.add(v, c, E());
       if (TOP) {
         high = fmaxf(high, mx);
         slots[slot * kLpThreads] = high;
-        if (--left == 0) ++slot, left = 1 << shift, high = kLowest;
+        if (--left == 0) ++slot, left = 1 << shift, high = neg_inf();
       }
     });
     if (rank == 0) {

@@ -104,6 +104,32 @@ def test_alternatives_all_in_one_place(dtype):
         assert np.array_equal(got["top_ids"], R.logprobs(z, y, 1.0, 32)["top_ids"]), step
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,n_top", [(1, 131072, 20), (3, 70001, 32), (320, 40000, 20), (320, 9000, 8), (40, 6007, 32),
+                                       (33, 700, 20)])
+def test_masks_leave_fewer_ids_than_alternatives(T, V, n_top, dtype):
+    """Rows that a mask leaves 0, 1, 2, .. ids, the others -inf or the type's
+    lowest value."""
+    import torch
+    rng = np.random.default_rng(V + n_top)
+    for mask in [-np.inf, R.LOWEST[dtype]]:
+        full = R.round_to(rng.standard_normal((T, V)).astype(np.float32), dtype)
+        z = np.full((T, V), mask, np.float32)
+        y = np.full(T, -1, np.int32)
+        for t in range(T):
+            left = rng.choice(V, t % (n_top + 2), replace=False)
+            z[t, left] = full[t, left]
+            if len(left):
+                y[t] = left[0]
+        got = host(forward(R.device_rows(z, dtype, 1, 1), torch.from_numpy(y).cuda(), 1.0, n_top))
+        ref = R.logprobs(z, y, 1.0, n_top)
+        assert got["status"][0] == 0
+        near(got["logprob"], ref["logprob"], 4e-6 + 3e-7 * np.abs(ref["logprob"]))
+        near(got["entropy"], ref["entropy"], 8e-6 * (1 + ref["entropy"]))
+        assert np.array_equal(got["top_ids"], ref["top_ids"])
+        near(got["top_logprob"], ref["top_logprob"], 4e-6 + 3e-7 * np.abs(ref["top_logprob"]))
+
+
 def test_nonfinite_rows_and_bad_targets():
     import torch
     for dtype in ["bf16", "f32"]:
