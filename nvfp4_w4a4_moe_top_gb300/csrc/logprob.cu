@@ -90,11 +90,16 @@ __device__ __forceinline__ uint32_t top_bound2(uint32_t bound, int n, const TopS
   return __reduce_max_sync(0xFFFFFFFFu, lane < 2 * NW && reach >= k ? v : 0u);
 }
 
-// The candidates through per-warp lists of the 32 largest, each warp with its
-// own hot threads, 32 candidates at a time; any number of candidates.  The
-// group's list goes to sh.cand, zeros after the last.
+// The alternatives of a part that has any number of candidates (ties): its
+// vectors read again by all warps, each with a list of the 32 largest that it
+// fills 32 candidates at a time; keys below the n-th largest so far are dropped
+// at once, so that of equal logits only the first are sorted.  The group's list
+// goes to sh.cand, zeros after the last.  4096 x 131072 BF16 with 5 ids that
+// are not at the lowest value, 20 alternatives: 447 us (one candidate load at a
+// time, tested element by element: 803; four loads at a time: 392, but the
+// kernel then spills registers and rows without ties take 5% longer).
 template <int TH, typename E>
-__device__ __noinline__ void list_top(const Row<E>& r, int v0, int v1, bool ends, uint32_t mine, uint32_t bound, int n,
+__device__ __noinline__ void list_top(const Row<E>& r, int v0, int v1, bool ends, uint32_t bound, int n,
                                       TopShared<TH>& sh) {
   constexpr int N = Row<E>::kVec, NW = TH / 32;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x & (TH - 1)) >> 5;
@@ -121,17 +126,21 @@ __device__ __noinline__ void list_top(const Row<E>& r, int v0, int v1, bool ends
     held += __popc(who);
     if (held >= 32) flush();
   };
-  uint32_t hot = __ballot_sync(0xFFFFFFFFu, mine >= bound);
-  while (hot) {
-    const int h = __ffs(hot) - 1;
-    hot &= hot - 1;
-    for (int i0 = v0 + warp * 32 + h; i0 < v1; i0 += 32 * TH) {
-      const bool valid = lane < (v1 - i0 + TH - 1) / TH;
-      const int i = i0 + (valid ? lane * TH : 0);
-      float x[N];
-      unpack(r.vec()[i], x);
+  constexpr int B = 2;
+  for (int i0 = v0 + warp * 32; i0 < v1; i0 += TH * B) {
+    uint4 v[B];
 #pragma unroll
-      for (int e = 0; e < N; ++e) offer(x[e], r.head + i * N + e, valid);
+    for (int u = 0; u < B; ++u) v[u] = r.vec()[min(i0 + u * TH + lane, v1 - 1)];
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+      const int i = i0 + u * TH + lane;
+      float x[N], high = neg_inf();
+      unpack(v[u], x);
+#pragma unroll
+      for (int e = 0; e < N; ++e) high = fmaxf(high, x[e]);
+      if (!__any_sync(0xFFFFFFFFu, i < v1 && rank_key(high, (uint32_t)(r.head + i * N)) >= least)) continue;
+#pragma unroll
+      for (int e = 0; e < N; ++e) offer(x[e], r.head + i * N + e, i < v1);
     }
   }
   if (warp == 0 && ends) {  // the elements outside the vectors
@@ -217,7 +226,7 @@ __device__ __forceinline__ int group_top(const Row<E>& r, int v0, int v1, bool e
   const int c = sh.ncand;
   if (k == 0) sh.nhot = 0;
   if (nhot <= TopShared<TH>::kHot && c <= TopShared<TH>::kCap) return c;
-  list_top<TH>(r, v0, v1, ends, rank_value(mine), bound, n, sh);
+  list_top<TH>(r, v0, v1, ends, bound, n, sh);
   group_sync<TH>();
   return 32;
 }
