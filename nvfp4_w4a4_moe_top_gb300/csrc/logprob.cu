@@ -11,11 +11,14 @@ namespace moe {
 constexpr int kLpThreads = 256;
 constexpr int kLpU = 4;  // vectors per group of copies
 constexpr int kLpBlocksPerSm = 3;
-// Groups in flight: 64 KB of ring per block, or 48 KB and the 8 KB of maxima
+// Groups in flight: 64 KB of ring per block, or 48 KB and the 16 KB of maxima
 // that the alternatives need.
 template <bool TOP>
 constexpr int kLpD = TOP ? 3 : 4;
-constexpr int kLpSlots = 8;  // maxima kept per thread
+// Maxima kept per thread: with more of them the runs that are read again are
+// shorter (20 alternatives, BF16: 10000 x 16384 97 us with 8, 76 with 16; 8000 x
+// 24000 114 and 87; 4096 x 131072 191 and 185).
+constexpr int kLpSlots = 16;
 // Resident grids of rows per launch at most: blocks that end early make room
 // for others (one grid of blocks that take all rows in turn waits for the
 // slowest SM: 4096 rows of 131072, 178 us against 158), and each still has a
@@ -41,17 +44,14 @@ __device__ __forceinline__ void group_sync() {
 // L2, by all threads together; a run of nothing but -inf reaches no bound, so
 // rows that leave fewer than n ids unmasked are as fast (2 x 131072 BF16 with 5
 // ids left, 20 alternatives: 7.3 us; 4096 rows 169 us; through the lists below
-// 24 and 764).  The few logits at or above the bound (ties
-// among them) are listed, and each finds its place by counting the larger
-// ones: no sorting, and no order of atomics in the result.  More runs or
-// candidates than fit (long ties) go through sorted lists of 32 per warp
-// instead (list_top).
+// 24 and 764).  The few logits at or above the bound (ties among them) are
+// listed, and each finds its place by counting the larger ones: no sorting, and
+// no order of atomics in the result.  More runs or candidates than fit (long
+// ties) go through sorted lists of 32 per warp instead (list_top).
 template <int TH>
 struct TopShared {
   static constexpr int NW = TH / 32, kCap = TH < 128 ? 128 : 256, kHot = TH < 64 ? 64 : TH;
   uint64_t cand[kCap];
-  uint64_t pending[NW][64];
-  uint64_t lists[NW][32];
   uint32_t vals[2][NW];
   int hot[kHot];  // thread * kLpSlots + slot
   int nhot, ncand;
@@ -100,18 +100,23 @@ __device__ __forceinline__ uint32_t top_bound2(uint32_t bound, int n, const TopS
 // kernel then spills registers and rows without ties take 5% longer).
 template <int TH, typename E>
 __device__ __noinline__ void list_top(const Row<E>& r, int v0, int v1, bool ends, uint32_t bound, int n,
-                                      TopShared<TH>& sh) {
+                                      float* slots, TopShared<TH>& sh) {
   constexpr int N = Row<E>::kVec, NW = TH / 32;
+  static_assert(kLpSlots >= 6, "the slots hold 96 keys per warp");
   const int lane = threadIdx.x & 31, warp = (threadIdx.x & (TH - 1)) >> 5;
   uint64_t list = 0, least = (uint64_t)bound << 32;  // keys below `least` cannot enter
-  uint64_t* pend = sh.pending[warp];
+  // the warps' slots, no longer needed, take up to 64 pending keys and a list
+  auto keys = [&](int w, int i) -> uint64_t& {
+    return reinterpret_cast<uint64_t*>(slots + (w - warp) * 32 - lane + (i >> 4) * kLpThreads)[i & 15];
+  };
+  auto pend = [&](int i) -> uint64_t& { return keys(warp, i); };
   int held = 0;
   auto flush = [&]() {  // sorts up to 32 pending keys into the list
     __syncwarp();
-    const uint64_t key = lane < held ? pend[lane] : 0;
-    const uint64_t rest = lane + 32 < held ? pend[lane + 32] : 0;
+    const uint64_t key = lane < held ? pend(lane) : 0;
+    const uint64_t rest = lane + 32 < held ? pend(lane + 32) : 0;
     __syncwarp();
-    if (lane + 32 < held) pend[lane] = rest;
+    if (lane + 32 < held) pend(lane) = rest;
     held = held > 32 ? held - 32 : 0;
     list = list_merge(list, list_sort(key));
     least = max(least, __shfl_sync(0xFFFFFFFFu, list, n - 1));
@@ -122,7 +127,7 @@ __device__ __noinline__ void list_top(const Row<E>& r, int v0, int v1, bool ends
     const bool in = valid && x != neg_inf() && key >= least;
     const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
     if (who == 0) return;
-    if (in) pend[held + __popc(who & ((1u << lane) - 1))] = key;
+    if (in) pend(held + __popc(who & ((1u << lane) - 1))) = key;
     held += __popc(who);
     if (held >= 32) flush();
   };
@@ -151,9 +156,9 @@ __device__ __noinline__ void list_top(const Row<E>& r, int v0, int v1, bool ends
   if (held) flush();
 #pragma unroll
   for (int m = NW / 2; m > 0; m >>= 1) {
-    if (warp >= m && warp < 2 * m) sh.lists[warp][lane] = list;
+    if (warp >= m && warp < 2 * m) keys(warp, 64 + lane) = list;
     group_sync<TH>();
-    if (warp < m) list = list_merge(list, sh.lists[warp + m][lane]);
+    if (warp < m) list = list_merge(list, keys(warp + m, 64 + lane));
   }
   if (warp == 0) sh.cand[lane] = list;
 }
@@ -164,7 +169,7 @@ __device__ __noinline__ void list_top(const Row<E>& r, int v0, int v1, bool ends
 // after a group_sync that follows top_bound1 and the last use of sh.ncand.
 template <int TH, typename E>
 __device__ __forceinline__ int group_top(const Row<E>& r, int v0, int v1, bool ends, float mine, uint32_t bound1,
-                                         const float* slots, int shift, int n, TopShared<TH>& sh) {
+                                         float* slots, int shift, int n, TopShared<TH>& sh) {
   constexpr int N = Row<E>::kVec;
   const int k = threadIdx.x & (TH - 1);
   const int run = kLpU << shift, used = ((v1 - v0 + TH - 1) / TH + run - 1) / run;  // vectors in a run; runs
@@ -196,7 +201,6 @@ __device__ __forceinline__ int group_top(const Row<E>& r, int v0, int v1, bool e
   const int nhot = sh.nhot;
   if (nhot <= TopShared<TH>::kHot) {
     const int items = nhot * run;
-#pragma unroll 4
     for (int q = k; q < items; q += TH) {
       const int who = sh.hot[q / kLpU >> shift];
       const int i = v0 + (who & 0xFFFF) + ((who >> 16) * run + (q & (run - 1))) * TH;
@@ -226,7 +230,7 @@ __device__ __forceinline__ int group_top(const Row<E>& r, int v0, int v1, bool e
   const int c = sh.ncand;
   if (k == 0) sh.nhot = 0;
   if (nhot <= TopShared<TH>::kHot && c <= TopShared<TH>::kCap) return c;
-  list_top<TH>(r, v0, v1, ends, bound, n, sh);
+  list_top<TH>(r, v0, v1, ends, bound, n, slots, sh);
   group_sync<TH>();
   return 32;
 }
@@ -287,7 +291,7 @@ __device__ __forceinline__ void place_lists(const uint64_t* lists, int nb, int n
 // 4096 x 131072 BF16 with entropy: 157 us, 6.83 TB/s, 1.0 of the measured copy
 // rate (loads into registers in batches of four, two blocks per SM: 234 us,
 // waiting for them; the ring keeps 64 KB per block on the way).  With 20
-// alternatives 191 us: what a row's end waits for, its barriers and the second
+// alternatives 185 us: what a row's end waits for, its barriers and the second
 // read of the candidates, is then no longer hidden.
 template <typename E, bool ENT, bool TOP, int TH>
 __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSm) token_logprobs_kernel(LogprobArgs a) {
@@ -551,17 +555,18 @@ int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
   const bool bf = a.dtype == MOE_DTYPE_BF16, ent = a.entropy != nullptr, top = a.n_top > 0;
   const int64_t nvec = (int64_t)a.V * (bf ? 2 : 4) / 16;
   const int most = kLpBlocksPerSm * gemm_num_ctas();  // resident blocks
-  // Threads per row.  With enough rows to fill the GPU, as few as hide the
-  // row's end (sums, alternatives) behind other rows: a warp for short rows,
-  // four for long ones (BF16, no alternatives: 4000 x 8192 16, 19 and 29 us with
-  // 32, 128 and 256 threads; 2000 x 20000 17, 19 and 25; 4000 x 50000 67, 62 and
-  // 73).  With alternatives L2 should still hold a row at its end: 256 threads
-  // from 160 KB on (4096 x 131072 with 20: 247 us with 128, 191 with 256; 8000 x
-  // 65536: 212 and 218).  Else blocks, and clusters of up to 8 of them while they
-  // fill the GPU and each thread keeps two vectors (2 x 131072 with 20: 18 us
-  // with one block per row, 14 with 8).
-  const bool warp = (nvec <= 1024 && (a.T >= 304 || nvec <= 128)) || (nvec <= 3072 && a.T >= 1000);
-  const int th = warp ? 32 : a.T >= 304 && !(top && nvec > 10240) ? 128 : kLpThreads;
+  // Threads per row.  256 where each row can have a block at once (400 x 16384
+  // BF16 4.9 us, with 128 threads 5.9; with 20 alternatives 8.1 and 11).  With
+  // more rows as few as hide a row's end (sums, alternatives) behind the others:
+  // a warp for short rows, four for long ones (BF16, no alternatives: 4000 x 8192
+  // 16, 19 and 29 us with 32, 128 and 256 threads; 2000 x 20000 17, 19 and 25;
+  // 4000 x 50000 67, 62 and 70; 900 x 8192 5.9, 4.6 and 6.2).  With alternatives
+  // L2 should still hold a row at its end: 256 threads from 160 KB on (2000 x
+  // 131072 with 20: 113 us with 128, 99 with 256; 4000 x 65536: 107 and 108).
+  // Where blocks are left over, clusters of up to 8 of them, while each thread
+  // keeps two vectors (2 x 131072 with 20: 18 us with one block per row, 14 with 8).
+  const bool warp = nvec <= 128 || (nvec <= 256 && a.T >= 304) || (nvec <= 3072 && a.T >= 1000);
+  const int th = warp ? 32 : a.T > most && !(top && nvec > 10240) ? 128 : kLpThreads;
   int nb = 1;
   if (th == kLpThreads)
     while (nb < 8 && (int64_t)a.T * nb * 2 <= most && nvec / (nb * 2) >= 2 * kLpThreads) nb *= 2;
