@@ -315,8 +315,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a
 
 // dw from the blocks' parts: 32 columns per block, the parts in 32 slices that
 // meet in shared memory; always the same order.
-__global__ void __launch_bounds__(1024) add_rmsnorm_dw_kernel(const float* __restrict__ part, int nb, int d,
-                                                              float* dw) {
+__global__ void __launch_bounds__(1024) add_rmsnorm_dw_kernel(const float* part, int nb, int d, float* dw) {
   __shared__ float sh[32][33];
   begin_kernel();
   const int i = blockIdx.x * 32 + threadIdx.x;
