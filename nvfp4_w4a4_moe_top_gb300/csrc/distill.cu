@@ -420,16 +420,25 @@ static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
     while (nb < 8 && (int64_t)a.T * nb < 16 * sms && nvec / (nb * 2) >= 2048) nb *= 2;
   const int64_t part = nvec / nb;
   // Threads per row: as few as hide a row's ends (list, sums, loss) behind
-  // other rows.  Loss, BF16: 4000 x 10000 25 us with 32 and 30 with 128; 16384 x
+  // other rows.  Loss, BF16: 6000 x 8192 27 us with 32 and 34 with 128; 16384 x
   // 32768 175 with 128 and 213 with 256; 4096 x 131072 166 and 153.  Gradient:
-  // 4000 x 10000 40 with 32 and 33 with 128.  The step's 1024 threads per SM
-  // work on rows that L2 has to hold between the passes: 80 MB of it (4096 x
-  // 131072: 372 with 512, 455 with 256).
-  int th = part <= (sums ? 2048 : 1024) ? 32 : part <= 8192 ? 128 : 256;
+  // 6000 x 8192 38 with 32 and 41 with 128; 6000 x 16384 71 and 64.  The step:
+  // 6000 x 8192 51 and 56, 6000 x 16384 93 and 84; its 1024 threads per SM work
+  // on rows that L2 has to hold between the passes: 80 MB of it (4096 x 131072:
+  // 372 with 512, 455 with 256).
+  int th = part <= (grad ? 1024 : 2048) ? 32 : part <= 8192 ? 128 : 256;
   if (sums && grad && th > 32) th = part <= 3072 ? 128 : part <= 8192 ? 256 : part <= 16384 ? 512 : 1024;
   if (bits > 40 * 1024 && th < 256) th = 256;
-  if ((int64_t)a.T * nb <= 2 * sms)
-    while (th < 512 && part > 2 * th) th = th == 32 ? 128 : th * 2;
+  // More while all rows have them at once, 128 also in two rounds (the step, 600
+  // x 16384: 23 us with 32 threads, 11 with 256; 2000 x 16384: 43 and 33 with 128;
+  // the loss, 600 x 16384: 11 and 7); very short rows only where SMs would be
+  // left idle (the step, 4 x 4096: 9.1 us with 32, 5.6 with 256; 2000 x 2000:
+  // 11.2 and 13.1 with 128).
+  auto more = [](int n) { return n == 32 ? 128 : 2 * n; };
+  const int64_t rows = (int64_t)a.T * nb, room = (int64_t)sms * kDsMaxThreads;
+  while (th < 512 && part > (th == 32 && rows > 2 * sms ? 512 : 2 * th) &&
+         rows * more(th) <= (th == 32 ? 2 * room : room))
+    th = more(th);
   if (th > most) th = most;
   const int smem = th * kDsU * kDsD * 16 + bits;
   int fit = 227 * 1024 / (smem + 5 * 1024);
