@@ -560,12 +560,13 @@ int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
   // more rows as few as hide a row's end (sums, alternatives) behind the others:
   // a warp for short rows, four for long ones (BF16, no alternatives: 4000 x 8192
   // 16, 19 and 29 us with 32, 128 and 256 threads; 2000 x 20000 17, 19 and 25;
-  // 4000 x 50000 67, 62 and 70; 900 x 8192 5.9, 4.6 and 6.2).  With alternatives
+  // 4000 x 50000 67, 62 and 70; 1500 x 16384 17, 14 and 15).  With alternatives
   // L2 should still hold a row at its end: 256 threads from 160 KB on (2000 x
   // 131072 with 20: 113 us with 128, 99 with 256; 4000 x 65536: 107 and 108).
   // Where blocks are left over, clusters of up to 8 of them, while each thread
   // keeps two vectors (2 x 131072 with 20: 18 us with one block per row, 14 with 8).
-  const bool warp = nvec <= 128 || (nvec <= 256 && a.T >= 304) || (nvec <= 3072 && a.T >= 1000);
+  const bool warp = nvec <= 128 || (nvec <= 256 && a.T >= 304) || (nvec <= 512 && a.T >= 1000) ||
+                    (nvec <= 3072 && a.T >= 2000);
   const int th = warp ? 32 : a.T > most && !(top && nvec > 10240) ? 128 : kLpThreads;
   int nb = 1;
   if (th == kLpThreads)
