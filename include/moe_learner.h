@@ -176,8 +176,9 @@ int moe_distill_topk(const void* logits, int dtype, int64_t ld, int T, int V,
  *   dlogits_v = g inv_temperature (p_v Q - q_v)          on the list,
  *               g inv_temperature t_v (s Q - r)          off it, t_v = p_v / s
  * with Q = sum q_i + r (1, or 0 for a row without teacher entries).  dlogits
- * as in moe_token_logprobs_backward; rows without a distribution get zeros.
- * One launch. */
+ * as in moe_token_logprobs_backward.  Rows without a distribution, and rows
+ * with g = 0 whatever their numbers hold, get zeros (the numbers of a row with
+ * g = 0 still set status bits).  One launch. */
 int moe_distill_topk_backward(const void* logits, int dtype, int64_t ld, int T,
                               int V, const int32_t* teacher_ids,
                               const float* teacher_logits,
@@ -188,7 +189,8 @@ int moe_distill_topk_backward(const void* logits, int dtype, int64_t ld, int T,
 
 /* moe_distill_topk and its gradient in one call, for weights g that are known
  * beforehand (a mean over tokens, a mask): loss as the forward gives it, not
- * multiplied by g.  dlogits may be the logits themselves.  One launch. */
+ * multiplied by g.  Zeros where moe_distill_topk_backward gives them.  dlogits
+ * may be the logits themselves.  One launch. */
 int moe_distill_topk_train(const void* logits, int dtype, int64_t ld, int T,
                            int V, const int32_t* teacher_ids,
                            const float* teacher_logits,

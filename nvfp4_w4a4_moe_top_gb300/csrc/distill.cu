@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(TH, TH == 32 ? 24 : kDsMaxThreads / TH) distil
     // (maximum and ln-sum of the row, m, l, and off the list, mt, lt) where the
     // sums end, and the loss and the gradient on the list beside the gradient
     // off it, which is coef[0] times 2^(x c - coef[1]), or 2^((x - coef[1]) c)
-    // with `diff`.
+    // with `diff`.  Weight 0 (a masked row) gives zeros and no product with
+    // what the row's numbers give, which may be NaN.
     Teacher T;
     float m = 0.0f, l = 0.0f, mt = 0.0f, lt = 0.0f;
     if (k < 32)
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(TH, TH == 32 ? 24 : kDsMaxThreads / TH) distil
     auto weights = [&](float rescale, float shift) {
       const float ls = (mt - m) * a.inv_t + lt - l;  // ln of the mass off the list
       if (lane == 0) {
-        coef[0] = mt == neg_inf() ? 0.0f : g_row * a.inv_t * (expf(ls) * T.Q - T.r) * rescale;
+        coef[0] = mt == neg_inf() || g_row == 0.0f ? 0.0f : g_row * a.inv_t * (expf(ls) * T.Q - T.r) * rescale;
         coef[1] = shift;
       }
     };
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(TH, TH == 32 ? 24 : kDsMaxThreads / TH) distil
       for (int j = lane; j < a.K; j += 32) {
         const float q = teacher_q(T, list, j, a.inv_t), lp = (list.x[j] - m) * a.inv_t - l;
         if (SUMS && list.id[j] >= 0 && !(q == 0.0f)) part += none ? -neg_inf() : q * (T.lq(list.a[j], a.inv_t) - lp);
-        if (GRAD) list.a[j] = none ? 0.0f : g_row * a.inv_t * (expf(lp) * T.Q - q);
+        if (GRAD) list.a[j] = none || g_row == 0.0f ? 0.0f : g_row * a.inv_t * (expf(lp) * T.Q - q);
       }
       if (SUMS) {
         part = warp_sum(part);
