@@ -149,7 +149,9 @@ int moe_token_logprobs_backward(const void* logits, int dtype, int64_t ld,
  *   loss = sum_i q_i (ln q_i - ln p_{c_i}) + r (ln r - ln s)
  *   teacher_lse given: q_i = exp(a_i inv_temperature - teacher_lse), the
  *     teacher's mass r = max(0, 1 - sum q_i) off the list and the student's
- *     mass s = sum of p off the list compared as one outcome
+ *     mass s = sum of p off the list compared as one outcome.  r counts as 0
+ *     up to 2^-23 (8 + 2 |teacher_lse|), what rounding leaves of 1 - sum q_i
+ *     where the list holds all of the teacher's mass
  *   teacher_lse NULL: q = softmax over the listed a_i inv_temperature, r = 0
  *   teacher_ids     i32 [T][K], in any order.  A negative id is an empty
  *                   place.  An id >= V, or one listed before in its row, sets
