@@ -487,9 +487,11 @@ __global__ void __launch_bounds__(kLbThreads) token_logprobs_backward_kernel(Log
   const float m = a.stats[2 * t], l = a.stats[2 * t + 1];
   const bool zero = m == neg_inf() || (g == 0.0f && ge == 0.0f);
   const float A = -g - (a.g_entropy ? ge * a.entropy[t] : 0.0f);
-  // -inf gives p = 0 times a finite number; a NaN row's l makes all its values NaN
+  // a masked id gives p = 0 times a finite number: its ln p is held at a value
+  // where p is 0 long since, small enough for any product with g_entropy
+  // inv_temperature below 3e34; a NaN row's l makes all its values NaN
   auto grad = [&](float x) {
-    const float lp = fmaxf((x - m) * a.inv_t, -1e30f) - l;
+    const float lp = fmaxf((x - m) * a.inv_t, -1e4f) - l;
     return exp2_fast(lp * kLog2e) * fmaf(-ge, lp, A);
   };
   const Row<E> r(row, a.V);
