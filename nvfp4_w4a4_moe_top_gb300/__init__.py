@@ -276,28 +276,43 @@ def backward_workspace_bytes(T, E, k, d, d_ff):
 
 # --------------------------------------------------------------------------
 # learner operators (include/moe_learner.h): sizes and strides come from the
-# tensors, whose types and sizes are checked here
+# tensors, whose types, sizes and devices are checked here
 # --------------------------------------------------------------------------
-def _tensor(t, dtypes, shape, what):
-    """Pointer of a contiguous device tensor of one of `dtypes` and of `shape`
-    (None: an optional argument left out)."""
+def _place(t):
+    """Where a tensor is, for a message."""
+    dev = t.get_device()
+    return "the host" if dev < 0 else "device %d" % dev
+
+
+def _here(t, what):
+    """Index of the current device, on which a call's first tensor has to be
+    (and all others: the launch and its stream are that device's)."""
+    dev = t.get_device()
+    if dev < 0 or dev != _types.device():
+        raise ValueError("%s: a tensor on the current CUDA device expected, got one on %s" % (what, _place(t)))
+    return dev
+
+
+def _tensor(t, dtypes, shape, what, dev):
+    """Pointer of a contiguous tensor on device `dev` of one of `dtypes` and of
+    `shape` (None: an optional argument left out)."""
     if t is None:
         return None
-    if t.dtype not in dtypes or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError("%s: a contiguous CUDA tensor %s of %s expected, got %s of %s"
-                         % (what, tuple(shape), " or ".join(map(str, dtypes)), tuple(t.shape), t.dtype))
+    if t.dtype not in dtypes or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s: a contiguous CUDA tensor %s of %s on device %d expected, got %s of %s on %s"
+                         % (what, tuple(shape), " or ".join(map(str, dtypes)), dev, tuple(t.shape), t.dtype, _place(t)))
     return t.data_ptr()
 
 
-def _rows(t, dtypes, shape, what):
-    """Pointer, row stride and shape of a 2-D device tensor whose rows are
-    contiguous."""
+def _rows(t, dtypes, shape, what, dev):
+    """Pointer, row stride and shape of a 2-D tensor on device `dev` whose rows
+    are contiguous."""
     own, st = t.shape, t.stride()
-    if len(own) != 2 or (shape is not None and own != shape) or t.dtype not in dtypes or not t.is_cuda or \
+    if len(own) != 2 or (shape is not None and own != shape) or t.dtype not in dtypes or t.get_device() != dev or \
             (st[1] != 1 and own[1] > 1):
-        raise ValueError("%s: a 2-D CUDA tensor%s of %s with contiguous rows expected, got %s of %s, strides %s"
-                         % (what, "" if shape is None else " %s" % (tuple(shape),), " or ".join(map(str, dtypes)),
-                            tuple(own), t.dtype, st))
+        raise ValueError("%s: a 2-D CUDA tensor%s of %s with contiguous rows on device %d expected, got %s of %s on "
+                         "%s, strides %s" % (what, "" if shape is None else " %s" % (tuple(shape),),
+                                             " or ".join(map(str, dtypes)), dev, tuple(own), t.dtype, _place(t), st))
     return t.data_ptr(), (st[0] if own[0] > 1 else own[1]), own
 
 
@@ -311,6 +326,7 @@ class _Types:
         self.b16 = (torch.bfloat16, torch.int16, torch.uint16)
         self.f32 = (torch.float32,)
         self.i32 = (torch.int32,)
+        self.status = (torch.int32, torch.uint32)
         self.logits = self.b16 + self.f32
         self.codes = (torch.uint8, torch.float8_e4m3fn)
         self.scales = (torch.uint8, torch.float8_e8m0fnu)
@@ -330,12 +346,29 @@ def _dt():
     return _types
 
 
-def _opt(t):
-    return None if t is None else t.data_ptr()
+def _status(t, dev):
+    """Pointer of a status word, an int on device `dev`."""
+    if t is None:
+        return None
+    if t.dtype not in _types.status or t.get_device() != dev or t.numel() < 1:
+        raise ValueError("status: a 32-bit integer on device %d expected, got %s of %s on %s"
+                         % (dev, tuple(t.shape), t.dtype, _place(t)))
+    return t.data_ptr()
 
 
-def _stream(stream):
-    return _types.raw_stream(_types.device()) if stream is None else stream.cuda_stream
+def _workspace(t, dev):
+    """Pointer and bytes of a workspace, contiguous memory on device `dev` of
+    any type."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("ws: a contiguous CUDA tensor on device %d expected, got %s on %s, strides %s"
+                         % (dev, tuple(t.shape), _place(t), t.stride()))
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _stream(stream, dev):
+    return _types.raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def mx8_sf_bytes(rows, d):
@@ -352,17 +385,18 @@ def moe_add_rmsnorm(x, res, w, eps, h, y, y8=None, y8_sf=None, rstd=None, status
     res [T][d] may have strided rows."""
     ty = _dt()
     b16 = ty.b16
-    px, ldx, shape = _rows(x, b16, None, "x")
+    dev = _here(x, "x")
+    px, ldx, shape = _rows(x, b16, None, "x", dev)
     T, d = shape
-    pr, ldr, _ = (None, d, None) if res is None else _rows(res, b16, shape, "res")
-    if y8_sf is not None and (not y8_sf.is_contiguous() or y8_sf.dtype not in ty.scales or not y8_sf.is_cuda
+    pr, ldr, _ = (None, d, None) if res is None else _rows(res, b16, shape, "res", dev)
+    if y8_sf is not None and (not y8_sf.is_contiguous() or y8_sf.dtype not in ty.scales or y8_sf.get_device() != dev
                               or y8_sf.numel() < (T + 127) // 128 * (d // 128) * 512):
-        raise ValueError("y8_sf: at least %d contiguous scale bytes on the GPU expected" % mx8_sf_bytes(T, d))
+        raise ValueError("y8_sf: at least %d contiguous scale bytes on device %d expected" % (mx8_sf_bytes(T, d), dev))
     _check("moe_add_rmsnorm", lib().moe_add_rmsnorm(
-        px, ldx, pr, ldr, _tensor(w, b16, (d,), "w"), eps, T, d, _tensor(h, b16, shape, "h"),
-        _tensor(y, b16, shape, "y"), _tensor(y8, ty.codes, shape, "y8"),
-        _opt(y8_sf), _tensor(rstd, ty.f32, (T,), "rstd"), _opt(status),
-        _stream(stream)))
+        px, ldx, pr, ldr, _tensor(w, b16, (d,), "w", dev), eps, T, d, _tensor(h, b16, shape, "h", dev),
+        _tensor(y, b16, shape, "y", dev), _tensor(y8, ty.codes, shape, "y8", dev),
+        None if y8_sf is None else y8_sf.data_ptr(), _tensor(rstd, ty.f32, (T,), "rstd", dev), _status(status, dev),
+        _stream(stream, dev)))
 
 
 def moe_add_rmsnorm_backward(dy, dh, h, rstd, w, dx, dw, ws, status=None, stream=None):
@@ -374,11 +408,13 @@ def moe_add_rmsnorm_backward(dy, dh, h, rstd, w, dx, dw, ws, status=None, stream
     if dy.dim() != 2:
         raise ValueError("dy: a 2-D tensor expected, got %s" % (tuple(shape),))
     T, d = shape
+    dev = _here(dy, "dy")
+    pws, ws_bytes = _workspace(ws, dev)
     _check("moe_add_rmsnorm_backward", lib().moe_add_rmsnorm_backward(
-        _tensor(dy, b16, shape, "dy"), _tensor(dh, b16, shape, "dh"), _tensor(h, b16, shape, "h"),
-        _tensor(rstd, ty.f32, (T,), "rstd"), _tensor(w, b16, (d,), "w"), T, d, _tensor(dx, b16, shape, "dx"),
-        _tensor(dw, ty.f32, (d,), "dw"), _opt(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _opt(status), _stream(stream)))
+        _tensor(dy, b16, shape, "dy", dev), _tensor(dh, b16, shape, "dh", dev), _tensor(h, b16, shape, "h", dev),
+        _tensor(rstd, ty.f32, (T,), "rstd", dev), _tensor(w, b16, (d,), "w", dev), T, d,
+        _tensor(dx, b16, shape, "dx", dev), _tensor(dw, ty.f32, (d,), "dw", dev), pws, ws_bytes,
+        _status(status, dev), _stream(stream, dev)))
 
 
 def moe_token_logprobs(logits, targets, inv_temperature, n_top, logprob, entropy, stats, top_ids=None,
@@ -388,13 +424,14 @@ def moe_token_logprobs(logits, targets, inv_temperature, n_top, logprob, entropy
     allowed).  Outputs that are None are left out."""
     ty = _dt()
     f32 = ty.f32
-    pl, ld, shape = _rows(logits, ty.logits, None, "logits")
+    dev = _here(logits, "logits")
+    pl, ld, shape = _rows(logits, ty.logits, None, "logits", dev)
     T, V = shape
     _check("moe_token_logprobs", lib().moe_token_logprobs(
-        pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty.i32, (T,), "targets"), inv_temperature,
-        n_top, _tensor(logprob, f32, (T,), "logprob"), _tensor(entropy, f32, (T,), "entropy"),
-        _tensor(stats, f32, (T, 2), "stats"), _tensor(top_ids, ty.i32, (T, n_top), "top_ids"),
-        _tensor(top_logprob, f32, (T, n_top), "top_logprob"), _opt(status), _stream(stream)))
+        pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty.i32, (T,), "targets", dev), inv_temperature,
+        n_top, _tensor(logprob, f32, (T,), "logprob", dev), _tensor(entropy, f32, (T,), "entropy", dev),
+        _tensor(stats, f32, (T, 2), "stats", dev), _tensor(top_ids, ty.i32, (T, n_top), "top_ids", dev),
+        _tensor(top_logprob, f32, (T, n_top), "top_logprob", dev), _status(status, dev), _stream(stream, dev)))
 
 
 def moe_token_logprobs_backward(logits, targets, inv_temperature, stats, entropy, g_logprob, g_entropy, dlogits,
@@ -403,26 +440,27 @@ def moe_token_logprobs_backward(logits, targets, inv_temperature, stats, entropy
     be the logits themselves."""
     ty = _dt()
     f32 = ty.f32
-    pl, ld, shape = _rows(logits, ty.logits, None, "logits")
+    dev = _here(logits, "logits")
+    pl, ld, shape = _rows(logits, ty.logits, None, "logits", dev)
     T, V = shape
-    pd, ldd, _ = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
+    pd, ldd, _ = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits", dev)
     _check("moe_token_logprobs_backward", lib().moe_token_logprobs_backward(
-        pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty.i32, (T,), "targets"), inv_temperature,
-        _tensor(stats, f32, (T, 2), "stats"), _tensor(entropy, f32, (T,), "entropy"),
-        _tensor(g_logprob, f32, (T,), "g_logprob"), _tensor(g_entropy, f32, (T,), "g_entropy"), pd, ldd, _opt(status),
-        _stream(stream)))
+        pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(targets, ty.i32, (T,), "targets", dev), inv_temperature,
+        _tensor(stats, f32, (T, 2), "stats", dev), _tensor(entropy, f32, (T,), "entropy", dev),
+        _tensor(g_logprob, f32, (T,), "g_logprob", dev), _tensor(g_entropy, f32, (T,), "g_entropy", dev), pd, ldd,
+        _status(status, dev), _stream(stream, dev)))
 
 
-def _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature):
-    pl, ld, shape = _rows(logits, ty.logits, None, "logits")
+def _distill_args(ty, dev, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature):
+    pl, ld, shape = _rows(logits, ty.logits, None, "logits", dev)
     T, V = shape
     if teacher_ids.dim() != 2:
         raise ValueError("teacher_ids: a 2-D tensor expected, got %s" % (tuple(teacher_ids.shape),))
     K = teacher_ids.shape[1]
     return (pl, 1 if logits.dtype in ty.f32 else 0, ld, T, V,
-            _tensor(teacher_ids, ty.i32, (T, K), "teacher_ids"),
-            _tensor(teacher_logits, ty.f32, (T, K), "teacher_logits"),
-            _tensor(teacher_lse, ty.f32, (T,), "teacher_lse"), K, inv_temperature)
+            _tensor(teacher_ids, ty.i32, (T, K), "teacher_ids", dev),
+            _tensor(teacher_logits, ty.f32, (T, K), "teacher_logits", dev),
+            _tensor(teacher_lse, ty.f32, (T,), "teacher_lse", dev), K, inv_temperature)
 
 
 def moe_distill_topk(logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature, loss, stats, status=None,
@@ -432,10 +470,11 @@ def moe_distill_topk(logits, teacher_ids, teacher_logits, teacher_lse, inv_tempe
     outcome; None: over the listed ids)."""
     ty = _dt()
     T = logits.shape[0]
-    a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
+    dev = _here(logits, "logits")
+    a = _distill_args(ty, dev, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
     _check("moe_distill_topk", lib().moe_distill_topk(
-        *a, _tensor(loss, ty.f32, (T,), "loss"), _tensor(stats, ty.f32, (T, 4), "stats"), _opt(status),
-        _stream(stream)))
+        *a, _tensor(loss, ty.f32, (T,), "loss", dev), _tensor(stats, ty.f32, (T, 4), "stats", dev),
+        _status(status, dev), _stream(stream, dev)))
 
 
 def moe_distill_topk_backward(logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature, stats, g, dlogits,
@@ -444,11 +483,12 @@ def moe_distill_topk_backward(logits, teacher_ids, teacher_logits, teacher_lse, 
     themselves."""
     ty = _dt()
     T = logits.shape[0]
-    a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
-    pd, ldd, _ = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
+    dev = _here(logits, "logits")
+    a = _distill_args(ty, dev, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
+    pd, ldd, _ = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits", dev)
     _check("moe_distill_topk_backward", lib().moe_distill_topk_backward(
-        *a, _tensor(stats, ty.f32, (T, 4), "stats"), _tensor(g, ty.f32, (T,), "g"), pd, ldd, _opt(status),
-        _stream(stream)))
+        *a, _tensor(stats, ty.f32, (T, 4), "stats", dev), _tensor(g, ty.f32, (T,), "g", dev), pd, ldd,
+        _status(status, dev), _stream(stream, dev)))
 
 
 def moe_distill_topk_train(logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature, g, loss, dlogits,
@@ -457,11 +497,12 @@ def moe_distill_topk_train(logits, teacher_ids, teacher_logits, teacher_lse, inv
     weighted by g."""
     ty = _dt()
     T = logits.shape[0]
-    a = _distill_args(ty, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
-    pd, ldd, _ = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits")
+    dev = _here(logits, "logits")
+    a = _distill_args(ty, dev, logits, teacher_ids, teacher_logits, teacher_lse, inv_temperature)
+    pd, ldd, _ = _rows(dlogits, ty.same[logits.dtype], logits.shape, "dlogits", dev)
     _check("moe_distill_topk_train", lib().moe_distill_topk_train(
-        *a, _tensor(g, ty.f32, (T,), "g"), _tensor(loss, ty.f32, (T,), "loss"), pd, ldd, _opt(status),
-        _stream(stream)))
+        *a, _tensor(g, ty.f32, (T,), "g", dev), _tensor(loss, ty.f32, (T,), "loss", dev), pd, ldd, _status(status, dev),
+        _stream(stream, dev)))
 
 
 class Pipeline:
