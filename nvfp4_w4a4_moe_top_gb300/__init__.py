@@ -293,6 +293,13 @@ def _here(t, what):
     return dev
 
 
+def _ints(shape, what):
+    """Refuses rows and columns beyond the library's int, which would be passed
+    modulo 2^32."""
+    if shape[0] > 0x7FFFFFFF or shape[1] > 0x7FFFFFFF:
+        raise ValueError("%s: at most 2^31 - 1 rows and columns expected, got %s" % (what, tuple(shape)))
+
+
 def _tensor(t, dtypes, shape, what, dev):
     """Pointer of a contiguous tensor on device `dev` of one of `dtypes` and of
     `shape` (None: an optional argument left out)."""
@@ -313,6 +320,7 @@ def _rows(t, dtypes, shape, what, dev):
         raise ValueError("%s: a 2-D CUDA tensor%s of %s with contiguous rows on device %d expected, got %s of %s on "
                          "%s, strides %s" % (what, "" if shape is None else " %s" % (tuple(shape),),
                                              " or ".join(map(str, dtypes)), dev, tuple(own), t.dtype, _place(t), st))
+    _ints(own, what)
     return t.data_ptr(), (st[0] if own[0] > 1 else own[1]), own
 
 
@@ -407,6 +415,7 @@ def moe_add_rmsnorm_backward(dy, dh, h, rstd, w, dx, dw, ws, status=None, stream
     shape = dy.shape
     if dy.dim() != 2:
         raise ValueError("dy: a 2-D tensor expected, got %s" % (tuple(shape),))
+    _ints(shape, "dy")
     T, d = shape
     dev = _here(dy, "dy")
     pws, ws_bytes = _workspace(ws, dev)
@@ -456,6 +465,7 @@ def _distill_args(ty, dev, logits, teacher_ids, teacher_logits, teacher_lse, inv
     T, V = shape
     if teacher_ids.dim() != 2:
         raise ValueError("teacher_ids: a 2-D tensor expected, got %s" % (tuple(teacher_ids.shape),))
+    _ints(teacher_ids.shape, "teacher_ids")
     K = teacher_ids.shape[1]
     return (pl, 1 if logits.dtype in ty.f32 else 0, ld, T, V,
             _tensor(teacher_ids, ty.i32, (T, K), "teacher_ids", dev),

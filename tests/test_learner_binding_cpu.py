@@ -135,3 +135,20 @@ def test_workspaces(library):
         call(**{**args, "ws": Stand((64, 64), U8, contiguous=False)})
     call(**{**args, "ws": Stand((1024,), F32)})
     call(**{**args, "ws": None, "dw": None})
+
+
+def test_sizes_beyond_32_bits(library):
+    """Rows that the library's int cannot count are refused, not counted modulo
+    2^32."""
+    big = (1 << 32) + 4
+    for shape in [(big, 1), (1, big), (1 << 31, 1)]:
+        with pytest.raises(ValueError):
+            M.moe_token_logprobs(Stand(shape, B16), None, 1.0, 0, None, None, Stand((shape[0], 2), F32))
+    with pytest.raises(ValueError):
+        M.moe_add_rmsnorm(Stand((big, D), B16), None, Stand((D,), B16), 1e-6, None, Stand((big, D), B16))
+    x = Stand((big, D), B16)
+    with pytest.raises(ValueError):
+        M.moe_add_rmsnorm_backward(x, None, x, Stand((big,), F32), Stand((D,), B16), x, None, None)
+    with pytest.raises(ValueError):
+        M.moe_distill_topk(Stand((T, V), B16), Stand((T, big), I32), Stand((T, big), F32), None, 1.0, Stand((T,), F32), None)
+    assert library.calls == 0
