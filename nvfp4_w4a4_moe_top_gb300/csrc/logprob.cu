@@ -585,7 +585,7 @@ int launch_token_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t s) {
   // A warp per row where a row is too short for a block (40000 x 2000 BF16: 89
   // us with blocks, 53 with warps).
   const bool small = nvec <= 512 && a.T >= 1024;
-  const int rows = small ? (a.T + kLbThreads / 32 - 1) / (kLbThreads / 32) : a.T;
+  const unsigned rows = small ? ((unsigned)a.T + kLbThreads / 32 - 1) / (kLbThreads / 32) : (unsigned)a.T;
   const unsigned nb = (unsigned)(small || nvec <= kLbPart ? 1 : (nvec + kLbPart - 1) / kLbPart);
   const unsigned gy = rows < 65535 ? rows : 65535, gz = (rows + gy - 1) / gy;
   auto f = a.dtype == MOE_DTYPE_BF16 ? (small ? token_logprobs_backward_kernel<uint16_t, 32>

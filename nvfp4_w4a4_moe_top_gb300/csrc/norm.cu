@@ -335,8 +335,8 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_dw_kernel(const float* part,
 template <int TPR, int NV>
 static int launch_norm(const NormArgs& a, cudaStream_t s) {
   constexpr int rows = TPR < 128 ? 128 / TPR : 1;
-  return launch_kernel(add_rmsnorm_kernel<TPR, NV>, dim3((unsigned)((a.T + rows - 1) / rows)), TPR < 128 ? 128 : TPR, 0,
-                       1, s, a);
+  const unsigned blocks = ((unsigned)a.T + rows - 1) / rows;  // T may be the largest int
+  return launch_kernel(add_rmsnorm_kernel<TPR, NV>, dim3(blocks), TPR < 128 ? 128 : TPR, 0, 1, s, a);
 }
 int launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
   const int n = a.d / 16;  // chunks
@@ -365,8 +365,9 @@ static NormBwdPlan norm_bwd_plan(int T, int d) {
   const int nb = p.threads * p.groups;
   p.smem = nb * p.nv * 3 * 16 * rows * p.depth;
   const int fit = 220 * 1024 / (p.smem + 2048), cap = 1536 / nb;
-  const int per = fit < cap ? (fit < 1 ? 1 : fit) : cap, all = (T + rows * p.groups - 1) / (rows * p.groups);
-  p.blocks = 152 * per < all ? 152 * per : all;
+  const int per = fit < cap ? (fit < 1 ? 1 : fit) : cap;
+  const int64_t all = ((int64_t)T + rows * p.groups - 1) / (rows * p.groups);
+  p.blocks = 152 * per < all ? 152 * per : (int)all;
   return p;
 }
 size_t add_rmsnorm_backward_ws(int T, int d) { return (size_t)norm_bwd_plan(T, d).blocks * d * 4; }
