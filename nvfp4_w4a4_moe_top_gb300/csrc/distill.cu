@@ -417,8 +417,9 @@ template <typename E>
 static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
   const int64_t nvec = (int64_t)a.V / Row<E>::kVec;
   const bool sums = a.loss != nullptr, grad = a.dlogits != nullptr;
-  const int sms = gemm_num_ctas(), bits = (a.V + 2 * Row<E>::kVec + 31) / 32 * 4;
-  const int most = bits <= 80 * 1024 ? 1024 : 512;  // threads whose ring fits beside the bits
+  auto bits_of = [](int V) { return (V + 2 * Row<E>::kVec + 31) / 32 * 4; };
+  const int sms = gemm_num_ctas(), bits = bits_of(a.V), bits_1024 = 80 * 1024;
+  const int most = bits <= bits_1024 ? 1024 : 512;  // threads whose ring fits beside the bits
   // Few rows: more blocks per row until there is one for each SM.
   int nb = 1;
   while (nb < 8 && (int64_t)a.T * nb < sms && nvec / (nb * 2) >= 512) nb *= 2;
@@ -449,7 +450,8 @@ static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
          rows * more(th) <= (th == 32 ? 2 * room : room))
     th = more(th);
   if (th > most) th = most;
-  const int smem = th * kDsU * kDsD * 16 + bits;
+  const int ring = th * kDsU * kDsD * 16, smem = ring + bits;
+  const int smem_most = ring + (th == 1024 ? bits_1024 : bits_of(MOE_DISTILL_MAX_V));
   int fit = 227 * 1024 / (smem + 5 * 1024);
   if (fit > kDsMaxThreads / th) fit = kDsMaxThreads / th;
   if (fit < 1) fit = 1;
@@ -457,7 +459,7 @@ static int launch_distill_of(const DistillArgs& a, cudaStream_t s) {
   auto f = !sums  ? distill_of<E, false, true>(th)
            : grad ? distill_of<E, true, true>(th)
                   : distill_of<E, true, false>(th);
-  if (!allow_smem((const void*)f, smem)) return -1;
+  if (!allow_smem((const void*)f, smem, smem_most)) return -1;
   return launch_kernel(f, dim3(nb, (unsigned)(a.T < grid ? a.T : grid)), th, smem, sums ? nb : 1, s, a);
 }
 int launch_distill(const DistillArgs& a, cudaStream_t s) {

@@ -3,9 +3,10 @@
 #include "kernels.cuh"
 #include "learner.cuh"
 
-bool moe::allow_smem(const void* kernel, int bytes) {
+bool moe::allow_smem(const void* kernel, int bytes, int most) {
   return bytes <= 16 * 1024 ||  // with the kernel's static share, within the 48 KB that need no asking
-         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+         (bytes <= most &&
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess);
 }
 
 namespace {

@@ -86,7 +86,10 @@ struct DistillArgs {
   int* status;
 };
 // Lets a kernel use `bytes` of dynamic shared memory on the current device.
-bool allow_smem(const void* kernel, int bytes);
+// `most` is what its largest launch needs: the limit is the kernel's own, not
+// the launch's, so every call sets that one value, and a thread with a small
+// launch takes nothing from another thread's large one.
+bool allow_smem(const void* kernel, int bytes, int most);
 
 int launch_add_rmsnorm(const NormArgs& a, cudaStream_t s);
 size_t add_rmsnorm_backward_ws(int T, int d);

@@ -577,7 +577,7 @@ int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s) {
   const int64_t grid = nb > 1 ? most / nb : (int64_t)most * kLpTurns;
   const int smem = top ? kLpSmem<true> : kLpSmem<false>;
   auto f = bf ? token_logprobs_of<uint16_t>(th, ent, top) : token_logprobs_of<float>(th, ent, top);
-  if (!allow_smem((const void*)f, smem)) return -1;
+  if (!allow_smem((const void*)f, smem, smem)) return -1;
   return launch_kernel(f, dim3(nb, (unsigned)(want < grid ? want : grid)), kLpThreads, smem, nb, s, a);
 }
 int launch_token_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t s) {

@@ -350,9 +350,10 @@ int launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
 }
 
 // The backward's launch for a size: threads per row, groups of threads per
-// block, rows a group takes at a time, groups of rows in flight, blocks.
+// block, rows a group takes at a time, groups of rows in flight, blocks, shared
+// memory of the launch and of the largest launch of the same kernel.
 struct NormBwdPlan {
-  int nv, depth, threads, groups, blocks, smem;
+  int nv, depth, threads, groups, blocks, smem, smem_most;
 };
 static NormBwdPlan norm_bwd_plan(int T, int d) {
   NormBwdPlan p;
@@ -364,6 +365,7 @@ static NormBwdPlan norm_bwd_plan(int T, int d) {
   p.groups = p.threads <= 128 ? 256 / p.threads : 1;
   const int nb = p.threads * p.groups;
   p.smem = nb * p.nv * 3 * 16 * rows * p.depth;
+  p.smem_most = (p.groups > 1 || p.depth == 3 ? 256 : 512) * p.nv * 3 * 16 * rows * p.depth;
   const int fit = 220 * 1024 / (p.smem + 2048), cap = 1536 / nb;
   const int per = fit < cap ? (fit < 1 ? 1 : fit) : cap;
   const int64_t all = ((int64_t)T + rows * p.groups - 1) / (rows * p.groups);
@@ -379,7 +381,7 @@ int launch_add_rmsnorm_backward(const NormBwdArgs& a, cudaStream_t s) {
            : p.groups > 1 ? add_rmsnorm_backward_kernel<1, 2, 2, true>
            : p.depth == 3 ? add_rmsnorm_backward_kernel<1, 2, 3, false>
                           : add_rmsnorm_backward_kernel<1, 2, 2, false>;
-  if (!allow_smem((const void*)f, p.smem)) return -1;
+  if (!allow_smem((const void*)f, p.smem, p.smem_most)) return -1;
   if (launch_kernel(f, dim3((unsigned)p.blocks), p.threads * p.groups, p.smem, 1, s, a, p.threads) != 0) return -1;
   if (!a.dw) return 0;
   return launch_kernel(add_rmsnorm_dw_kernel, dim3((unsigned)((a.d + 31) / 32)), dim3(32, 32), 0, 1, s, a.part, p.blocks,
