@@ -90,6 +90,8 @@ size_t moe_add_rmsnorm_backward_workspace_bytes(int T, int d);
  *   dx    bf16 [T][d] (out); may be dy or dh itself
  *   dw    f32 [d] (out), or NULL (then ws is not read).  Summed in a fixed
  *         order.
+ * A dx that is no finite BF16 number (a non-finite dy, dh, h, rstd or w, or an
+ * overflow) sets MOE_STATUS_NONFINITE_X; the other rows' dx are as without it.
  * Needs d % 16 == 0, 16 <= d <= 16384.  Two launches (one without dw). */
 int moe_add_rmsnorm_backward(const uint16_t* dy, const uint16_t* dh,
                              const uint16_t* h, const float* rstd,

@@ -98,7 +98,7 @@ int moe_add_rmsnorm_backward(const uint16_t* dy, const uint16_t* dh, const uint1
   if (rc != MOE_OK) return rc;
   if (T == 0)
     return finish(dw && cudaMemsetAsync(dw, 0, (size_t)d * 4, (cudaStream_t)stream) != cudaSuccess ? -1 : 0);
-  const moe::NormBwdArgs a = {dy, dh, h, rstd, w, T, d, dx, dw, static_cast<float*>(ws)};
+  const moe::NormBwdArgs a = {dy, dh, h, rstd, w, T, d, dx, dw, static_cast<float*>(ws), status};
   return finish(moe::launch_add_rmsnorm_backward(a, (cudaStream_t)stream));
 }
 

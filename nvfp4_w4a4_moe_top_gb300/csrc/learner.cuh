@@ -35,6 +35,7 @@ struct NormBwdArgs {
   uint16_t* dx;
   float* dw;
   float* part;  // dw of each block, [blocks][d]
+  int* status;
 };
 struct LogprobArgs {
   const void* logits;
@@ -150,6 +151,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The larger magnitude of each half, NaN if either is; the sign is of no use.
+__device__ __forceinline__ uint32_t max_abs_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 __device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {

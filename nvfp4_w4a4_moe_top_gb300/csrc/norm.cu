@@ -179,6 +179,9 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a
   const int group = GROUPS ? threadIdx.x / nt : 0, k = threadIdx.x - group * nt;
   const int lane = threadIdx.x & 31, nw = nt >> 5, warp0 = group * nw;  // the group's warps
   float dw[NV][8], w[NV][8];
+  // largest magnitude of the thread's dx: any input that is no finite number
+  // leaves one in its row (dh in its place)
+  uint32_t big = 0;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = k + v * nt;
@@ -278,13 +281,19 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(NormBwdArgs a
             const float m = r[q] * (y[i] * w[v][i] - x[i] * c1);
             o[i] = a.dh ? o[i] + m : m;
           }
-          if (c < n) __stcs(reinterpret_cast<uint4*>(a.dx) + t * n + c, pack(o));
+          if (c < n) {
+            const uint4 p = pack(o);
+            __stcs(reinterpret_cast<uint4*>(a.dx) + t * n + c, p);
+            big = max_abs_nan_bf16x2(max_abs_nan_bf16x2(big, p.x), p.y);
+            big = max_abs_nan_bf16x2(max_abs_nan_bf16x2(big, p.z), p.w);
+          }
         }
       }
     }
     fetch(t0 + D * step, g);  // into the slots just read
     g = g + 1 == D ? 0 : g + 1;
   }
+  if (!bf16x2_finite(big)) set_status(a.status, MOE_STATUS_NONFINITE_X);
   if (!a.dw) return;
   // the groups' parts of dw, added in order, make the block's
   if constexpr (GROUPS) {
