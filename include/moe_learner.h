@@ -14,7 +14,7 @@
  * every call enqueued on `stream`, no allocation, no synchronisation, return
  * codes checked on the host before anything is enqueued, `status` an optional
  * device int that receives MOE_STATUS_* bits, results deterministic bit for
- * bit.  Differences:
+ * bit.  Host threads may call them at the same time.  Differences:
  *   - logits and their gradients need only the alignment of their element
  *     (rows of any length and stride); every other 16-bit and byte tensor is
  *     16-byte aligned, int32 and float vectors 4-byte aligned (the stats of
@@ -68,10 +68,11 @@ size_t moe_mx8_sf_bytes(int64_t rows, int d);
  *         saturates.  Scale bytes of rows >= T are untouched.
  *   rstd  f32 [T] (out), or NULL
  * Needs d % 16 == 0 (y8: d % 128 == 0), 16 <= d <= 16384, ldx, ldr >= d and
- * multiples of 8, eps >= 0 finite.  Non-finite values of h set
+ * multiples of 8, 0 <= eps <= 1e30.  Non-finite values of h set
  * MOE_STATUS_NONFINITE_X (the row's outputs are then unspecified).  The sum of
  * squares is FP32: rows whose sum exceeds its range (|h| about 1e18 and more)
- * give y = 0, and a row of zeros with eps = 0 gives NaN.  One launch. */
+ * give y = 0; with eps = 0, rows whose squares all underflow (|h| below about
+ * 1e-23) give infinities, and NaN for their zeros.  One launch. */
 int moe_add_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* res,
                     int64_t ldr, const uint16_t* w, float eps, int T, int d,
                     uint16_t* h, uint16_t* y, uint8_t* y8, uint8_t* y8_sf,

@@ -99,8 +99,10 @@ int launch_token_logprobs(const LogprobArgs& a, cudaStream_t s);
 int launch_token_logprobs_backward(const LogprobBwdArgs& a, cudaStream_t s);
 int launch_distill(const DistillArgs& a, cudaStream_t s);
 
-// A launch whose grid may be set up while the stream's kernel before it ends
-// (kernels begin with begin_kernel), in clusters of `cluster` blocks along x.
+// A launch whose grid may be set up while the stream's kernel before it ends,
+// where that begins with begin_kernel as all kernels launched here do (after
+// any other kernel, or a copy, it starts as launches do), in clusters of
+// `cluster` blocks along x.
 template <typename... P, typename... A>
 int launch_kernel(void (*f)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t s, const A&... args) {
   cudaLaunchConfig_t cfg = {};

@@ -21,8 +21,9 @@ constexpr int kLpD = TOP ? 3 : 4;
 constexpr int kLpSlots = 16;
 // Resident grids of rows per launch at most: blocks that end early make room
 // for others (one grid of blocks that take all rows in turn waits for the
-// slowest SM: 4096 rows of 131072, 178 us against 158), and each still has a
-// next row to fetch while it ends one.
+// slowest SM: 4096 rows of 131072, 178 us against 158).  With no more rows than
+// that each group has one row, and the other blocks of its SM cover its end;
+// beyond it a group takes several and fetches the next while it ends one.
 constexpr int kLpTurns = 8;
 template <bool TOP>
 constexpr int kLpSmem = kLpThreads * (kLpU * kLpD<TOP> * 16 + (TOP ? kLpSlots * 4 : 0));
@@ -285,9 +286,9 @@ __device__ __forceinline__ void place_lists(const uint64_t* lists, int nb, int n
 
 // TH threads per row (or, for a cluster of nb = gridDim.x blocks, per part of
 // a row), the blocks taking rows in turn.  A thread keeps its own running
-// maximum and sums over its vectors; the threads meet at the row's end while
-// the next row's vectors are on their way.  The parts of a cluster meet in its
-// first block through distributed shared memory.
+// maximum and sums over its vectors; the threads meet at the row's end, with
+// the next row's vectors, if they have one, on their way.  The parts of a
+// cluster meet in its first block through distributed shared memory.
 // 4096 x 131072 BF16 with entropy: 157 us, 6.83 TB/s, 1.0 of the measured copy
 // rate (loads into registers in batches of four, two blocks per SM: 234 us,
 // waiting for them; the ring keeps 64 KB per block on the way).  With 20

@@ -57,8 +57,8 @@ struct Chunk {
 // threads per row where rows are few or long.  Two lanes share a block of 32
 // values of the 8-bit output, eight a word of four scale bytes, so codes leave
 // in 16-byte and scales in 4-byte stores.
-// 65536 x 2048: 159 us, 6.75 TB/s, 0.99 of the measured copy rate; 16384 x 2048
-// with the 8-bit output 48 us, 6.4 TB/s, 0.94.
+// 65536 x 2048: 156 us, 6.9 TB/s, 1.01 of the measured copy rate; 16384 x 2048
+// 42 us, with the 8-bit output 47.5 us, 6.4 TB/s, 0.94.
 template <int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rmsnorm_kernel(NormArgs a) {
   constexpr int kThreads = TPR < 128 ? 128 : TPR, kRows = kThreads / TPR, NW = TPR / 32;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rmsnorm_kernel(Norm
 // groups.  A group takes R rows at a time (one barrier serves R row sums);
 // each thread fetches its own columns of dy, h and dh D groups of
 // rows ahead, by asynchronous copies into shared memory that only it reads.
-// 65536 x 2048: 160 us, 6.7 TB/s, 0.98 of the measured copy rate (four rows of
+// 65536 x 2048: 161 us, 6.7 TB/s, 0.98 of the measured copy rate (four rows of
 // loads in registers and no ring: 194 us, the loads waited out at each barrier).
 // GROUPS false: one group.
 template <int NV, int R, int D, bool GROUPS>
