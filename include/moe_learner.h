@@ -165,8 +165,8 @@ int moe_token_logprobs_backward(const void* logits, int dtype, int64_t ld,
  *                   moe_token_logprobs) of the whole row, then of the part
  *                   off the list ((-inf, 0) where that has no mass)
  * s is summed off the list alone, not as 1 minus the rest, so it keeps its
- * precision when the student is peaked.  q_i > 0 with p = 0 gives +inf, and so
- * does r > 0 with s = 0; a row with no teacher entry and no teacher_lse gives
+ * precision when the student is peaked.  q_i > 0 with p = 0 (or ln p below
+ * FP32's range) gives +inf, and so does r > 0 with s = 0; a row with no teacher entry and no teacher_lse gives
  * 0; a row without a distribution gives +inf (0 where the teacher has no
  * mass).  NaN or +inf in the teacher's numbers gives NaN and
  * MOE_STATUS_NONFINITE_LOGITS.
