@@ -22,11 +22,13 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmoe_nvfp4.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_nvfp4.h")
 LEARNER_HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_learner.h")
+TOKENS_HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_tokens.h")
 
 MOE_OK, MOE_ERR_POINTER, MOE_ERR_SHAPE, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE = 0, -1, -2, -3, -4, -5
 STATUS_NONFINITE_X, STATUS_NONFINITE_LOGITS, STATUS_NONFINITE_WEIGHT = 0x1, 0x2, 0x4
-STATUS_BAD_ROUTING, STATUS_TIMEOUT, STATUS_BAD_TOKEN = 0x8, 0x10, 0x20
+STATUS_BAD_ROUTING, STATUS_TIMEOUT, STATUS_BAD_TOKEN, STATUS_BAD_SAMPLING = 0x8, 0x10, 0x20, 0x40
 LOGPROBS_MAX_TOP, DISTILL_MAX_K, DISTILL_MAX_V = 32, 256, 1 << 20
+EMBED_MAX_V, EMBED_MAX_D, SAMPLE_MAX_V = 1 << 24, 16384, 1 << 20
 
 WS_FIELDS = ["topk_ids", "topk_w", "token_slot_row", "counts", "offsets", "row_to_token",
              "amax_tok", "x_codes", "x_sf", "x_g", "h_codes", "h_sf", "h_g", "slots",
@@ -76,6 +78,10 @@ _SIGS = {
     "moe_distill_topk": (I32, [P, I32, I64, I32, I32, P, P, P, I32, F32, P, P, P, P]),
     "moe_distill_topk_backward": (I32, [P, I32, I64, I32, I32, P, P, P, I32, F32, P, P, P, I64, P, P]),
     "moe_distill_topk_train": (I32, [P, I32, I64, I32, I32, P, P, P, I32, F32, P, P, P, I64, P, P]),
+    "moe_embed_tokens": (I32, [P, P, I32, I64, I32, I32, I32, F32, P, I64, P, P]),
+    "moe_embed_tokens_backward_workspace_bytes": (SZ, [I32, I32, I32]),
+    "moe_embed_tokens_backward": (I32, [P, I64, P, I32, I32, I32, F32, I32, P, P, SZ, P, P]),
+    "moe_sample_tokens": (I32, [P, I32, I64, I32, I32] + [P] * 10),
 }
 
 _lib = None
@@ -513,6 +519,73 @@ def moe_distill_topk_train(logits, teacher_ids, teacher_logits, teacher_lse, inv
     _check("moe_distill_topk_train", lib().moe_distill_topk_train(
         *a, _tensor(g, ty.f32, (T,), "g", dev), _tensor(loss, ty.f32, (T,), "loss", dev), pd, ldd, _status(status, dev),
         _stream(stream, dev)))
+
+
+# --------------------------------------------------------------------------
+# the operators at the token ends (include/moe_tokens.h)
+# --------------------------------------------------------------------------
+def _ids(t, dtypes, what, dev):
+    """Pointer and length of a vector of token ids on device `dev`."""
+    if t.dim() != 1 or t.shape[0] > 0x7FFFFFFF:
+        raise ValueError("%s: a vector of at most 2^31 - 1 ids expected, got %s" % (what, tuple(t.shape)))
+    return _tensor(t, dtypes, t.shape, what, dev), t.shape[0]
+
+
+def moe_embed_tokens(ids, table, scale, out, status=None, stream=None):
+    """out[t] = scale * table[ids[t]] in BF16, zeros for a negative id.  The rows
+    of table [V][d] (BF16 or FP32) and out [T][d] may be strided."""
+    ty = _dt()
+    dev = _here(ids, "ids")
+    pi, T = _ids(ids, ty.i32, "ids", dev)
+    pt, ldt, (V, d) = _rows(table, ty.logits, None, "table", dev)
+    po, ldo, shape = _rows(out, ty.b16, None, "out", dev)
+    if shape[0] != T or shape[1] != d:
+        raise ValueError("out: %s expected, got %s" % ((T, d), tuple(shape)))
+    _check("moe_embed_tokens", lib().moe_embed_tokens(
+        pi, pt, 1 if table.dtype in ty.f32 else 0, ldt, T, V, d, scale, po, ldo, _status(status, dev),
+        _stream(stream, dev)))
+
+
+def embed_tokens_backward_workspace_bytes(T, V, d):
+    return int(lib().moe_embed_tokens_backward_workspace_bytes(T, V, d))
+
+
+def moe_embed_tokens_backward(dy, ids, scale, dtable, ws, accumulate=False, status=None, stream=None):
+    """Gradient of moe_embed_tokens with respect to the table, dtable [V][d] in
+    FP32: all rows written, or, with accumulate, the named rows added to.  The
+    rows of dy [T][d] may be strided."""
+    ty = _dt()
+    dev = _here(dy, "dy")
+    py, ldy, (T, d) = _rows(dy, ty.b16, None, "dy", dev)
+    if dtable.dim() != 2:
+        raise ValueError("dtable: a 2-D tensor expected, got %s" % (tuple(dtable.shape),))
+    _ints(dtable.shape, "dtable")
+    V = dtable.shape[0]
+    pws, ws_bytes = _workspace(ws, dev)
+    _check("moe_embed_tokens_backward", lib().moe_embed_tokens_backward(
+        py, ldy, _tensor(ids, ty.i32, (T,), "ids", dev), T, V, d, scale, 1 if accumulate else 0,
+        _tensor(dtable, ty.f32, (V, d), "dtable", dev), pws, ws_bytes, _status(status, dev), _stream(stream, dev)))
+
+
+def moe_sample_tokens(logits, u, tokens, inv_temperature=None, top_k=None, top_p=None, min_p=None, logprob=None,
+                      kept_logprob=None, status=None, stream=None):
+    """A token of each row of logits [T][V] (strided rows allowed), drawn with
+    the random number u[t] in [0, 1) and the row's own temperature and filters
+    (vectors [T]; None: off); its log-probability under the whole row and under
+    what the filters kept."""
+    ty = _dt()
+    f32 = ty.f32
+    dev = _here(logits, "logits")
+    pl, ld, (T, V) = _rows(logits, ty.logits, None, "logits", dev)
+    row = (T,)
+    if u is None or tokens is None:
+        raise ValueError("u and tokens are needed")
+    _check("moe_sample_tokens", lib().moe_sample_tokens(
+        pl, 1 if logits.dtype in f32 else 0, ld, T, V, _tensor(inv_temperature, f32, row, "inv_temperature", dev),
+        _tensor(top_k, ty.i32, row, "top_k", dev), _tensor(top_p, f32, row, "top_p", dev),
+        _tensor(min_p, f32, row, "min_p", dev), _tensor(u, f32, row, "u", dev), _tensor(tokens, ty.i32, row, "tokens", dev),
+        _tensor(logprob, f32, row, "logprob", dev), _tensor(kept_logprob, f32, row, "kept_logprob", dev),
+        _status(status, dev), _stream(stream, dev)))
 
 
 class Pipeline:

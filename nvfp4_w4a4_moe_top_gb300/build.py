@@ -17,9 +17,10 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmoe_nvfp4.so")
 SOURCES = ["abi.cu", "quant.cu", "route.cu", "gemm.cu", "bwd.cu", "noalloc.cu", "pipeline.cu",
-           "norm.cu", "logprob.cu", "distill.cu", "learner.cu"]
-HEADERS = ["common.cuh", "kernels.cuh", "swiglu.cuh", "exp_table.cuh", "learner.cuh",
-           os.path.join("..", "..", "include", "moe_nvfp4.h"), os.path.join("..", "..", "include", "moe_learner.h")]
+           "norm.cu", "logprob.cu", "distill.cu", "learner.cu", "embed.cu", "sample.cu", "tokens.cu"]
+HEADERS = ["common.cuh", "kernels.cuh", "swiglu.cuh", "exp_table.cuh", "learner.cuh", "tokens.cuh",
+           os.path.join("..", "..", "include", "moe_nvfp4.h"), os.path.join("..", "..", "include", "moe_learner.h"),
+           os.path.join("..", "..", "include", "moe_tokens.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

@@ -1,0 +1,346 @@
+// The embedding's rows and the gradient of its table.
+//   out_t = scale table[ids_t];   dtable_v = scale sum_{t: ids_t = v} dy_t.
+// Both are bound by HBM: the rows that tokens name in and one row per token
+// out; one row per token in and every row of the table out.
+#include "tokens.cuh"
+
+namespace moe {
+
+constexpr int kEmThreads = 256;
+
+// Vectors of 8 values: TX threads along a row (a power of two), 256 / TX rows
+// at a time, kEmRows rows per thread, their loads issued together.
+constexpr int kEmRows = 4;
+
+__device__ __forceinline__ uint4 scaled8(const uint16_t* p, float scale) {
+  float x[8];
+  unpack(*reinterpret_cast<const uint4*>(p), x);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= scale;
+  return pack(x);
+}
+__device__ __forceinline__ uint4 scaled8(const float* p, float scale) {
+  float a[4], b[4], x[8];
+  unpack(reinterpret_cast<const uint4*>(p)[0], a);
+  unpack(reinterpret_cast<const uint4*>(p)[1], b);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = a[e] * scale, x[4 + e] = b[e] * scale;
+  return pack(x);
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kEmThreads) embed_tokens_kernel(EmbedArgs a, int tx_log) {
+  const int tx = 1 << tx_log, rows = kEmThreads >> tx_log;
+  const int c = (blockIdx.y * tx + (threadIdx.x & (tx - 1))) * 8;
+  const int64_t t0 = (int64_t)blockIdx.x * rows * kEmRows + (threadIdx.x >> tx_log);
+  begin_kernel();
+  if (c >= a.d) return;
+  int id[kEmRows];
+#pragma unroll
+  for (int r = 0; r < kEmRows; ++r) id[r] = t0 + r * rows < a.T ? a.ids[t0 + r * rows] : -1;
+  uint4 v[kEmRows];
+#pragma unroll
+  for (int r = 0; r < kEmRows; ++r) {
+    v[r] = make_uint4(0u, 0u, 0u, 0u);
+    if ((unsigned)id[r] < (unsigned)a.V) v[r] = scaled8(static_cast<const E*>(a.table) + (int64_t)id[r] * a.ldt + c, a.scale);
+    else if (id[r] >= a.V && c == 0) set_status(a.status, MOE_STATUS_BAD_TOKEN);
+  }
+#pragma unroll
+  for (int r = 0; r < kEmRows; ++r)
+    if (t0 + r * rows < a.T) __stcs(reinterpret_cast<uint4*>(a.out + (t0 + r * rows) * a.ldo + c), v[r]);
+}
+
+// log2 of the threads along a row of `vecs` vectors.
+static int threads_along(int vecs) {
+  int l = 0;
+  while (l < 8 && (1 << l) < vecs) ++l;
+  return l;
+}
+
+int launch_embed_tokens(const EmbedArgs& a, cudaStream_t s) {
+  const int l = threads_along(a.d / 8), rows = (kEmThreads >> l) * kEmRows;
+  const dim3 grid((unsigned)((a.T + (int64_t)rows - 1) / rows), (unsigned)((a.d / 8 + (1 << l) - 1) >> l));
+  auto f = a.dtype == MOE_DTYPE_BF16 ? embed_tokens_kernel<uint16_t> : embed_tokens_kernel<float>;
+  return launch_kernel(f, grid, kEmThreads, 0, 1, s, a, l);
+}
+
+// ---- gradient ----
+// The tokens are sorted by id (stable, so ascending t within an id) with a
+// radix sort of up to 9 bits a pass; tiles of the sorted tokens are then summed
+// run by run.  A run inside one tile goes to the table at once; the parts of a
+// run that crosses tiles go to the workspace and are added in the order of the
+// tiles by a last launch.  Ids out of range sort behind all others, as V.
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxBits = 9, kBins = 1 << kMaxBits;
+
+struct SortPlan {
+  int passes, bits;  // bits of a digit
+  int items;         // tokens of a thread
+  int blocks;
+  int tile, tiles;   // sorted tokens summed by one group of threads
+  size_t key[2], val[2], hist[3], bitmap, part, bytes;
+};
+
+static SortPlan sort_plan(int T, int V, int d) {
+  SortPlan p;
+  int n = 1;
+  while ((int64_t(1) << n) <= V) ++n;  // ids up to V
+  p.passes = (n + kMaxBits - 1) / kMaxBits;
+  p.bits = (n + p.passes - 1) / p.passes;
+  p.items = 1;
+  while (p.items < 32 && (int64_t)p.items * kSortThreads * 128 < T) p.items *= 2;
+  const int chunk = p.items * kSortThreads;
+  p.blocks = (T + chunk - 1) / chunk;
+  p.tile = 4;
+  const int64_t cols = (d / 8 + 255) / 256;
+  while (p.tile < 32 && T / p.tile * cols > 2048) p.tile *= 2;
+  p.tiles = (T + p.tile - 1) / p.tile;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += (n + 255) / 256 * 256;
+    return o;
+  };
+  for (int i = 0; i < 2; ++i) p.key[i] = take((size_t)T * 4), p.val[i] = take((size_t)T * 4);
+  for (int i = 0; i < 3; ++i) p.hist[i] = i < p.passes ? take((size_t)p.blocks * kBins * 4) : 0;
+  p.bitmap = take((size_t)(V + 31) / 32 * 4);
+  p.part = take((size_t)p.tiles * 2 * d * 4);
+  p.bytes = at;
+  return p;
+}
+size_t embed_tokens_backward_ws(int T, int V, int d) { return sort_plan(T, V, d).bytes; }
+
+__device__ __forceinline__ int sort_key(int id, int V) { return (unsigned)id < (unsigned)V ? id : V; }
+
+// Digits of each chunk of the tokens, [chunk][bin]; clears the next passes'
+// counts and the bit map.
+__global__ void __launch_bounds__(kSortThreads)
+    embed_sort_count_kernel(const int32_t* ids, int T, int V, int items, int bits, uint32_t* hist, uint32_t* clear,
+                            int64_t clear_words, uint32_t* bitmap, int bitmap_words, int* status) {
+  __shared__ uint32_t bins[kBins];
+  const int k = threadIdx.x;
+  bins[k] = 0;
+  begin_kernel();
+  __syncthreads();
+  const int t0 = blockIdx.x * items * kSortThreads;
+  bool bad = false;
+  for (int i = 0; i < items; ++i) {
+    const int t = t0 + i * kSortThreads + k;
+    if (t < T) {
+      const int id = ids[t];
+      bad |= id >= V;
+      atomicAdd(&bins[sort_key(id, V) & ((1 << bits) - 1)], 1u);
+    }
+  }
+  if (bad) set_status(status, MOE_STATUS_BAD_TOKEN);
+  __syncthreads();
+  hist[(int64_t)blockIdx.x * kBins + k] = bins[k];
+  const int64_t n = (int64_t)gridDim.x * kSortThreads, g = (int64_t)blockIdx.x * kSortThreads + k;
+  for (int64_t i = g; i < clear_words; i += n) clear[i] = 0;
+  for (int64_t i = g; i < bitmap_words; i += n) bitmap[i] = 0;
+}
+
+// One pass: each chunk's tokens to their places by the digit at `shift`, and
+// the next digit's counts of the chunks where they land (next_hist, or NULL).
+// key_in NULL: the first pass, of the ids themselves, which also marks them in
+// the bit map.
+__global__ void __launch_bounds__(kSortThreads)
+    embed_sort_scatter_kernel(const int32_t* ids, const int32_t* key_in, const int32_t* val_in, int T, int V, int items,
+                              int bits, int shift, const uint32_t* hist, uint32_t* next_hist, uint32_t* bitmap,
+                              int32_t* key_out, int32_t* val_out) {
+  __shared__ uint32_t place[kSortWarps][kBins];
+  __shared__ uint32_t sums[kSortWarps];
+  const int k = threadIdx.x, warp = k >> 5, lane = k & 31;
+  const uint32_t mask = (1u << bits) - 1;
+  for (int w = 0; w < kSortWarps; ++w) place[w][k] = 0;
+  begin_kernel();
+  // tokens of smaller digits, and of this digit in earlier chunks
+  uint32_t before = 0, total = 0;
+  for (int b = 0; b < (int)gridDim.x; ++b) {
+    const uint32_t c = hist[(int64_t)b * kBins + k];
+    before += b < (int)blockIdx.x ? c : 0;
+    total += c;
+  }
+  uint32_t incl = total;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t n = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += n;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  uint32_t base = incl - total + before;
+  for (int w = 0; w < warp; ++w) base += sums[w];
+  // warp w takes items * 32 consecutive tokens
+  const int64_t w0 = (int64_t)blockIdx.x * items * kSortThreads + (int64_t)warp * items * 32;
+  auto load = [&](int i, int& key, int& val) {
+    const int64_t t = w0 + i * 32 + lane;
+    key = -1, val = (int)t;
+    if (t < T) {
+      if (key_in) key = key_in[t], val = val_in[t];
+      else key = sort_key(ids[t], V);
+    }
+  };
+  for (int i = 0; i < items; ++i) {
+    int key, val;
+    load(i, key, val);
+    if (key >= 0) atomicAdd(&place[warp][(key >> shift) & mask], 1u);
+  }
+  __syncthreads();
+  for (int w = 0; w < kSortWarps; ++w) {
+    const uint32_t c = place[w][k];
+    place[w][k] = base;
+    base += c;
+  }
+  __syncthreads();
+  const int chunk = items * kSortThreads;
+  for (int i = 0; i < items; ++i) {
+    int key, val;
+    load(i, key, val);
+    const uint32_t digit = key >= 0 ? (key >> shift) & mask : kBins;  // kBins: no token
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit);
+    if (key >= 0) {
+      const uint32_t at = place[warp][digit] + __popc(same & ((1u << lane) - 1));
+      key_out[at] = key;
+      val_out[at] = val;
+      if (next_hist) atomicAdd(&next_hist[(int64_t)(at / chunk) * kBins + ((key >> (shift + bits)) & mask)], 1u);
+      if (!key_in && key < V) atomicOr(&bitmap[key >> 5], 1u << (key & 31));
+    }
+    __syncwarp();
+    if (key >= 0 && lane == __ffs(same) - 1) place[warp][digit] += __popc(same);
+    __syncwarp();
+  }
+}
+
+struct SumArgs {
+  EmbedBwdArgs a;
+  const int32_t* key;
+  const int32_t* val;
+  const uint32_t* bitmap;
+  float* part;
+  int tile, tiles, sum_blocks, zero_rows;
+};
+
+__device__ __forceinline__ void put8(float* p, const float (&x)[8], float scale, bool add) {
+  float4 lo = make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale);
+  float4 hi = make_float4(x[4] * scale, x[5] * scale, x[6] * scale, x[7] * scale);
+  float4* q = reinterpret_cast<float4*>(p);
+  if (add) {
+    const float4 a = q[0], b = q[1];
+    lo.x += a.x, lo.y += a.y, lo.z += a.z, lo.w += a.w;
+    hi.x += b.x, hi.y += b.y, hi.z += b.z, hi.w += b.w;
+  }
+  __stcs(q, lo);
+  __stcs(q + 1, hi);
+}
+
+// Blocks 0 .. sum_blocks - 1: 256 / TX tiles of sorted tokens each.  The rest:
+// zeros into the rows of the table that no token names.
+__global__ void __launch_bounds__(kEmThreads) embed_sum_kernel(SumArgs s, int tx_log) {
+  const EmbedBwdArgs& a = s.a;
+  const int tx = 1 << tx_log, ty = threadIdx.x >> tx_log, rows = kEmThreads >> tx_log;
+  const int c = (blockIdx.y * tx + (threadIdx.x & (tx - 1))) * 8;
+  begin_kernel();
+  if (c >= a.d) return;
+  if ((int)blockIdx.x >= s.sum_blocks) {
+    const int v0 = ((int)blockIdx.x - s.sum_blocks) * s.zero_rows, v1 = min(a.V, v0 + s.zero_rows);
+    for (int v = v0 + ty; v < v1; v += rows)
+      if (!(s.bitmap[v >> 5] >> (v & 31) & 1)) {
+        float4* q = reinterpret_cast<float4*>(a.dtable + (int64_t)v * a.d + c);
+        __stcs(q, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        __stcs(q + 1, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+      }
+    return;
+  }
+  const int64_t tile = (int64_t)blockIdx.x * rows + ty;
+  if (tile >= s.tiles) return;
+  const int64_t p0 = tile * s.tile, p1 = p0 + s.tile < a.T ? p0 + s.tile : a.T;
+  int cur = s.key[p0];
+  bool from = p0 > 0 && s.key[p0 - 1] == cur;  // the run began in an earlier tile
+  const int next = p1 < a.T ? s.key[p1] : -1;
+  float acc[8] = {};
+  for (int64_t p = p0; p < p1; p += 4) {
+    int id[4];
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      id[i] = p + i < p1 ? s.key[p + i] : -1;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (id[i] >= 0 && id[i] < a.V) v[i] = __ldcs(reinterpret_cast<const uint4*>(a.dy + (int64_t)s.val[p + i] * a.ldy + c));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (id[i] < 0) break;
+      if (id[i] != cur) {
+        if (cur < a.V) {
+          if (from) put8(s.part + (tile * 2) * a.d + c, acc, 1.0f, false);
+          else put8(a.dtable + (int64_t)cur * a.d + c, acc, a.scale, a.accumulate);
+        }
+        cur = id[i], from = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+      }
+      float x[8];
+      unpack(v[i], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += x[e];
+    }
+  }
+  if (cur < a.V) {
+    if (from) put8(s.part + (tile * 2) * a.d + c, acc, 1.0f, false);
+    else if (next == cur) put8(s.part + (tile * 2 + 1) * a.d + c, acc, 1.0f, false);
+    else put8(a.dtable + (int64_t)cur * a.d + c, acc, a.scale, a.accumulate);
+  }
+}
+
+// The parts of each run that begins in a tile and ends in a later one, added in
+// the order of the tiles.
+__global__ void __launch_bounds__(kEmThreads) embed_join_kernel(SumArgs s, int tx_log) {
+  const EmbedBwdArgs& a = s.a;
+  const int tx = 1 << tx_log, rows = kEmThreads >> tx_log;
+  const int c = (blockIdx.y * tx + (threadIdx.x & (tx - 1))) * 8;
+  const int64_t tile = (int64_t)blockIdx.x * rows + (threadIdx.x >> tx_log);
+  begin_kernel();
+  if (c >= a.d || tile + 1 >= s.tiles) return;
+  const int64_t p0 = tile * s.tile, p1 = p0 + s.tile;
+  const int id = s.key[p1 - 1];
+  if (id >= a.V || s.key[p1] != id) return;                        // no run goes on into the next tile
+  if (s.key[p0] == id && p0 > 0 && s.key[p0 - 1] == id) return;    // it began in an earlier one
+  float acc[8];
+  const float* own = s.part + (tile * 2 + 1) * a.d + c;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = own[e];
+  for (int64_t j = tile + 1; j < s.tiles && s.key[j * s.tile] == id; ++j) {
+    const float* p = s.part + j * 2 * a.d + c;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += p[e];
+  }
+  put8(a.dtable + (int64_t)id * a.d + c, acc, a.scale, a.accumulate);
+}
+
+int launch_embed_tokens_backward(const EmbedBwdArgs& a, cudaStream_t s) {
+  const SortPlan p = sort_plan(a.T, a.V, a.d);
+  auto ints = [&](size_t o) { return reinterpret_cast<int32_t*>(a.ws + o); };
+  auto words = [&](size_t o) { return reinterpret_cast<uint32_t*>(a.ws + o); };
+  int rc = launch_kernel(embed_sort_count_kernel, p.blocks, kSortThreads, 0, 1, s, a.ids, a.T, a.V, p.items, p.bits,
+                         words(p.hist[0]), words(p.hist[1]),
+                         p.passes > 1 ? (int64_t)(p.bitmap - p.hist[1]) / 4 : int64_t(0), words(p.bitmap), (a.V + 31) / 32,
+                         a.status);
+  for (int i = 0; i < p.passes && rc == 0; ++i)
+    rc = launch_kernel(embed_sort_scatter_kernel, p.blocks, kSortThreads, 0, 1, s, a.ids,
+                       i ? ints(p.key[(i - 1) & 1]) : nullptr, i ? ints(p.val[(i - 1) & 1]) : nullptr, a.T, a.V, p.items,
+                       p.bits, i * p.bits, words(p.hist[i]), i + 1 < p.passes ? words(p.hist[i + 1]) : nullptr,
+                       words(p.bitmap), ints(p.key[i & 1]), ints(p.val[i & 1]));
+  if (rc != 0) return rc;
+  const int last = (p.passes - 1) & 1, l = threads_along(a.d / 8), rows = kEmThreads >> l;
+  SumArgs m = {a, ints(p.key[last]), ints(p.val[last]), words(p.bitmap), reinterpret_cast<float*>(a.ws + p.part),
+               p.tile, p.tiles, (p.tiles + rows - 1) / rows, 32 * rows};
+  const unsigned cols = (unsigned)((a.d / 8 + (1 << l) - 1) >> l);
+  const unsigned zero = a.accumulate ? 0u : (unsigned)((a.V + (int64_t)m.zero_rows - 1) / m.zero_rows);
+  rc = launch_kernel(embed_sum_kernel, dim3((unsigned)m.sum_blocks + zero, cols), kEmThreads, 0, 1, s, m, l);
+  if (rc != 0) return rc;
+  return launch_kernel(embed_join_kernel, dim3((unsigned)m.sum_blocks, cols), kEmThreads, 0, 1, s, m, l);
+}
+
+}  // namespace moe
