@@ -10,8 +10,10 @@
 // result is one.
 //
 // There are two kinds of weights.  Weights from FP32 exponentials make sums with
-// a relative error below delta (see row_delta); a decision that is nearer to its
-// border than that is made again with weights to about 2^-37.
+// a bounded relative error (sum_error); a row with a decision that is nearer to
+// its border than that, and a row that keeps too many elements for a list, is left
+// to a second launch, in which eight blocks together decide it with weights to
+// about 2^-34.
 #include "exp_table.cuh"
 #include "tokens.cuh"
 
@@ -20,14 +22,18 @@ namespace moe {
 constexpr int kSaU = 4;     // vectors read together
 constexpr int kSaD = 2;     // groups of them on the way
 constexpr int kSaRuns = 8;  // runs of a thread at most
-constexpr int kSaBins = 2048;
 constexpr int kSaNear = 1024;  // bins of the sixteen powers of two below the maximum
 constexpr float kMinExponent = -42.0f;  // weights below 2^-42 count as 0
+// In tokens: left to the second launch, kOpen - ceil(log2(the row's weight)).
+constexpr int kOpen = -2;
 
+// In parts of 27 bits, 32 of which add up in a word.
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
+  constexpr uint32_t k27 = (1u << 27) - 1;
+  const uint32_t a = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)v & k27);
+  const uint32_t b = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)(v >> 27) & k27);
+  const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)(v >> 54));
+  return a + ((uint64_t)b << 27) + ((uint64_t)c << 54);
 }
 
 // total p for 0 <= p < 1, rounded down or up to a whole number.
@@ -41,26 +47,40 @@ __device__ __forceinline__ uint64_t part_of(uint64_t total, float p) {
   return (hi >> down) + (UP && rest ? 1 : 0);
 }
 
+// w as a fixed-point number of unit 2^-s, 43 <= s <= 52, 0 <= w < 2^11.
+__device__ __forceinline__ uint64_t fixed(float w, int s) {
+  const int e = (int)(__float_as_uint(w) >> 23) - 127;
+  const uint64_t v = ((__float_as_uint(w) & 0x7FFFFFu) | 0x800000u);
+  return e < -s ? 0 : e + s >= 23 ? v << (e + s - 23) : v >> (23 - e - s);
+}
+
 template <int TH>
 struct SampleShared {
   static constexpr int NW = TH / 32, kList = TH < 1024 ? 2 * TH : TH;
   uint64_t exp2[64];               // 2^(j/64) 2^62
   uint64_t part[kSaRuns + 2][NW];  // sums of the runs by warp; the row's ends
-  uint64_t pre[kSaRuns + 3];       // what comes before each of them
+  uint64_t sums[kSaRuns + 2];      // of all warps
   uint64_t scan[2][NW];
   float wmax[NW];
   float edge[2];  // ln(min_p) / inv_temperature, a pair
   // results that one thread finds for all
-  uint64_t target, key, incl, before, after, base_n, base_w;
-  uint32_t found, listed;
-  int bin, sure_bin, id, kept;
+  uint64_t target, before, after, left;
+  uint32_t found, listed, hot;
+  int bin, id, kept, at;
   float x;
 };
 // What shares its memory with the ring that the logits come through.
 template <int TH>
 struct SampleWork {
+  static constexpr int kHot = 1024;
   uint64_t list[SampleShared<TH>::kList], weight[SampleShared<TH>::kList];
-  uint32_t lo[kSaBins], hi[kSaBins];
+  union {
+    struct {
+      uint32_t lo[kSaNear], hi[kSaNear];
+    };
+    uint32_t hot[kHot];      // thread, run << 16
+    uint64_t group[kSaNear]; // sums of 32 vectors of one run, of 2^15 vectors at most
+  };
 };
 template <int TH>
 constexpr int kSaRing = TH * kSaU * kSaD * 16;
@@ -87,7 +107,7 @@ struct Weights {
   static __device__ __forceinline__ uint64_t mantissa(float w) { return (__float_as_uint(w) & 0x7FFFFFu) | 0x800000u; }
   __device__ __forceinline__ uint64_t fast(float x) const {
     const float w = ratio(x);  // in [0, 1]
-    return w > 0.0f ? mantissa(w) << (s - 23) >> (127 - (int)(__float_as_uint(w) >> 23)) : 0;
+    return fixed(w, s);
   }
   // To about 2^-37: the exponent is formed from the exact difference x - m as a
   // pair of floats and split into a multiple of 1/64, whose power is read from a
@@ -114,23 +134,76 @@ struct Weights {
     const int down = 62 - s - (i >> 6);
     return (w + (1ull << (down - 1))) >> down;
   }
-  template <bool EXACT>
-  __device__ __forceinline__ uint64_t of(float x) const {
-    return EXACT ? exact(x) : fast(x);
-  }
 };
 
-// A bound of the relative error of sums of fast weights, of a row whose V
-// weights sum to S >= 1.  A weight 2^-t, t >= 0, is off by the exponential's
-// 2^-22, by less than 3 2^-24 t ln 2 from the roundings of its exponent (the
-// difference, c, the product), and by the additions: 18 2^-24 at most (10 in a
-// batch, one per batch of a run), and the change from the batches' shift to m,
-// 2^-21.  The mean of t over the weights is at most (S - 1) / S log2(V / (S -
-// 1)), its value where all but the first are equal.
-__device__ __forceinline__ float row_delta(float S, int V) {
+// Bounds of the relative error of a row's sums of V weights with sum S >= 1.  The
+// exponential is off by 2^-22 of itself.  A weight 2^-t, t >= 0, is off by t ln 2
+// times each relative error of its exponent: 2^-24 for each rounding (one in the
+// pass over the row, the difference and the product in a weight by itself), and
+// the part of c that ch leaves out.  (t up to 1 larger in the pass, whose weights
+// are about the shift.)  The mean of t over the weights is at most (S - 1) / S
+// log2(V / (S - 1)), its value where all but the first are equal.  `adds`: the
+// FP32 additions that an element goes through.
+__device__ __forceinline__ float sum_error(float S, int V, const float cl_over_ch, int roundings, int adds) {
   const float rest = fmaxf(S - 1.0f, 1e-12f);
-  return 0x1p-19f + 0x1p-22f * (rest / S * log2f((float)V / rest) + 1.0f);
+  const float t = __fdividef(rest, S) * __log2f(__fdividef((float)V, rest)) + 1.01f;
+  return 0x1p-22f + 0x1p-24f * (float)adds + 0.7f * t * (0x1p-24f * (float)roundings + cl_over_ch);
 }
+
+// Maximum and sum of a run in the pass over the row: about its own integer
+// shift, as Run's (learner.cuh), with four sums of pairs for a batch of vectors,
+// so that an element goes through few additions.
+struct RunSum {
+  float m = neg_inf(), M = -kShiftLimit, s = 0.0f;
+  static __device__ __forceinline__ float shift_of(float m, float c) {
+    return fmaxf(ceilf(fmaxf(m, kLowest) * c), -kShiftLimit);
+  }
+  __device__ __forceinline__ void raise(float x, float c) {
+    m = max_nan(m, x);
+    const float n = shift_of(m, c);
+    s *= exp2_fast(M - n);
+    M = n;
+  }
+  template <int N>
+  __device__ __forceinline__ void take(const uint64_t (&x)[N], float c) {
+    const uint64_t nM2 = f32x2_pack(-M, -M), c2 = f32x2_pack(c, c);
+    uint64_t w[4] = {0ull, 0ull, 0ull, 0ull}, none[1] = {0ull};
+#pragma unroll
+    for (int i = 0; i < N; ++i) Run<false>::step(x[i], c2, nM2, w[i & 3], none[0]);
+    float a, b;
+    unpack2(add_f32x2(add_f32x2(w[0], w[1]), add_f32x2(w[2], w[3])), a, b);
+    s += a + b;
+  }
+  template <int U>
+  __device__ __forceinline__ void add(const uint4 (&v)[U], float c, uint16_t) {
+    uint32_t w[4 * U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[4 * u] = v[u].x, w[4 * u + 1] = v[u].y, w[4 * u + 2] = v[u].z, w[4 * u + 3] = v[u].w;
+    uint32_t mx[4] = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+    for (int i = 4; i < 4 * U; ++i) mx[i & 3] = max_nan_bf16x2(mx[i & 3], w[i]);
+    const uint32_t mp = max_nan_bf16x2(max_nan_bf16x2(mx[0], mx[1]), max_nan_bf16x2(mx[2], mx[3]));
+    raise(max_nan(bf16_lo(mp), bf16_hi(mp)), c);
+    uint64_t x[4 * U];
+#pragma unroll
+    for (int i = 0; i < 4 * U; ++i) x[i] = f32x2_pack(bf16_lo(w[i]), bf16_hi(w[i]));
+    take(x, c);
+  }
+  template <int U>
+  __device__ __forceinline__ void add(const uint4 (&v)[U], float c, float) {
+    uint64_t x[2 * U];
+    float mx = neg_inf();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float a = __uint_as_float(v[u].x), b = __uint_as_float(v[u].y), d = __uint_as_float(v[u].z),
+                  e = __uint_as_float(v[u].w);
+      mx = max_nan(mx, max_nan(max_nan(a, b), max_nan(d, e)));
+      x[2 * u] = f32x2_pack(a, b), x[2 * u + 1] = f32x2_pack(d, e);
+    }
+    raise(mx, c);
+    take(x, c);
+  }
+};
 
 // A row's elements in the order of the ids: the elements in front of the
 // vectors, the vectors in runs, the elements after them.  Run q of thread k:
@@ -181,7 +254,7 @@ struct SampleRow {
     if ((int)threadIdx.x < r.tail) f(to_f32(r.p[id]), id);
   }
   // Runs without a logit of rank `least` are skipped.
-  __device__ __forceinline__ bool has(int q, uint32_t least) const { return rank_value(high[q * TH]) >= least; }
+  __device__ __forceinline__ bool has(int q, uint32_t least) const { return least == 0 || rank_value(high[q * TH]) >= least; }
   template <typename F>
   __device__ __forceinline__ void all(uint32_t least, F f) const {
     front(f);
@@ -211,110 +284,150 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t& total, Samp
   return incl - v + warp_sum64(lane < warp ? w : 0);
 }
 
-// The first id up to which the sum of whole numbers over the row is above
-// target(sum over the row): sh.id, sh.x, and the sum before and with it,
-// sh.before, sh.after.  own(q): this thread's sum of run q; f(x, id) one
-// element's.  sh.id = -1 where the elements of the run do not reach what its
-// sum says (fast weights).  Returns the sum over the row.
-template <typename E, int TH, typename S, typename F, typename G>
-__device__ __forceinline__ uint64_t pick(const SampleRow<E, TH>& row, S own, F f, G target_of, SampleShared<TH>& sh,
-                                         int& turn) {
+// The part of the row with the target: e = 0 the elements before the vectors, 1
+// + q run q, then the elements after them.  Finds in it the first id up to which
+// the sum of f(x, id) is above `left`; `first`: the sum before the part.  sh.id
+// (-1 if the elements do not reach it), sh.x, and the sum over the row before and
+// with that element, sh.before, sh.after.
+template <typename E, int TH, typename F>
+__device__ __forceinline__ void pick_in(const SampleRow<E, TH>& row, int e, uint64_t left, uint64_t first, F f,
+                                        SampleShared<TH>& sh, uint64_t* group, int& turn) {
   constexpr int NW = TH / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t v = 0;
-  auto add = [&](float x, int id) { v += f(x, id); };
-  for (int q = 0; q < row.runs; ++q) {
-    v = warp_sum64(own(q));
-    if (lane == 0) sh.part[q + 1][warp] = v;
-  }
-  if (warp == 0) {
-    v = 0;
-    row.front(add);
-    v = warp_sum64(v);
-    if (lane == 0) sh.part[0][0] = v;
-    v = 0;
-    row.back(add);
-    v = warp_sum64(v);
-    if (lane == 0) sh.part[row.runs + 1][0] = v;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    uint64_t sum = 0;
-    for (int e = 0; e < row.runs + 2; ++e) {
-      const int n = e == 0 || e == row.runs + 1 ? 1 : NW;
-      v = warp_sum64(lane < n ? sh.part[e][lane] : 0);
-      if (lane == 0) sh.pre[e] = sum;
-      sum += v;
-    }
-    if (lane == 0) {
-      sh.pre[row.runs + 2] = sum;
-      const uint64_t t = target_of(sum);
-      sh.target = t < sum ? t : sum - 1;  // sum > 0
-      sh.id = -1;
-    }
-  }
-  __syncthreads();
-  const uint64_t total = sh.pre[row.runs + 2], target = sh.target;
-  int e = 0;
-  while (e < row.runs + 1 && sh.pre[e + 1] <= target) ++e;
-  const uint64_t first = sh.pre[e];
-  uint64_t left = target - first;
-  // walks the elements of one part of the row in order
-  bool done = false;
-  auto walk = [&](float x, int id) {
+  auto walk = [&](float x, int id, uint64_t& before, bool& done) {
     const uint64_t w = f(x, id);
-    if (!done && w > left) {
+    if (!done && before + w > left) {
       done = true;
-      sh.id = id;
-      sh.x = x;
-      sh.before = target - left;
-      sh.after = target - left + w;
+      sh.id = id, sh.x = x;
+      sh.before = first + before, sh.after = first + before + w;
     }
-    left -= w;
+    before += w;
   };
+  if (threadIdx.x == 0) sh.id = -1, sh.at = -1;
   if (e == 0 || e == row.runs + 1) {
     if (threadIdx.x == 0) {
       const int i0 = e == 0 ? 0 : row.r.tail_start(), n = e == 0 ? row.r.head : row.r.tail;
-      for (int i = 0; i < n && !done; ++i) walk(to_f32(row.r.p[i0 + i]), i0 + i);
+      uint64_t before = 0;
+      bool done = false;
+      for (int i = 0; i < n && !done; ++i) walk(to_f32(row.r.p[i0 + i]), i0 + i, before, done);
     }
-  } else {  // thread k takes `per` vectors in a row
-    const int i0 = ((e - 1) * TH + (int)threadIdx.x) * row.per, i1 = min(i0 + row.per, row.r.nvec);
-    v = 0;
-    for (int i = i0; i < i1; ++i) row.vector(row.r.vec()[i], i, add);
-    uint64_t sum;
-    const uint64_t before = block_scan<TH>(v, sum, sh, turn);
-    if (before <= left && left < before + v) {
-      left -= before;
-      for (int i = i0; i < i1 && !done; ++i) row.vector(row.r.vec()[i], i, walk);
+    __syncthreads();
+    return;
+  }
+  // sums of 32 vectors in a row, then the vectors, then the elements
+  const int start = (e - 1) * row.per * TH;
+  for (int j = 0; j < row.per; j += kSaU) {
+    uint4 v[kSaU];
+    const int i0 = start + j * TH + (int)threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < kSaU; ++u) v[u] = row.r.vec()[min(i0 + u * TH, row.r.nvec - 1)];
+#pragma unroll
+    for (int u = 0; u < kSaU; ++u) {
+      uint64_t w = 0;
+      if (i0 + u * TH < row.r.nvec) row.vector(v[u], i0 + u * TH, [&](float x, int id) { w += f(x, id); });
+      w = warp_sum64(w);
+      if (lane == 0) group[(j + u) * NW + warp] = w;
     }
   }
   __syncthreads();
+  const int n = row.per * NW, each = (n + TH - 1) / TH, g0 = (int)threadIdx.x * each;
+  uint64_t sum = 0, total;
+  for (int g = g0; g < min(g0 + each, n); ++g) sum += group[g];
+  uint64_t before = block_scan<TH>(sum, total, sh, turn);
+  if (before <= left && left < before + sum) {
+    int g = g0;
+    while (before + group[g] <= left) before += group[g++];
+    sh.at = g, sh.left = before;
+  }
+  __syncthreads();
+  if (warp == 0 && sh.at >= 0) {
+    const int i = start + sh.at * 32 + lane;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    uint64_t w = 0;
+    if (i < row.r.nvec) {
+      v = row.r.vec()[i];
+      row.vector(v, i, [&](float x, int id) { w += f(x, id); });
+    }
+    uint64_t incl = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t m = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += m;
+    }
+    uint64_t b = sh.left + incl - w;
+    if (b <= left && left < b + w) {
+      bool done = false;
+      row.vector(v, i, [&](float x, int id) { walk(x, id, b, done); });
+    }
+  }
+  __syncthreads();
+}
+
+// sh.part summed over the warps; the row's sum.  After the barrier that follows
+// the last of sh.part.
+template <typename E, int TH>
+__device__ __forceinline__ uint64_t sum_parts(const SampleRow<E, TH>& row, SampleShared<TH>& sh) {
+  constexpr int NW = TH / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int e = warp; e < row.runs + 2; e += NW) {
+    const int n = e == 0 || e == row.runs + 1 ? 1 : NW;
+    const uint64_t v = warp_sum64(lane < n ? sh.part[e][lane] : 0);
+    if (lane == 0) sh.sums[e] = v;
+  }
+  __syncthreads();
+  uint64_t total = 0;
+  for (int e = 0; e < row.runs + 2; ++e) total += sh.sums[e];
   return total;
 }
-// The same with the runs' sums from their elements; runs without a logit of
-// rank `least` add nothing.
-template <typename E, int TH, typename F, typename G>
-__device__ __forceinline__ uint64_t pick_all(const SampleRow<E, TH>& row, uint32_t least, F f, G target_of,
-                                             SampleShared<TH>& sh, int& turn) {
-  return pick<E, TH>(row, [&](int q) {
-    uint64_t v = 0;
-    if (row.has(q, least)) row.run(q, [&](float x, int id) { v += f(x, id); });
-    return v;
-  }, f, target_of, sh, turn);
+
+// The part with the target, from sh.sums.
+template <typename E, int TH>
+__device__ __forceinline__ int find_part(const SampleRow<E, TH>& row, uint64_t target, uint64_t& first,
+                                         const SampleShared<TH>& sh) {
+  int e = 0;
+  first = 0;
+  while (e < row.runs + 1 && first + sh.sums[e] <= target) first += sh.sums[e++];
+  return e;
 }
 
-// Bins of the distance below the row's maximum in the order of rank_value: by
-// 1/64 of a power of two over sixteen of them, then by half of one.
-__device__ __forceinline__ int first_bin(uint32_t d) {
-  return d < (1u << 27) ? (int)(d >> 17) : kSaNear + (int)((d - (1u << 27)) >> 22);
-}
-__device__ __forceinline__ uint32_t first_bin_start(int b) {
-  return b < kSaNear ? (uint32_t)b << 17 : (1u << 27) + ((uint32_t)(b - kSaNear) << 22);
+// The ends of the row into sh.part, by the first warp.
+template <typename E, int TH, typename F>
+__device__ __forceinline__ void sum_ends(const SampleRow<E, TH>& row, F f, SampleShared<TH>& sh) {
+  if (threadIdx.x >= 32) return;
+  uint64_t a = 0, b = 0;
+  if (row.r.head) row.front([&](float x, int id) { a = f(x, id); });
+  if (row.r.tail) row.back([&](float x, int id) { b = f(x, id); });
+  if (row.r.head) a = warp_sum64(a);
+  if (row.r.tail) b = warp_sum64(b);
+  if (threadIdx.x == 0) sh.part[0][0] = a, sh.part[row.runs + 1][0] = b;
 }
 
-// n distinct keys, descending, in list (room for kList).
+// The first id up to which the sum of whole numbers over the row is above
+// target_of(sum over the row), as pick_in gives it, with the target in
+// sh.target.  own(q): this thread's sum of run q; f(x, id) one element's; group:
+// room for the sums within a run, in use by nobody.  Returns the sum over the
+// row, which is not 0.
+template <typename E, int TH, typename S, typename F, typename G>
+__device__ __forceinline__ uint64_t pick(const SampleRow<E, TH>& row, S own, F f, G target_of, SampleShared<TH>& sh,
+                                         uint64_t* group, int& turn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int q = 0; q < row.runs; ++q) {
+    const uint64_t v = warp_sum64(own(q));
+    if (lane == 0) sh.part[q + 1][warp] = v;
+  }
+  sum_ends<E, TH>(row, f, sh);
+  __syncthreads();
+  const uint64_t total = sum_parts<E, TH>(row, sh);
+  const uint64_t target = min((unsigned long long)target_of(total), (unsigned long long)total - 1);
+  uint64_t first;
+  const int e = find_part<E, TH>(row, target, first, sh);
+  if (threadIdx.x == 0) sh.target = target;
+  pick_in<E, TH>(row, e, target - first, first, f, sh, group, turn);
+  return total;
+}
+// n distinct keys, descending, in list (room for the next power of two).
 template <int TH>
-__device__ __forceinline__ void sort_list(uint64_t* list, int n) {
+__device__ __noinline__ void sort_list(uint64_t* list, int n) {
   const int k = threadIdx.x;
   if (n <= 256 && n <= TH) {  // each key's place by counting the larger ones
     const uint64_t key = k < n ? list[k] : 0;
@@ -341,10 +454,10 @@ __device__ __forceinline__ void sort_list(uint64_t* list, int n) {
     }
 }
 
-// Sums of the n weights up to and with each, in their place; returns their sum.
-template <int TH>
+// Sums of the n <= LIST weights up to and with each, in their place.
+template <int LIST, int TH>
 __device__ __forceinline__ void sum_list(uint64_t* weight, int n, SampleShared<TH>& sh, int& turn) {
-  constexpr int PER = SampleShared<TH>::kList / TH;
+  constexpr int PER = LIST / TH;
   uint64_t w[PER], v = 0, total;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -361,126 +474,6 @@ __device__ __forceinline__ void sum_list(uint64_t* weight, int n, SampleShared<T
   __syncthreads();
 }
 
-// The last element of the shortest leading part, in the order of the keys and
-// of the keys >= least, that holds `target` elements (COUNT) or weight: its key
-// in sh.key, the weight up to and with it in sh.incl, what comes before it in
-// sh.before.  False if all together do not.  target >= 1.  With fast weights
-// sh.sure_bin is the first bin of distances whose elements may or may not be in
-// that part, given an error `err` of the weights.
-template <bool COUNT, bool EXACT, typename E, int TH>
-__device__ __noinline__ bool select(const SampleRow<E, TH>& row, const Weights& weight, uint64_t target,
-                                    uint64_t least, uint32_t skip, uint64_t err, SampleShared<TH>& sh,
-                                    SampleWork<TH>& work, int& turn) {
-  constexpr int PER = kSaBins / TH, kList = SampleShared<TH>::kList;
-  const uint32_t top = rank_value(weight.m);
-  const int up = COUNT || EXACT ? 0 : weight.s - 31;  // unit of the bins' weights: 2^-31 for fast ones
-  uint32_t d0 = 0, d1 = 0xFFFFFFFFu;  // distances in question
-  uint64_t base_n = 0, base_w = 0;    // elements (COUNT) or weight before them
-  for (int level = 0;; ++level) {
-    int shift = 0;
-    while (((d1 - d0) >> shift) >= (uint32_t)kSaBins) ++shift;
-    for (int b = threadIdx.x; b < kSaBins; b += TH) work.lo[b] = 0, work.hi[b] = 0;
-    if (threadIdx.x == 0) sh.found = 0, sh.listed = 0;
-    __syncthreads();
-    row.all(skip, [&](float x, int id) {
-      const uint64_t key = rank_key(x, (uint32_t)id);
-      const uint32_t d = top - (uint32_t)(key >> 32);
-      if (x == neg_inf() || key < least || d < d0 || d > d1) return;
-      const int b = level == 0 ? first_bin(d) : (int)((d - d0) >> shift);
-      if (COUNT) {
-        atomicAdd(&work.lo[b], 1u);
-      } else if (EXACT) {
-        const uint64_t w = weight.exact(x);
-        if (w) add64(&work.lo[b], &work.hi[b], w);
-      } else {
-        const float w = weight.ratio(x);
-        const uint32_t v = (uint32_t)Weights::mantissa(w) << 8 >> min(31, 127 - (int)(__float_as_uint(w) >> 23));
-        if (w > 0.0f && v) {
-          const uint32_t was = atomicAdd(&work.lo[b], v);
-          if (was + v < was) atomicAdd(&work.hi[b], 1u);
-        }
-      }
-    });
-    __syncthreads();
-    auto bin = [&](int b) { return ((uint64_t)work.hi[b] << 32 | work.lo[b]) << up; };
-    uint64_t n = 0, total;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) n += bin(threadIdx.x * PER + i);
-    uint64_t n0 = (COUNT ? base_n : base_w) + block_scan<TH>(n, total, sh, turn);
-    const uint64_t low = target > err ? target - err : 0;  // what is certainly in the part
-    if (!COUNT && level == 0 && n0 < low && low <= n0 + n) {
-      uint64_t c = n0;
-      int i = 0;
-      while (i < PER - 1 && c + bin(threadIdx.x * PER + i) < low) c += bin(threadIdx.x * PER + i++);
-      sh.sure_bin = threadIdx.x * PER + i;
-    }
-    if (!COUNT && level == 0 && threadIdx.x == 0 && low == 0) sh.sure_bin = 0;
-    if (n0 < target && target <= n0 + n) {
-      int i = 0;
-      while (i < PER - 1 && n0 + bin(threadIdx.x * PER + i) < target) n0 += bin(threadIdx.x * PER + i++);
-      sh.found = 1, sh.bin = threadIdx.x * PER + i;
-      sh.base_n = n0;
-    }
-    __syncthreads();
-    if (!sh.found) return false;
-    const int b = sh.bin;
-    (COUNT ? base_n : base_w) = sh.base_n;
-    if (level == 0) {
-      d0 = first_bin_start(b);
-      d1 = b + 1 < kSaBins ? first_bin_start(b + 1) - 1 : 0xFFFFFFFFu;
-    } else {
-      const uint32_t start = d0 + ((uint32_t)b << shift), rest = d1 - start, width = (1u << shift) - 1;
-      d0 = start;
-      d1 = start + min(rest, width);
-    }
-    // the elements of the bin, if they are few
-    row.all(skip, [&](float x, int id) {
-      const uint64_t key = rank_key(x, (uint32_t)id);
-      const uint32_t d = top - (uint32_t)(key >> 32);
-      if (x != neg_inf() && key >= least && d >= d0 && d <= d1) {
-        const uint32_t at = atomicAdd(&sh.listed, 1u);
-        if (at < (uint32_t)kList) work.list[at] = key;
-      }
-    });
-    __syncthreads();
-    const int in = (int)sh.listed;
-    if (in <= kList) {
-      sort_list<TH>(work.list, in);
-      if constexpr (COUNT) {
-        if (threadIdx.x == 0) sh.key = work.list[target - base_n - 1];
-      } else {
-        for (int j = threadIdx.x; j < in; j += TH) work.weight[j] = weight.exact(rank_logit(work.list[j]));
-        __syncthreads();
-        sum_list<TH>(work.weight, in, sh, turn);
-        // the first that reaches the target; the last where the fast weights of
-        // the bins reached it and these do not
-        for (int j = threadIdx.x; j < in; j += TH) {
-          const uint64_t before = base_w + (j ? work.weight[j - 1] : 0), incl = base_w + work.weight[j];
-          if (before < target && (target <= incl || j == in - 1))
-            sh.key = work.list[j], sh.incl = incl, sh.before = before;
-        }
-      }
-      __syncthreads();
-      return true;
-    }
-    if (d0 == d1) {  // ties: the first of them in the order of the ids
-      const uint32_t value = top - d0;
-      const uint64_t w1 = COUNT ? 1 : max(1ull, (unsigned long long)weight.exact(rank_logit((uint64_t)value << 32)));
-      uint64_t take = COUNT ? target - base_n : (target - base_w + w1 - 1) / w1;
-      take = max(1ull, min((unsigned long long)take, (unsigned long long)in));
-      pick_all<E, TH>(row, skip, [&](float x, int id) {
-        return (uint64_t)(x != neg_inf() && rank_value(x) == value && rank_key(x, (uint32_t)id) >= least);
-      }, [&](uint64_t) { return take - 1; }, sh, turn);
-      if (threadIdx.x == 0) {
-        sh.key = rank_key(sh.x, (uint32_t)sh.id);
-        sh.incl = base_w + take * w1, sh.before = sh.incl - w1;
-      }
-      __syncthreads();
-      return true;
-    }
-  }
-}
-
 struct Filters {
   float inv_t, u, top_p, min_p;
   int top_k;  // 0: off
@@ -491,53 +484,50 @@ struct Drawn {
   uint64_t total, kept;  // weight of the row and of what is kept
 };
 
-// A row whose kept elements are too many for a list.  False where fast weights
-// leave the decision open.
-template <bool EXACT, typename E, int TH>
-__device__ __noinline__ bool draw_many(const SampleRow<E, TH>& row, const Weights& weight, const Filters& a, int V,
-                                       uint64_t total, uint64_t err, uint64_t edge, uint32_t skip, Drawn& out,
-                                       SampleShared<TH>& sh, SampleWork<TH>& work, int& turn) {
-  uint64_t least = 0, mass = total, sum;  // kept: keys from least on
-  if (EXACT && a.top_k == 0 && a.top_p < 1.0f) {
-    mass = 0;
-    row.all(0, [&](float x, int) { mass += weight.exact(x); });
-    block_scan<TH>(mass, sum, sh, turn);
-    mass = out.total = sum;
-  }
-  if (a.top_k > 0 && select<true, EXACT, E, TH>(row, weight, (uint64_t)a.top_k, 0, skip, 0, sh, work, turn))
-    least = sh.key;
-  uint32_t sure = 0xFFFFFFFFu;  // elements nearer to the maximum than this are kept for certain
-  if (a.top_p < 1.0f) {
-    if (a.top_k > 0) {
-      uint64_t v = 0;
-      row.all(max(skip, (uint32_t)(least >> 32)),
-              [&](float x, int id) { v += rank_key(x, (uint32_t)id) >= least ? weight.of<EXACT>(x) : 0; });
-      block_scan<TH>(v, mass, sh, turn);
-    }
-    const uint64_t target = max(1ull, (unsigned long long)part_of<true>(mass, fmaxf(a.top_p, 0.0f)));
-    // the sums of the bins, of unit 2^-31, lose less than one unit per element
-    const uint64_t open = EXACT ? 0 : 2 * err + ((uint64_t)V << (weight.s - 31));
-    if (select<false, EXACT, E, TH>(row, weight, target, least, skip, open, sh, work, turn)) {
-      least = max(least, sh.key);
-      const uint64_t w = sh.incl - sh.before;
-      if (!EXACT && (target - sh.before <= open || sh.incl < target + open)) {
-        // whether a few elements next to the border are kept is open: harmless
-        // where they weigh no more than the error, unless one of them is drawn
-        if (w > open) return false;
-        sure = first_bin_start(sh.sure_bin);
-        err += 4 * open;
-      }
-    }
-    __syncthreads();
-  }
-  least = max(least, edge);
-  out.kept = pick_all<E, TH>(row, max(skip, (uint32_t)(least >> 32)), [&](float x, int id) {
-    return x != neg_inf() && rank_key(x, (uint32_t)id) >= least ? weight.of<EXACT>(x) : 0;
-  }, [&](uint64_t all) { return part_of<false>(all, a.u); }, sh, turn);
-  out.id = sh.id, out.x = sh.x;
-  if (EXACT) return true;
-  if (sh.id < 0 || rank_value(weight.m) - rank_value(sh.x) >= sure) return false;
-  return (sh.before == 0 || sh.target - sh.before > err) && (sh.after >= out.kept || sh.after - sh.target > err);
+// A row's numbers, and whether they are in range.
+__device__ __forceinline__ Filters filters_of(const SampleArgs& a, int64_t t, bool& good) {
+  Filters f;
+  f.inv_t = a.inv_t ? a.inv_t[t] : 1.0f, f.u = a.u[t];
+  f.top_p = a.top_p ? a.top_p[t] : 1.0f, f.min_p = a.min_p ? a.min_p[t] : 0.0f;
+  f.top_k = a.top_k ? a.top_k[t] : 0;
+  if (f.top_k < 0 || f.top_k >= a.V) f.top_k = 0;
+  good = f.inv_t >= 1e-6f && f.inv_t <= 1e6f && f.u >= 0.0f && f.u < 1.0f && f.top_p == f.top_p && f.min_p == f.min_p;
+  return f;
+}
+// ln(min_p) / inv_temperature as a pair.
+__device__ __forceinline__ void min_p_edge(const Filters& f, float (&edge)[2]) {
+  const double e = log((double)fminf(f.min_p, 1.0f)) / (double)f.inv_t;
+  edge[0] = (float)e;
+  edge[1] = (float)(e - (double)(float)e);
+}
+// The key from which on logits have min_p: of the smallest float that is not
+// below m + ln(min_p) / inv_temperature.
+__device__ __forceinline__ uint64_t min_p_key(float m, const float (&edge)[2]) {
+  const float v = m + edge[0], b = v - m, lost = (m - (v - b)) + (edge[0] - b);
+  const float up = __fadd_ru(v, lost + edge[1]);
+  return (uint64_t)rank_value(up >= -3.402823466e+38f ? up : kLowest) << 32;  // also where the sum is out of range
+}
+__device__ __forceinline__ Weights weights_of(float inv_t, float m, int V, const uint64_t* exp2) {
+  Weights w;
+  w.m = m;
+  w.ch = __fmul_rn(inv_t, kLog2e);
+  w.cl = fmaf(inv_t, 1.92596303e-8f, fmaf(inv_t, kLog2e, -w.ch));  // log2(e) = kLog2e + 1.93e-8
+  w.s = min(52, 63 - (32 - __clz(V - 1)));
+  w.exp2 = exp2;
+  return w;
+}
+template <int TH>
+__device__ __forceinline__ void load_exp2(SampleShared<TH>& sh) {
+  if (threadIdx.x < 64)
+    sh.exp2[threadIdx.x] = (uint64_t)__float2ll_rn(kExp2Tab[threadIdx.x][0] * 0x1p62f) +
+                           (uint64_t)__float2ll_rn(kExp2Tab[threadIdx.x][1] * 0x1p62f);
+}
+__device__ __forceinline__ void put_drawn(const SampleArgs& a, int64_t t, const Drawn& d, float inv_t, float m, int s) {
+  const float z = (d.x - m) * inv_t, unit = ldexpf(1.0f, -s);
+  const int64_t one = int64_t(1) << s;
+  a.tokens[t] = d.id;
+  if (a.logprob) a.logprob[t] = z - log1pf((float)((int64_t)d.total - one) * unit);
+  if (a.kept_logprob) a.kept_logprob[t] = z - log1pf((float)((int64_t)d.kept - one) * unit);
 }
 
 template <typename E, int TH>
@@ -552,53 +542,38 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
                                           TH * kSaRuns * 8) + threadIdx.x;
   float* sums = highs + TH * kSaRuns;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x < 64)
-    sh.exp2[threadIdx.x] = (uint64_t)__float2ll_rn(kExp2Tab[threadIdx.x][0] * 0x1p62f) +
-                           (uint64_t)__float2ll_rn(kExp2Tab[threadIdx.x][1] * 0x1p62f);
+  load_exp2(sh);
   begin_kernel();
   int turn = 0;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const E* logits = static_cast<const E*>(a.logits) + t * a.ld;
     const SampleRow<E, TH> row(logits, a.V, highs);
-    Filters fl;
-    fl.inv_t = a.inv_t ? a.inv_t[t] : 1.0f, fl.u = a.u[t];
-    fl.top_p = a.top_p ? a.top_p[t] : 1.0f, fl.min_p = a.min_p ? a.min_p[t] : 0.0f;
-    fl.top_k = a.top_k ? a.top_k[t] : 0;
-    if (fl.top_k < 0 || fl.top_k >= a.V) fl.top_k = 0;
-    const bool params = fl.inv_t >= 1e-6f && fl.inv_t <= 1e6f && fl.u >= 0.0f && fl.u < 1.0f && fl.top_p == fl.top_p &&
-                        fl.min_p == fl.min_p;
+    bool params;
+    const Filters fl = filters_of(a, t, params);
     // ---- one pass: maximum and sum of each run ----
-    Weights weight;
-    weight.ch = __fmul_rn(fl.inv_t, kLog2e);
-    weight.cl = fmaf(fl.inv_t, 1.92596303e-8f, fmaf(fl.inv_t, kLog2e, -weight.ch));  // log2(e) = kLog2e + 1.93e-8
-    weight.s = min(52, 63 - (32 - __clz(a.V - 1)));
-    weight.exp2 = sh.exp2;
+    Weights weight = weights_of(fl.inv_t, 0.0f, a.V, sh.exp2);
     const float c = weight.ch;
-    float m = neg_inf();
+    float m = neg_inf(), own;
     {
       auto part = [&](int64_t) { return Part{row.r.vec(), row.r.nvec}; };
       Stream<TH, kSaU, kSaD, 1, E, decltype(part)> stream(part, ring + threadIdx.x, TH, threadIdx.x, t, 1, t + 1);
-      if (fl.min_p > 0.0f && threadIdx.x == TH - 1) {
-        const double e = log((double)fminf(fl.min_p, 1.0f)) / (double)fl.inv_t;
-        sh.edge[0] = (float)e;
-        sh.edge[1] = (float)(e - (double)(float)e);
-      }
-      Run<false> acc;
-      float high = neg_inf();
+      if (fl.min_p > 0.0f && threadIdx.x == TH - 1) min_p_edge(fl, sh.edge);
+      RunSum acc;
       int q = 0, left = row.per / kSaU;
       stream.row(row.r.nvec, [](uint4*, int) {}, [&](const auto& v, int) {
-        high = max_nan(high, acc.add(v, c, E()));
-        if (q < kSaRuns) highs[q * TH] = high, sums[q * TH] = acc.s;
+        acc.add(v, c, E());
+        highs[q * TH] = acc.m, sums[q * TH] = acc.s;
         if (--left == 0) {
-          m = max_nan(m, high);
-          ++q, left = row.per / kSaU, high = neg_inf(), acc = Run<false>();
+          m = max_nan(m, acc.m);
+          q = min(q + 1, kSaRuns - 1), left = row.per / kSaU, acc = RunSum();
         }
       });
-      m = max_nan(m, high);
+      m = max_nan(m, acc.m);
       cp_async_wait_all();
     }
     row.front([&](float x, int) { m = max_nan(m, x); });
     row.back([&](float x, int) { m = max_nan(m, x); });
+    own = m;  // this thread's maximum
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     if (lane == 0) sh.wmax[warp] = m;
@@ -619,66 +594,91 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
       continue;
     }
     weight.m = m;
-    // the runs' sums from their own shifts to the maximum
-    const float mc = __fmul_rn(m, c), M = fmaxf(ceilf(mc), -kShiftLimit);
+    // the runs' sums from their own shifts to the maximum, of unit 2^-s
+    const float mc = __fmul_rn(m, c), M = fmaxf(ceilf(mc), -kShiftLimit), cl_ch = fabsf(weight.cl) / weight.ch;
     const float to_m = exp2_fast((M - mc) - fmaf(m, c, -mc));
-    auto run_sum = [&](int q) {
-      const float h = fmaxf(highs[q * TH], kLowest), shift = fmaxf(ceilf(h * c), -kShiftLimit) - M;
-      const float w = sums[q * TH] * exp2_fast(shift) * to_m;
-      return (uint64_t)__float2ull_rn(ldexpf(w, weight.s));
+    auto run_float = [&](int q) {  // at most 2^10
+      return sums[q * TH] * exp2_fast(RunSum::shift_of(highs[q * TH], c) - M) * to_m;
     };
+    auto run_sum = [&](int q) { return fixed(run_float(q), weight.s); };
     const bool shift_ok = fabsf(mc) <= kShiftLimit;
     const bool filtered = fl.top_k > 0 || fl.top_p < 1.0f || fl.min_p > 0.0f;
     uint64_t edge = 0;  // keys below have less than min_p
-    if (fl.min_p > 0.0f) {  // the smallest float that is not below m + ln(min_p) / inv_temperature
-      const float e = sh.edge[0], v = m + e, b = v - m, lost = (m - (v - b)) + (e - b);
-      const float up = __fadd_ru(v, lost + sh.edge[1]);
-      edge = (uint64_t)rank_value(up >= -3.402823466e+38f ? up : kLowest) << 32;  // also where the sum is out of range
-    }
+    if (fl.min_p > 0.0f) edge = min_p_key(m, sh.edge);
     Drawn out;
-    uint64_t sum = 0, err = 0;
-    if (shift_ok) {
-      if (filtered) {
-        for (int q = 0; q < row.runs; ++q) sum += run_sum(q);
-        row.front([&](float x, int) { sum += weight.fast(x); });
-        row.back([&](float x, int) { sum += weight.fast(x); });
-        block_scan<TH>(sum, out.total, sh, turn);
-      } else {
-        out.total = out.kept =
-            pick<E, TH>(row, run_sum, [&](float x, int) { return weight.fast(x); },
-                        [&](uint64_t all) { return part_of<false>(all, fl.u); }, sh, turn);
-        out.id = sh.id, out.x = sh.x;
-      }
-      const float S = (float)out.total * ldexpf(1.0f, -weight.s);
-      err = (uint64_t)((float)out.total * row_delta(S, a.V));
-    } else {
-      row.all(0, [&](float x, int) { sum += weight.exact(x); });
+    uint64_t sum = 0, err, weight_err;  // errors of sums of the pass, and of weights by themselves
+    const float unit = ldexpf(1.0f, -weight.s);
+    int e = 0;  // the part of the row with the token
+    if (!shift_ok) {  // the pass's weights are out of range
+      row.all(0, [&](float x, int) { sum += weight.fast(x); });
+      block_scan<TH>(sum, out.total, sh, turn);
+    } else if (filtered) {
+      float w = 0.0f;
+      for (int q = 0; q < row.runs; ++q) w += run_float(q);
+      sum = fixed(w, weight.s);
+      row.front([&](float x, int) { sum += weight.fast(x); });
+      row.back([&](float x, int) { sum += weight.fast(x); });
       block_scan<TH>(sum, out.total, sh, turn);
     }
+    if (!filtered) {
+      out.total = out.kept = pick<E, TH>(row, [&](int q) {
+        uint64_t v = 0;
+        if (shift_ok) v = run_sum(q);
+        else row.run(q, [&](float x, int) { v += weight.fast(x); });
+        return v;
+      }, [&](float x, int) { return weight.fast(x); }, [&](uint64_t all) { return part_of<false>(all, fl.u); }, sh,
+                                         work.group, turn);
+      out.id = sh.id, out.x = sh.x;
+      uint64_t first;
+      e = find_part<E, TH>(row, sh.target, first, sh);
+    }
+    {
+      // in the pass 3 additions per sum of pairs, 3 to join them, one per batch of
+      // a run, a product with to_m; with the filters 8 for the thread's runs, and
+      // to_m's own error, which is otherwise the same for all
+      const float S = (float)out.total * unit;
+      const float near = sum_error(S, a.V, cl_ch, 2, 0);
+      weight_err = (uint64_t)((float)(filtered ? out.total : sh.sums[e]) * (near + 0x1p-22f));
+      err = shift_ok ? (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 1, 7 + row.per / kSaU + (filtered ? 12 : 0)))
+                     : (uint64_t)((float)out.total * near);
+    }
+    const int open = kOpen - (64 - __clzll((long long)out.total) - weight.s);
     bool done = false;
     if (!filtered) {
-      done = shift_ok && sh.id >= 0 && (sh.before == 0 || sh.target - sh.before > err) &&
+      err += weight_err;  // of the run with the token
+      done = sh.id >= 0 && (sh.before == 0 || sh.target - sh.before > err) &&
              (sh.after >= out.total || sh.after - sh.target > err);
     } else {
-      // ---- a lower bound of what is kept, from the runs' maxima ----
+      // ---- a lower bound of what is kept, from the maxima ----
       const uint32_t top = rank_value(m);
       uint32_t skip = (uint32_t)(edge >> 32);
       const bool by_count = fl.top_k > 0, by_mass = !by_count && fl.top_p < 1.0f;
       if (by_count && fl.top_p < 1.0f) skip = 0;  // all of the top_k count for top_p
-      if (threadIdx.x == 0) sh.found = 0, sh.listed = 0;
+      if (threadIdx.x == 0) sh.found = 0, sh.listed = 0, sh.hot = 0;
       bool few = true;
       if (by_count || by_mass) {
         for (int b = threadIdx.x; b < kSaNear; b += TH) work.lo[b] = 0, work.hi[b] = 0;
         __syncthreads();
-        auto offer = [&](float x) {
+        auto offer = [&](float x, uint64_t w) {
           const uint32_t d = top - rank_value(x);
           if (d >= 1u << 27 || x == neg_inf()) return;
           if (by_count) atomicAdd(&work.lo[d >> 17], 1u);
-          else add64(&work.lo[d >> 17], &work.hi[d >> 17], weight.fast(x));
+          else add64(&work.lo[d >> 17], &work.hi[d >> 17], w);
         };
-        for (int q = 0; q < row.runs; ++q) offer(highs[q * TH]);
-        row.front([&](float x, int) { offer(x); });
-        row.back([&](float x, int) { offer(x); });
+        if (by_count) {
+          offer(own, 0);
+        } else {
+          // the weights that matter: all others together are below a quarter of
+          // what top_p leaves out
+          const float least = (1.0f - fl.top_p) * (float)out.total * unit * 0.25f / (float)(TH * kSaRuns);
+          auto heavy = [&](float x) {
+            const float w = weight.ratio(x);
+            if (w >= least) offer(x, fixed(w, weight.s));
+          };
+          for (int q = 0; q < row.runs; ++q) heavy(highs[q * TH]);
+          row.front([&](float x, int) { heavy(x); });
+          row.back([&](float x, int) { heavy(x); });
+        }
         __syncthreads();
         constexpr int PER = kSaNear / TH;
         uint64_t n = 0, all;
@@ -697,6 +697,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
           sh.found = 1, sh.bin = threadIdx.x * PER + i;
         }
         __syncthreads();
+        // (work.lo is read no more: the list of runs shares its memory)
         if (sh.found) skip = max(skip, top - min(top, ((uint32_t)(sh.bin + 1) << 17) - 1));
         else few = skip > 0;  // min_p's bound alone
       } else {
@@ -704,14 +705,34 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
       }
       // ---- the elements from there on, if they are few ----
       if (few) {
-        row.all(skip, [&](float x, int id) {
+        auto offer = [&](float x, int id) {
           if (rank_value(x) >= skip && x != neg_inf()) {
             const uint32_t at = atomicAdd(&sh.listed, 1u);
             if (at < (uint32_t)kList) work.list[at] = rank_key(x, (uint32_t)id);
           }
-        });
+        };
+        // the runs that have any, read by all threads together
+        constexpr int kHot = SampleWork<TH>::kHot;
+        if (rank_value(own) >= skip)
+          for (int q = 0; q < row.runs; ++q)
+            if (row.has(q, skip)) {
+              const uint32_t at = atomicAdd(&sh.hot, 1u);
+              if (at < (uint32_t)kHot) work.hot[at] = threadIdx.x | (uint32_t)q << 16;
+            }
         __syncthreads();
-        few = sh.listed <= (uint32_t)kList;
+        few = sh.hot <= (uint32_t)kHot;
+        if (few) {
+          const int items = (int)sh.hot * row.per;
+          for (int j = threadIdx.x; j < items; j += TH) {
+            const uint32_t who = work.hot[j / row.per];
+            const int i = ((int)(who >> 16) * row.per + j % row.per) * TH + (int)(who & 0xFFFFu);
+            if (i < row.r.nvec) row.vector(row.r.vec()[i], i, offer);
+          }
+          row.front(offer);
+          row.back(offer);
+        }
+        __syncthreads();
+        few &= sh.listed <= (uint32_t)kList;
       }
       if (few) {
         int n = (int)sh.listed;
@@ -719,10 +740,10 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
         if (fl.top_k > 0) n = min(n, fl.top_k);
         for (int j = threadIdx.x; j < n; j += TH) work.weight[j] = weight.exact(rank_logit(work.list[j]));
         __syncthreads();
-        sum_list<TH>(work.weight, n, sh, turn);
+        sum_list<kList, TH>(work.weight, n, sh, turn);
         if (fl.top_p < 1.0f) {
-          uint64_t mass = by_count ? work.weight[n - 1] : out.total, near = by_count ? 0 : err;
-          for (;;) {
+          const uint64_t mass = by_count ? work.weight[n - 1] : out.total, near = by_count ? 0 : err;
+          {
             const uint64_t target = max(1ull, (unsigned long long)part_of<true>(mass, fmaxf(fl.top_p, 0.0f)));
             const uint64_t all = work.weight[n - 1];  // below the target where min_p ends the list before top_p does
             if (threadIdx.x == 0) sh.kept = n, sh.found = near && all < target && target - all <= near;
@@ -735,12 +756,11 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
               }
             }
             __syncthreads();
-            if (!sh.found) break;
-            // too close for the fast sum of the row
-            sum = 0;
-            row.all(0, [&](float x, int) { sum += weight.exact(x); });
-            block_scan<TH>(sum, mass, sh, turn);
-            out.total = mass, near = 0;
+          }
+          if (sh.found) {  // too close for the fast sum of the row
+            if (threadIdx.x == 0) a.tokens[t] = open;
+            __syncthreads();
+            continue;
           }
           n = sh.kept;
         }
@@ -809,27 +829,517 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
         }
         out.id = sh.id, out.x = sh.x;
         done = true;
-      } else if (shift_ok) {
-        done = draw_many<false, E, TH>(row, weight, fl, a.V, out.total, err, edge, skip, out, sh, work, turn);
-        __syncthreads();
-        if (!done)
-          draw_many<true, E, TH>(row, weight, fl, a.V, out.total, 0, edge, skip, out, sh, work, turn), done = true;
       }
     }
-    if (!done) {  // fast weights leave it open, or are out of range
-      __syncthreads();
-      draw_many<true, E, TH>(row, weight, fl, a.V, out.total, 0, edge, 0, out, sh, work, turn);
-      if (!filtered) out.total = out.kept;
-    }
     if (threadIdx.x == 0) {
-      const float z = (out.x - m) * fl.inv_t, unit = ldexpf(1.0f, -weight.s);
-      const int64_t one = int64_t(1) << weight.s;
-      a.tokens[t] = out.id;
-      if (a.logprob) a.logprob[t] = z - log1pf((float)((int64_t)out.total - one) * unit);
-      if (a.kept_logprob) a.kept_logprob[t] = z - log1pf((float)((int64_t)out.kept - one) * unit);
+      if (done) put_drawn(a, t, out, fl.inv_t, m, weight.s);
+      else a.tokens[t] = open;
     }
     __syncthreads();
   }
+}
+
+// ---- rows that are left open: eight blocks per row, a part of it each, and
+// weights to 2^-34 ----
+constexpr int kTeam = 8, kTeamLog = 3;
+constexpr int kTeamThreads = 512, kTeamWarps = kTeamThreads / 32;
+constexpr int kTeamList = 2048;
+constexpr int kTeamBins = 4096, kTeamSlice = kTeamBins / kTeam;
+constexpr int kTeamGroups = 1024;  // of 32 vectors: (2^20 / 4 / 8) / 32
+using TeamShared = SampleShared<kTeamThreads>;
+static_assert(kTeamSlice == kTeamThreads, "a thread per bin of a slice");
+
+struct TeamWork {
+  uint64_t power[1024];             // 2^(j/1024) 2^62
+  uint64_t list[kTeamList], weight[kTeamList];
+  uint64_t group[kTeamGroups + 2];  // the elements before the vectors, 32 vectors in a row each, the elements after
+  uint32_t lo[kTeamBins], hi[kTeamBins];
+  uint64_t box[2][2];               // what the blocks tell one another, in turn
+  uint64_t base, key, incl;
+};
+
+// Bins of the ranks at and below the row's maximum's, `top`: by 1/128 of a power
+// of two over sixteen of them, then one bin down to -2^-10, then by 1/64 of a
+// power of two over 32 of them, and the rest.
+constexpr int kTeamNear = 2048;
+constexpr uint32_t kNegative = 0x7FFFFFFFu - 0x3A800000u;  // rank of -2^-10
+__device__ __forceinline__ int first_bin(uint32_t top, uint32_t rank) {
+  const uint32_t d = top - rank;
+  if (d < 1u << 27) return (int)(d >> 16);
+  return rank >= kNegative ? kTeamNear : min(kTeamBins - 1, kTeamNear + 1 + (int)((kNegative - 1 - rank) >> 17));
+}
+// First distance below `top` that is not in a bin before b.
+__device__ __forceinline__ uint32_t first_bin_start(uint32_t top, int b) {
+  if (b <= kTeamNear) return (uint32_t)b << 16;
+  const int64_t d = (int64_t)top - (int64_t)kNegative + 1 + ((int64_t)(b - kTeamNear - 1) << 17);
+  return b >= kTeamBins ? 0xFFFFFFFFu : (uint32_t)max((long long)d, 1ll << 27);
+}
+
+// A block's part of a row, ids from id0 on, and what the block and its team know.
+template <typename E>
+struct Team {
+  Row<E> r;
+  int id0, rank, turn, scan_turn, groups;
+  Weights weight;
+  TeamShared& sh;
+  TeamWork& work;
+
+  // Weights to 2^-34 as Weights::exact, but with the powers of 2^(1/1024): the
+  // rest's series has three terms, and its one FP32 number is good to 2^-35.
+  __device__ __forceinline__ uint64_t exact(float x) const {
+    const float m = weight.m, ch = weight.ch;
+    const float d = x - m;
+    const float p = __fmul_rn(d, ch);
+    if (!(p >= kMinExponent - 1.0f)) return 0;
+    const float b = d - x, lost = (x - (d - b)) + (-m - b);
+    const float e = fmaf(lost, ch, fmaf(d, weight.cl, fmaf(d, ch, -p)));
+    if ((p - kMinExponent) + e < 0.0f) return 0;
+    const float z = p + 12288.0f;  // 1.5 2^13: steps of 1/1024
+    const int i = __float_as_int(z) - __float_as_int(12288.0f);
+    const float q = (p - (z - 12288.0f)) + e;
+    const int n = __float2int_rn(q * fmaf(q, fmaf(q, 0x1p40f * 0.0555041087f, 0x1p40f * 0.240226507f), 0x1p40f * 0.69314718f));
+    const uint64_t t = work.power[i & 1023];
+    return (t + (uint64_t)(((int64_t)n * (int64_t)(t >> 32)) >> 8)) >> (62 - weight.s - (i >> 10));
+  }
+  // f(x, id, group) on this thread's elements of the part; end(group) after each
+  // group of this warp, in step
+  template <typename F, typename G>
+  __device__ __forceinline__ void each(F f, G end) const {
+    constexpr int N = Row<E>::kVec;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int g0 = warp; g0 < groups; g0 += kSaU * kTeamWarps) {
+      uint4 v[kSaU];
+#pragma unroll
+      for (int u = 0; u < kSaU; ++u) v[u] = r.vec()[min((g0 + u * kTeamWarps) * 32 + lane, r.nvec - 1)];
+#pragma unroll
+      for (int u = 0; u < kSaU; ++u) {
+        const int g = g0 + u * kTeamWarps, i = g * 32 + lane;
+        if (g >= groups) break;
+        if (i < r.nvec) {
+          float x[N];
+          unpack(v[u], x);
+#pragma unroll
+          for (int k = 0; k < N; ++k) f(x[k], id0 + r.head + i * N + k);
+        }
+        end(g + 1);
+      }
+    }
+    if (warp == 0) {
+      if (lane < r.head) f(to_f32(r.p[lane]), id0 + lane);
+      end(0);
+      if (lane < r.tail) f(to_f32(r.p[r.tail_start() + lane]), id0 + r.tail_start() + lane);
+      end(groups + 1);
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    each(f, [](int) {});
+  }
+  // f's sums into the groups
+  template <typename F>
+  __device__ __forceinline__ void sums(F f) const {
+    uint64_t v = 0;
+    each([&](float x, int id) { v += f(x, id); }, [&](int g) {
+      v = warp_sum64(v);
+      if ((threadIdx.x & 31) == 0) work.group[g] = v;
+      v = 0;
+    });
+    __syncthreads();
+  }
+  __device__ __forceinline__ uint64_t scan(uint64_t v, uint64_t& total) {
+    return block_scan<kTeamThreads>(v, total, sh, scan_turn);
+  }
+  // Two numbers of each block: lane r of every warp gets rank r's (0 from lane 8
+  // on).  A barrier of the team.
+  __device__ __forceinline__ void share(uint64_t a, uint64_t b, uint64_t& va, uint64_t& vb) {
+    const int lane = threadIdx.x & 31;
+    uint64_t* box = work.box[turn];
+    if (threadIdx.x == 0) box[0] = a, box[1] = b;
+    cluster_arrive();
+    cluster_wait();
+    va = vb = 0;
+    if (lane < kTeam) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(box);
+      va = cluster_load(p, lane) | (uint64_t)cluster_load(p + 1, lane) << 32;
+      vb = cluster_load(p + 2, lane) | (uint64_t)cluster_load(p + 3, lane) << 32;
+    }
+    turn ^= 1;
+  }
+  // The groups' sums over the team, and this block's and those before it.
+  __device__ __forceinline__ uint64_t total(uint64_t& mine, uint64_t& before) {
+    uint64_t v = 0, all, none;
+    for (int g = threadIdx.x; g < groups + 2; g += kTeamThreads) v += work.group[g];
+    scan(v, mine);
+    share(mine, 0, all, none);
+    before = warp_sum64((int)(threadIdx.x & 31) < rank ? all : 0);
+    return warp_sum64(all);
+  }
+  // The first id up to which the sum of f is above target, with the groups' sums
+  // given: true for the block that has it, sh.id (within the row) and sh.x.
+  template <typename F>
+  __device__ __forceinline__ bool find(uint64_t target, uint64_t mine, uint64_t before, F f) {
+    if (target < before || target >= before + mine) return false;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = groups + 2;
+    const int each = (n + kTeamThreads - 1) / kTeamThreads, g0 = (int)threadIdx.x * each;
+    const uint64_t left = target - before;
+    uint64_t sum = 0, all;
+    for (int g = g0; g < min(g0 + each, n); ++g) sum += work.group[g];
+    uint64_t b = scan(sum, all);
+    if (b <= left && left < b + sum) {
+      int g = g0;
+      while (b + work.group[g] <= left) b += work.group[g++];
+      sh.at = g, sh.left = b;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      constexpr int N = Row<E>::kVec;
+      const int g = sh.at, i = (g - 1) * 32 + lane;
+      float x[N];
+      int id = id0, k = 0;  // this lane's first id, and how many
+      if (g == 0 || g == groups + 1) {
+        id += (g ? r.tail_start() : 0) + lane;
+        k = lane < (g ? r.tail : r.head) ? 1 : 0;
+        if (k) x[0] = to_f32(r.p[id - id0]);
+      } else if (i < r.nvec) {
+        id += r.head + i * N;
+        k = N;
+        unpack(r.vec()[i], x);
+      }
+      uint64_t w = 0;
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (e < k) w += f(x[e], id + e);
+      uint64_t incl = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t m = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += m;
+      }
+      uint64_t at = sh.left + incl - w;
+      if (at <= left && left < at + w) {
+        bool done = false;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (e < k && !done) {
+            at += f(x[e], id + e);
+            if (at > left) done = true, sh.id = id + e, sh.x = x[e];
+          }
+      }
+    }
+    __syncthreads();
+    return true;
+  }
+  // The blocks' lists together in the first block's; counts: each block's, by lane.
+  __device__ __forceinline__ void gather(uint64_t counts) {
+    int at = (int)__shfl_sync(0xFFFFFFFFu, counts, 0);
+    for (int q = 1; q < kTeam; ++q) {
+      const int n = (int)__shfl_sync(0xFFFFFFFFu, counts, q);
+      for (int j = threadIdx.x; j < n; j += kTeamThreads) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(&work.list[j]);
+        work.list[at + j] = cluster_load(p, q) | (uint64_t)cluster_load(p + 1, q) << 32;
+      }
+      at += n;
+    }
+    __syncthreads();
+  }
+  // In the first block: the first of the n listed keys, in their order, with
+  // which `base` and the weights reach target: work.key and the sum, work.incl; 0
+  // if none does, or base alone.
+  __device__ __forceinline__ void reach(int n, uint64_t base, uint64_t target) {
+    sort_list<kTeamThreads>(work.list, n);
+    for (int j = threadIdx.x; j < n; j += kTeamThreads) work.weight[j] = exact(rank_logit(work.list[j]));
+    if (threadIdx.x == 0) work.key = work.incl = 0;
+    __syncthreads();
+    sum_list<kTeamList, kTeamThreads>(work.weight, n, sh, scan_turn);
+    for (int j = threadIdx.x; j < n; j += kTeamThreads) {
+      const uint64_t before = base + (j ? work.weight[j - 1] : 0), upto = base + work.weight[j];
+      if (before < target && target <= upto) work.key = work.list[j], work.incl = upto;
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void list(float x, int id) {
+    const uint32_t at = atomicAdd(&sh.listed, 1u);
+    if (at < (uint32_t)kTeamList) work.list[at] = rank_key(x, (uint32_t)id);
+  }
+  __device__ __forceinline__ void clear(bool both) {
+    for (int b = threadIdx.x; b < kTeamBins; b += kTeamThreads) {
+      work.lo[b] = 0;
+      if (both) work.hi[b] = 0;
+    }
+    if (threadIdx.x == 0) sh.listed = 0;
+    __syncthreads();
+  }
+  // This thread's bin of the block's slice, over the team, and what comes before
+  // it.  Barriers of the team.
+  __device__ __forceinline__ uint64_t slice(bool both, uint64_t& before, uint64_t& sum) {
+    cluster_arrive();
+    cluster_wait();
+    const int b = rank * kTeamSlice + (int)threadIdx.x;
+    uint64_t n = 0, mine, all, none;
+#pragma unroll
+    for (int q = 0; q < kTeam; ++q) {
+      n += cluster_load(&work.lo[b], q);
+      if (both) n += (uint64_t)cluster_load(&work.hi[b], q) << 32;
+    }
+    before = scan(n, mine);
+    share(mine, 0, all, none);
+    before += warp_sum64((int)(threadIdx.x & 31) < rank ? all : 0);
+    sum = warp_sum64(all);
+    return n;
+  }
+
+  // The last element of the shortest leading part, in the order of the keys and
+  // of the keys >= least, that holds `target` elements (COUNT) or weight: its key,
+  // and the weight up to and with it.  False if all together do not.
+  template <bool COUNT>
+  __device__ __noinline__ bool select(uint64_t target, uint64_t least, uint64_t& key_out, uint64_t& incl_out) {
+    const uint32_t top = rank_value(weight.m);
+    uint32_t d0 = 0, d1 = 0xFFFFFFFFu;
+    uint64_t base = 0, all, none;  // elements or weight before these distances
+    for (int level = 0;; ++level) {
+      int shift = 0;
+      while (((d1 - d0) >> shift) >= (uint32_t)kTeamBins) ++shift;
+      clear(true);
+      each([&](float x, int id) {
+        const uint64_t key = rank_key(x, (uint32_t)id);
+        const uint32_t d = top - (uint32_t)(key >> 32);
+        if (x == neg_inf() || key < least || d < d0 || d > d1) return;
+        const int b = level == 0 ? first_bin(top, top - d) : (int)((d - d0) >> shift);
+        if (COUNT) {
+          atomicAdd(&work.lo[b], 1u);
+        } else {
+          const uint64_t w = exact(x);
+          if (w) add64(&work.lo[b], &work.hi[b], w);
+        }
+      });
+      uint64_t n0, sum;
+      const uint64_t n = slice(true, n0, sum);
+      if (threadIdx.x == 0) sh.found = 0;
+      __syncthreads();
+      n0 += base;
+      if (n0 < target && target <= n0 + n) sh.found = 1 + rank * kTeamSlice + threadIdx.x, work.base = n0;
+      __syncthreads();
+      share(sh.found, sh.found ? work.base : 0, all, none);
+      const int bin = (int)warp_sum64(all) - 1;
+      if (bin < 0) return false;
+      base = warp_sum64(none);
+      if (level == 0) {
+        d0 = first_bin_start(top, bin);
+        d1 = bin + 1 < kTeamBins ? first_bin_start(top, bin + 1) - 1 : 0xFFFFFFFFu;
+      } else {
+        const uint32_t start = d0 + ((uint32_t)bin << shift), rest = d1 - start, width = (1u << shift) - 1;
+        d0 = start;
+        d1 = start + min(rest, width);
+      }
+      each([&](float x, int id) {
+        const uint64_t key = rank_key(x, (uint32_t)id);
+        const uint32_t d = top - (uint32_t)(key >> 32);
+        if (x != neg_inf() && key >= least && d >= d0 && d <= d1) list(x, id);
+      });
+      __syncthreads();
+      share(sh.listed, 0, all, none);
+      const uint64_t in = warp_sum64(all);
+      if (in <= (uint64_t)kTeamList) {  // the first block decides
+        uint64_t key = 0, incl = 0;
+        if (rank == 0) {
+          gather(all);
+          if (COUNT) {
+            sort_list<kTeamThreads>(work.list, (int)in);
+            key = work.list[target - base - 1];
+          } else {
+            reach((int)in, base, target);
+            key = work.key, incl = work.incl;
+          }
+        }
+        share(key, incl, all, none);
+        key_out = warp_sum64(all), incl_out = warp_sum64(none);
+        return true;
+      }
+      if (d0 == d1) {  // ties: the first of them in the order of the ids
+        const uint32_t value = top - d0;
+        const uint64_t w1 = COUNT ? 1 : exact(rank_logit((uint64_t)value << 32)), take = (target - base + w1 - 1) / w1;
+        auto tie = [&](float x, int id) {
+          return (uint64_t)(x != neg_inf() && rank_value(x) == value && rank_key(x, (uint32_t)id) >= least);
+        };
+        sums(tie);
+        uint64_t mine, before;
+        total(mine, before);
+        const uint64_t key = find(take - 1, mine, before, tie) ? rank_key(sh.x, (uint32_t)sh.id) : 0;
+        share(key, 0, all, none);
+        key_out = warp_sum64(all), incl_out = base + take * w1;
+        return true;
+      }
+    }
+  }
+
+  // The draw with top_p alone: a histogram of rounded weights says near which
+  // values the kept part ends; one pass then sums the weights above them and all
+  // weights, and lists the elements in between.  False, without a result, where
+  // these are too many or the end is not among them.  log_s: of the row's weight.
+  __device__ __forceinline__ bool draw_top_p(const Filters& fl, int V, int log_s, Drawn& out, bool& owner) {
+    const uint32_t top = rank_value(weight.m);
+    const float scale = ldexpf(1.0f, 31 - log_s);
+    clear(false);
+    each([&](float x, int) {
+      const uint32_t v = __float2uint_rn(weight.ratio(x) * scale);
+      if (v) atomicAdd(&work.lo[first_bin(top, rank_value(x))], v);
+    });
+    uint64_t n0, sum, all, none;
+    const uint64_t n = slice(false, n0, sum);
+    // off by half a unit per element, and the error of FP32 weights
+    const uint64_t mid = part_of<false>(sum, fmaxf(fl.top_p, 0.0f)), slack = (uint64_t)V / 2 + (sum >> 17) + 1;
+    const uint64_t low = mid > slack ? mid - slack : 0, high = min((unsigned long long)(mid + slack), (unsigned long long)sum);
+    if (threadIdx.x == 0) work.key = work.incl = 0;
+    __syncthreads();
+    if (n0 <= low && low < n0 + n) work.key = 1 + rank * kTeamSlice + threadIdx.x;
+    if (n0 < high && high <= n0 + n) work.incl = 1 + rank * kTeamSlice + threadIdx.x;
+    __syncthreads();
+    share(work.key, work.incl, all, none);
+    const int b0 = (int)warp_sum64(all) - 1, b1 = (int)warp_sum64(none) - 1;
+    if (b0 < 0 || b1 < b0) return false;
+    const uint32_t d0 = first_bin_start(top, b0), d1 = b1 + 1 < kTeamBins ? first_bin_start(top, b1 + 1) - 1 : 0xFFFFFFFFu;
+    uint64_t S = 0;
+    sums([&](float x, int id) {
+      const uint32_t d = top - rank_value(x);
+      const uint64_t w = exact(x);
+      S += w;
+      if (d >= d0 && d <= d1 && w) list(x, id);
+      return d < d0 ? w : 0;
+    });
+    const int listed = (int)sh.listed;
+    uint64_t part;
+    scan(S, part);
+    share(part, (uint64_t)listed, all, none);
+    S = warp_sum64(all);
+    if (warp_sum64(none) > (uint64_t)kTeamList) return false;
+    uint64_t mine, before;
+    const uint64_t base = total(mine, before);
+    const uint64_t target = max(1ull, (unsigned long long)part_of<true>(S, fmaxf(fl.top_p, 0.0f)));
+    uint64_t key = 0, kept = 0;
+    // the own list, before the first block mixes it with the others'
+    constexpr int PER = kTeamList / kTeamThreads;
+    uint64_t own[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) own[i] = (int)threadIdx.x + i * kTeamThreads < listed ? work.list[threadIdx.x + i * kTeamThreads] : 0;
+    if (rank == 0) {
+      __syncthreads();
+      gather(none);
+      reach((int)warp_sum64(none), base, target);
+      key = work.key, kept = work.incl;
+    }
+    share(key, kept, all, none);
+    key = warp_sum64(all), kept = warp_sum64(none);
+    if (key == 0) return false;
+    // the kept ones of the list join their groups
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (own[i] >= key) {
+        const int at = rank_id(own[i]) - id0, v = at - r.head;
+        const int g = at < r.head ? 0 : at >= r.tail_start() ? groups + 1 : 1 + v / (32 * Row<E>::kVec);
+        uint32_t* p = reinterpret_cast<uint32_t*>(&work.group[g]);
+        add64(p, p + 1, exact(rank_logit(own[i])));
+      }
+    __syncthreads();
+    out.total = S;
+    out.kept = total(mine, before);
+    owner = find(part_of<false>(out.kept, fl.u), mine, before, [&](float x, int id) {
+      return x != neg_inf() && rank_key(x, (uint32_t)id) >= key ? exact(x) : 0;
+    });
+    return true;
+  }
+
+  __device__ __forceinline__ bool draw(const Filters& fl, int V, int log_s, Drawn& out) {
+    const bool filtered = fl.top_k > 0 || fl.top_p < 1.0f || fl.min_p > 0.0f;
+    bool owner;
+    if (fl.top_k == 0 && fl.top_p < 1.0f && !(fl.min_p > 0.0f) && draw_top_p(fl, V, log_s, out, owner)) return owner;
+    uint64_t least = 0, key, incl, mine, before;
+    if (filtered) {
+      sums([&](float x, int) { return exact(x); });
+      out.total = total(mine, before);
+    }
+    if (fl.top_k > 0 && select<true>((uint64_t)fl.top_k, 0, key, incl)) least = key;
+    if (fl.top_p < 1.0f) {
+      uint64_t mass = out.total;
+      if (least) {
+        sums([&](float x, int id) { return rank_key(x, (uint32_t)id) >= least ? exact(x) : 0; });
+        mass = total(mine, before);
+      }
+      const uint64_t target = max(1ull, (unsigned long long)part_of<true>(mass, fmaxf(fl.top_p, 0.0f)));
+      if (select<false>(target, least, key, incl)) least = max(least, key);
+    }
+    if (fl.min_p > 0.0f) {
+      if (threadIdx.x == 0) min_p_edge(fl, sh.edge);
+      __syncthreads();
+      least = max(least, min_p_key(weight.m, sh.edge));
+    }
+    auto kept = [&](float x, int id) { return x != neg_inf() && rank_key(x, (uint32_t)id) >= least ? exact(x) : 0; };
+    sums(kept);
+    out.kept = total(mine, before);
+    if (!filtered) out.total = out.kept;
+    const uint64_t target = part_of<false>(out.kept, fl.u);
+    return find(min((unsigned long long)target, (unsigned long long)out.kept - 1), mine, before, kept);
+  }
+};
+
+template <typename E>
+__global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs a) {
+  extern __shared__ uint4 smem[];
+  TeamWork& work = *reinterpret_cast<TeamWork*>(smem);
+  TeamShared& sh = *reinterpret_cast<TeamShared*>(&work + 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = (int)blockIdx.x % kTeam;
+  const int64_t teams = gridDim.x / kTeam;
+  bool ready = false;
+  int turn = 0, scan_turn = 0;
+  begin_kernel();
+  for (int64_t t0 = blockIdx.x / kTeam; t0 < a.T; t0 += 32 * teams) {
+    const int64_t mine = t0 + lane * teams;
+    const int flag = mine < a.T ? a.tokens[mine] : 0;
+    uint32_t open = __ballot_sync(0xFFFFFFFFu, flag <= kOpen);
+    if (open && !ready) {
+      load_exp2(sh);
+      __syncthreads();
+      Weights one;  // 2^((j - 1024) / 1024) 2^52, for the powers
+      one.m = 1024.0f, one.ch = 0x1p-10f, one.cl = 0.0f, one.s = 61, one.exp2 = sh.exp2;
+      for (int j = threadIdx.x; j < 1024; j += kTeamThreads) work.power[j] = one.exact((float)j) << 2;
+      __syncthreads();
+      ready = true;
+    }
+    for (; open; open &= open - 1) {
+      const int who = __ffs(open) - 1;
+      const int64_t t = t0 + who * teams;
+      const int log_s = kOpen - __shfl_sync(0xFFFFFFFFu, flag, who);
+      const E* logits = static_cast<const E*>(a.logits) + t * a.ld;
+      const Row<E> whole(logits, a.V);
+      const int v0 = whole.part(rank, kTeamLog), v1 = whole.part(rank + 1, kTeamLog);
+      const int id0 = rank == 0 ? 0 : whole.head + v0 * Row<E>::kVec;
+      const int id1 = rank == kTeam - 1 ? a.V : whole.head + v1 * Row<E>::kVec;
+      const Row<E> r(logits + id0, id1 - id0);
+      Team<E> team = {r, id0, rank, turn, scan_turn, (r.nvec + 31) / 32, Weights(), sh, work};
+      bool params;
+      const Filters fl = filters_of(a, t, params);
+      // the row's maximum, in the order of rank_value
+      uint32_t top = 0;
+      team.each([&](float x, int) { top = max(top, rank_value(x)); });
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if (lane == 0) sh.scan[0][warp] = top;
+      __syncthreads();
+      top = __reduce_max_sync(0xFFFFFFFFu, lane < kTeamWarps ? (uint32_t)sh.scan[0][lane] : 0u);
+      __syncthreads();
+      uint64_t all, none;
+      team.share(top, 0, all, none);
+      top = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)all);
+      team.weight = weights_of(fl.inv_t, rank_logit((uint64_t)top << 32), a.V, sh.exp2);
+      Drawn out;
+      if (team.draw(fl, a.V, log_s, out) && threadIdx.x == 0) {
+        out.id = sh.id, out.x = sh.x;
+        put_drawn(a, t, out, fl.inv_t, team.weight.m, team.weight.s);
+      }
+      __syncthreads();
+      turn = team.turn, scan_turn = team.scan_turn;
+    }
+  }
+  cluster_arrive();  // no block ends while another reads its shared memory
+  cluster_wait();
 }
 
 template <int TH>
@@ -839,6 +1349,14 @@ static int launch_sample(const SampleArgs& a, cudaStream_t s) {
   if (!allow_smem((const void*)f, kSaSmem<TH>, kSaSmem<TH>)) return -1;
   return launch_kernel(f, (unsigned)(a.T < most ? a.T : most), TH, kSaSmem<TH>, 1, s, a);
 }
-int launch_sample_tokens(const SampleArgs& a, cudaStream_t s) { return launch_sample<512>(a, s); }
+int launch_sample_tokens(const SampleArgs& a, cudaStream_t s) {
+  const int rc = launch_sample<512>(a, s);
+  if (rc != 0) return rc;
+  constexpr int smem = (int)(sizeof(TeamWork) + sizeof(TeamShared));
+  auto f = a.dtype == MOE_DTYPE_BF16 ? sample_open_kernel<uint16_t> : sample_open_kernel<float>;
+  if (!allow_smem((const void*)f, smem, smem)) return -1;
+  const int teams = 2 * gemm_num_ctas() / kTeam;
+  return launch_kernel(f, (unsigned)((a.T < teams ? a.T : teams) * kTeam), kTeamThreads, smem, kTeam, s, a);
+}
 
 }  // namespace moe
