@@ -56,7 +56,7 @@ __device__ __forceinline__ uint64_t fixed(float w, int s) {
 
 template <int TH>
 struct SampleShared {
-  static constexpr int NW = TH / 32, kList = TH < 1024 ? 2 * TH : TH;
+  static constexpr int NW = TH / 32, kList = TH < 512 ? 4 * TH : TH < 1024 ? 2 * TH : TH;
   uint64_t exp2[64];               // 2^(j/64) 2^62
   uint64_t part[kSaRuns + 2][NW];  // sums of the runs by warp; the row's ends
   uint64_t sums[kSaRuns + 2];      // of all warps
@@ -665,8 +665,10 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
           if (by_count) atomicAdd(&work.lo[d >> 17], 1u);
           else add64(&work.lo[d >> 17], &work.hi[d >> 17], w);
         };
-        if (by_count) {
+        if (by_count && fl.top_k <= TH / 4) {
           offer(own, 0);
+        } else if (by_count) {
+          for (int q = 0; q < row.runs; ++q) offer(highs[q * TH], 0);
         } else {
           // the weights that matter: all others together are below a quarter of
           // what top_p leaves out
@@ -839,15 +841,19 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
   }
 }
 
-// ---- rows that are left open: eight blocks per row, a part of it each, and
-// weights to 2^-34 ----
+// ---- rows that are left open: a team of blocks per row, a part of it each, and
+// weights to 2^-34.  The team is a cluster of eight blocks, or, where a cluster
+// has several rows, one block: eight are sooner done with one row, but wait for
+// one another. ----
 constexpr int kTeam = 8, kTeamLog = 3;
 constexpr int kTeamThreads = 512, kTeamWarps = kTeamThreads / 32;
 constexpr int kTeamList = 2048;
-constexpr int kTeamBins = 4096, kTeamSlice = kTeamBins / kTeam;
+constexpr int kTeamBins = 4096;
 constexpr int kTeamGroups = 1024;  // of 32 vectors: (2^20 / 4 / 8) / 32
 using TeamShared = SampleShared<kTeamThreads>;
-static_assert(kTeamSlice == kTeamThreads, "a thread per bin of a slice");
+constexpr int kTeamU = 4;          // vectors read together
+constexpr int kTeamRows = 8;       // rows that are listed before they are worked on
+constexpr int kTeamAlone = 3;      // from this many on, each block takes one alone
 
 struct TeamWork {
   uint64_t power[1024];             // 2^(j/1024) 2^62
@@ -855,6 +861,8 @@ struct TeamWork {
   uint64_t group[kTeamGroups + 2];  // the elements before the vectors, 32 vectors in a row each, the elements after
   uint32_t lo[kTeamBins], hi[kTeamBins];
   uint64_t box[2][2];               // what the blocks tell one another, in turn
+  int64_t row[kTeamRows];           // open rows, and their flags
+  int flag[kTeamRows];
   uint64_t base, key, incl;
 };
 
@@ -879,40 +887,37 @@ __device__ __forceinline__ uint32_t first_bin_start(uint32_t top, int b) {
 template <typename E>
 struct Team {
   Row<E> r;
-  int id0, rank, turn, scan_turn, groups;
+  int id0, rank, size, turn, scan_turn, groups;
   Weights weight;
   TeamShared& sh;
   TeamWork& work;
 
   // Weights to 2^-34 as Weights::exact, but with the powers of 2^(1/1024): the
-  // rest's series has three terms, and its one FP32 number is good to 2^-35.
-  __device__ __forceinline__ uint64_t exact(float x) const {
-    const float m = weight.m, ch = weight.ch;
-    const float d = x - m;
-    const float p = __fmul_rn(d, ch);
-    if (!(p >= kMinExponent - 1.0f)) return 0;
-    const float b = d - x, lost = (x - (d - b)) + (-m - b);
-    const float e = fmaf(lost, ch, fmaf(d, weight.cl, fmaf(d, ch, -p)));
-    if ((p - kMinExponent) + e < 0.0f) return 0;
-    const float z = p + 12288.0f;  // 1.5 2^13: steps of 1/1024
-    const int i = __float_as_int(z) - __float_as_int(12288.0f);
-    const float q = (p - (z - 12288.0f)) + e;
-    const int n = __float2int_rn(q * fmaf(q, fmaf(q, 0x1p40f * 0.0555041087f, 0x1p40f * 0.240226507f), 0x1p40f * 0.69314718f));
-    const uint64_t t = work.power[i & 1023];
-    return (t + (uint64_t)(((int64_t)n * (int64_t)(t >> 32)) >> 8)) >> (62 - weight.s - (i >> 10));
+  // rest's series has three terms, and its one FP32 number is good to 2^-35.  A
+  // function object, so that loops keep its numbers in registers.
+  struct Exact {
+    float m, ch, cl;
+    int s;
+    const uint64_t* power;
+    __device__ __forceinline__ uint64_t operator()(float x) const;
+  };
+  __device__ __forceinline__ Exact exact_weights() const {
+    return {weight.m, weight.ch, weight.cl, weight.s, work.power};
   }
-  // f(x, id, group) on this thread's elements of the part; end(group) after each
-  // group of this warp, in step
-  template <typename F, typename G>
-  __device__ __forceinline__ void each(F f, G end) const {
+  // f(x, id) on this thread's elements of the part; after(x, n, id) behind each n
+  // elements from id on; end(group) behind each group of this warp, in step
+  template <typename F, typename G, typename H>
+  __device__ __forceinline__ void each(F f, G end, H after) const {
     constexpr int N = Row<E>::kVec;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int g0 = warp; g0 < groups; g0 += kSaU * kTeamWarps) {
-      uint4 v[kSaU];
+    const Row<E> r = this->r;
+    const int id0 = this->id0, groups = this->groups;
+    for (int g0 = warp; g0 < groups; g0 += kTeamU * kTeamWarps) {
+      uint4 v[kTeamU];
 #pragma unroll
-      for (int u = 0; u < kSaU; ++u) v[u] = r.vec()[min((g0 + u * kTeamWarps) * 32 + lane, r.nvec - 1)];
+      for (int u = 0; u < kTeamU; ++u) v[u] = r.vec()[min((g0 + u * kTeamWarps) * 32 + lane, r.nvec - 1)];
 #pragma unroll
-      for (int u = 0; u < kSaU; ++u) {
+      for (int u = 0; u < kTeamU; ++u) {
         const int g = g0 + u * kTeamWarps, i = g * 32 + lane;
         if (g >= groups) break;
         if (i < r.nvec) {
@@ -920,34 +925,58 @@ struct Team {
           unpack(v[u], x);
 #pragma unroll
           for (int k = 0; k < N; ++k) f(x[k], id0 + r.head + i * N + k);
+          after(x, N, id0 + r.head + i * N);
         }
         end(g + 1);
       }
     }
     if (warp == 0) {
-      if (lane < r.head) f(to_f32(r.p[lane]), id0 + lane);
+      float x[N];
+      if (lane < r.head) {
+        x[0] = to_f32(r.p[lane]);
+        f(x[0], id0 + lane);
+        after(x, 1, id0 + lane);
+      }
       end(0);
-      if (lane < r.tail) f(to_f32(r.p[r.tail_start() + lane]), id0 + r.tail_start() + lane);
+      if (lane < r.tail) {
+        const int id = r.tail_start() + lane;
+        x[0] = to_f32(r.p[id]);
+        f(x[0], id0 + id);
+        after(x, 1, id0 + id);
+      }
       end(groups + 1);
     }
   }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    each(f, [](int) {});
+    each(f, [](int) {}, [](const auto&, int, int) {});
   }
   // f's sums into the groups
-  template <typename F>
-  __device__ __forceinline__ void sums(F f) const {
+  template <typename F, typename H>
+  __device__ __forceinline__ void sums(F f, H after) const {
     uint64_t v = 0;
+    uint64_t* group = work.group;
     each([&](float x, int id) { v += f(x, id); }, [&](int g) {
       v = warp_sum64(v);
-      if ((threadIdx.x & 31) == 0) work.group[g] = v;
+      if ((threadIdx.x & 31) == 0) group[g] = v;
       v = 0;
-    });
+    }, after);
     __syncthreads();
+  }
+  template <typename F>
+  __device__ __forceinline__ void sums(F f) const {
+    sums(f, [](const auto&, int, int) {});
   }
   __device__ __forceinline__ uint64_t scan(uint64_t v, uint64_t& total) {
     return block_scan<kTeamThreads>(v, total, sh, scan_turn);
+  }
+  __device__ __forceinline__ void sync() const {
+    if (size == 1) {
+      __syncthreads();
+    } else {
+      cluster_arrive();
+      cluster_wait();
+    }
   }
   // Two numbers of each block: lane r of every warp gets rank r's (0 from lane 8
   // on).  A barrier of the team.
@@ -955,10 +984,11 @@ struct Team {
     const int lane = threadIdx.x & 31;
     uint64_t* box = work.box[turn];
     if (threadIdx.x == 0) box[0] = a, box[1] = b;
-    cluster_arrive();
-    cluster_wait();
+    sync();
     va = vb = 0;
-    if (lane < kTeam) {
+    if (size == 1) {
+      if (lane == 0) va = box[0], vb = box[1];
+    } else if (lane < kTeam) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(box);
       va = cluster_load(p, lane) | (uint64_t)cluster_load(p + 1, lane) << 32;
       vb = cluster_load(p + 2, lane) | (uint64_t)cluster_load(p + 3, lane) << 32;
@@ -1032,7 +1062,7 @@ struct Team {
   // The blocks' lists together in the first block's; counts: each block's, by lane.
   __device__ __forceinline__ void gather(uint64_t counts) {
     int at = (int)__shfl_sync(0xFFFFFFFFu, counts, 0);
-    for (int q = 1; q < kTeam; ++q) {
+    for (int q = 1; q < size; ++q) {
       const int n = (int)__shfl_sync(0xFFFFFFFFu, counts, q);
       for (int j = threadIdx.x; j < n; j += kTeamThreads) {
         const uint32_t* p = reinterpret_cast<const uint32_t*>(&work.list[j]);
@@ -1046,6 +1076,7 @@ struct Team {
   // which `base` and the weights reach target: work.key and the sum, work.incl; 0
   // if none does, or base alone.
   __device__ __forceinline__ void reach(int n, uint64_t base, uint64_t target) {
+    const Exact exact = exact_weights();
     sort_list<kTeamThreads>(work.list, n);
     for (int j = threadIdx.x; j < n; j += kTeamThreads) work.weight[j] = exact(rank_logit(work.list[j]));
     if (threadIdx.x == 0) work.key = work.incl = 0;
@@ -1069,23 +1100,41 @@ struct Team {
     if (threadIdx.x == 0) sh.listed = 0;
     __syncthreads();
   }
-  // This thread's bin of the block's slice, over the team, and what comes before
-  // it.  Barriers of the team.
-  __device__ __forceinline__ uint64_t slice(bool both, uint64_t& before, uint64_t& sum) {
-    cluster_arrive();
-    cluster_wait();
-    const int b = rank * kTeamSlice + (int)threadIdx.x;
+  // The bins' sums over the team, each block a slice of them; what comes before a
+  // thread's bins, and the sum of all.  Barriers of the team.
+  __device__ __forceinline__ uint64_t slice(bool both, uint64_t& sum) {
+    sync();
+    const int each = kTeamBins / size / kTeamThreads, b0 = (rank * kTeamThreads + (int)threadIdx.x) * each;
     uint64_t n = 0, mine, all, none;
+    for (int i = 0; i < each; ++i) n += bin(b0 + i, both);
+    uint64_t before = scan(n, mine);
+    share(mine, 0, all, none);
+    before += warp_sum64((int)(threadIdx.x & 31) < rank ? all : 0);
+    sum = warp_sum64(all);
+    return before;
+  }
+  __device__ __forceinline__ uint64_t bin(int b, bool both) const {
+    if (size == 1) return work.lo[b] + (both ? (uint64_t)work.hi[b] << 32 : 0);
+    uint64_t n = 0;
 #pragma unroll
     for (int q = 0; q < kTeam; ++q) {
       n += cluster_load(&work.lo[b], q);
       if (both) n += (uint64_t)cluster_load(&work.hi[b], q) << 32;
     }
-    before = scan(n, mine);
-    share(mine, 0, all, none);
-    before += warp_sum64((int)(threadIdx.x & 31) < rank ? all : 0);
-    sum = warp_sum64(all);
     return n;
+  }
+  // The bin in which the sum over the bins, `before` in front of this thread's,
+  // reaches target (1 .. the sum): true for its thread.
+  __device__ __forceinline__ bool bin_at(uint64_t target, uint64_t before, bool both, int& b, uint64_t& at) const {
+    const int each = kTeamBins / size / kTeamThreads, b0 = (rank * kTeamThreads + (int)threadIdx.x) * each;
+    at = before;
+    if (target <= at) return false;
+    for (b = b0; b < b0 + each; ++b) {
+      const uint64_t n = bin(b, both);
+      if (target <= at + n) return true;
+      at += n;
+    }
+    return false;
   }
 
   // The last element of the shortest leading part, in the order of the keys and
@@ -1094,6 +1143,8 @@ struct Team {
   template <bool COUNT>
   __device__ __noinline__ bool select(uint64_t target, uint64_t least, uint64_t& key_out, uint64_t& incl_out) {
     const uint32_t top = rank_value(weight.m);
+    const Exact exact = exact_weights();
+    uint32_t *lo = work.lo, *hi = work.hi;
     uint32_t d0 = 0, d1 = 0xFFFFFFFFu;
     uint64_t base = 0, all, none;  // elements or weight before these distances
     for (int level = 0;; ++level) {
@@ -1106,18 +1157,18 @@ struct Team {
         if (x == neg_inf() || key < least || d < d0 || d > d1) return;
         const int b = level == 0 ? first_bin(top, top - d) : (int)((d - d0) >> shift);
         if (COUNT) {
-          atomicAdd(&work.lo[b], 1u);
+          atomicAdd(&lo[b], 1u);
         } else {
           const uint64_t w = exact(x);
-          if (w) add64(&work.lo[b], &work.hi[b], w);
+          if (w) add64(&lo[b], &hi[b], w);
         }
       });
-      uint64_t n0, sum;
-      const uint64_t n = slice(true, n0, sum);
+      uint64_t sum, at;
+      const uint64_t n0 = slice(true, sum) + base;
       if (threadIdx.x == 0) sh.found = 0;
       __syncthreads();
-      n0 += base;
-      if (n0 < target && target <= n0 + n) sh.found = 1 + rank * kTeamSlice + threadIdx.x, work.base = n0;
+      int its;
+      if (bin_at(target, n0, true, its, at)) sh.found = 1 + its, work.base = at;
       __syncthreads();
       share(sh.found, sh.found ? work.base : 0, all, none);
       const int bin = (int)warp_sum64(all) - 1;
@@ -1177,34 +1228,50 @@ struct Team {
   // weights, and lists the elements in between.  False, without a result, where
   // these are too many or the end is not among them.  log_s: of the row's weight.
   __device__ __forceinline__ bool draw_top_p(const Filters& fl, int V, int log_s, Drawn& out, bool& owner) {
-    const uint32_t top = rank_value(weight.m);
-    const float scale = ldexpf(1.0f, 31 - log_s);
+    const float scale = ldexpf(1.0f, 31 - log_s), m = weight.m, ch = weight.ch;
+    const Exact exact = exact_weights();
+    uint32_t* lo = work.lo;
+    // Bins of the FP32 exponent, which never rises where the logit falls: equal
+    // logits share a bin, and a bin's logits are above the next one's.
+    auto bin_of = [](float t) {
+      return min((uint32_t)(__float_as_int(fmaf(t, -97.5f, 12582912.0f)) - 0x4B400000), (uint32_t)kTeamBins - 1);
+    };
     clear(false);
     each([&](float x, int) {
-      const uint32_t v = __float2uint_rn(weight.ratio(x) * scale);
-      if (v) atomicAdd(&work.lo[first_bin(top, rank_value(x))], v);
+      const float t = __fmul_rn(x - m, ch);
+      const uint32_t v = __float2uint_rn(t >= kMinExponent ? exp2_fast(t) * scale : 0.0f);
+      if (v) atomicAdd(&lo[bin_of(t)], v);
     });
-    uint64_t n0, sum, all, none;
-    const uint64_t n = slice(false, n0, sum);
+    uint64_t sum, all, none, ignored;
+    const uint64_t n0 = slice(false, sum);
     // off by half a unit per element, and the error of FP32 weights
     const uint64_t mid = part_of<false>(sum, fmaxf(fl.top_p, 0.0f)), slack = (uint64_t)V / 2 + (sum >> 17) + 1;
-    const uint64_t low = mid > slack ? mid - slack : 0, high = min((unsigned long long)(mid + slack), (unsigned long long)sum);
+    const uint64_t low = mid > slack ? mid - slack : 1, high = min((unsigned long long)(mid + slack), (unsigned long long)sum);
     if (threadIdx.x == 0) work.key = work.incl = 0;
     __syncthreads();
-    if (n0 <= low && low < n0 + n) work.key = 1 + rank * kTeamSlice + threadIdx.x;
-    if (n0 < high && high <= n0 + n) work.incl = 1 + rank * kTeamSlice + threadIdx.x;
+    int its;
+    if (bin_at(low, n0, false, its, ignored)) work.key = 1 + its;
+    if (bin_at(high, n0, false, its, ignored)) work.incl = 1 + its;
     __syncthreads();
     share(work.key, work.incl, all, none);
     const int b0 = (int)warp_sum64(all) - 1, b1 = (int)warp_sum64(none) - 1;
     if (b0 < 0 || b1 < b0) return false;
-    const uint32_t d0 = first_bin_start(top, b0), d1 = b1 + 1 < kTeamBins ? first_bin_start(top, b1 + 1) - 1 : 0xFFFFFFFFu;
     uint64_t S = 0;
-    sums([&](float x, int id) {
-      const uint32_t d = top - rank_value(x);
+    uint32_t near = 0;  // a bit per element that is to be listed, the last one lowest
+    sums([&](float x, int) {
+      const uint32_t b = bin_of(__fmul_rn(x - m, ch));
       const uint64_t w = exact(x);
       S += w;
-      if (d >= d0 && d <= d1 && w) list(x, id);
-      return d < d0 ? w : 0;
+      near = near << 1 | (b - (uint32_t)b0 <= (uint32_t)(b1 - b0) ? 1u : 0u);
+      return b < (uint32_t)b0 ? w : 0;
+    }, [&](const auto& x, int n, int id) {
+      if (near) {
+        constexpr int N = Row<E>::kVec;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          if (k < n && near >> (n - 1 - k) & 1) list(x[k], id + k);
+        near = 0;
+      }
     });
     const int listed = (int)sh.listed;
     uint64_t part;
@@ -1250,20 +1317,14 @@ struct Team {
 
   __device__ __forceinline__ bool draw(const Filters& fl, int V, int log_s, Drawn& out) {
     const bool filtered = fl.top_k > 0 || fl.top_p < 1.0f || fl.min_p > 0.0f;
+    const Exact exact = exact_weights();
     bool owner;
     if (fl.top_k == 0 && fl.top_p < 1.0f && !(fl.min_p > 0.0f) && draw_top_p(fl, V, log_s, out, owner)) return owner;
-    uint64_t least = 0, key, incl, mine, before;
-    if (filtered) {
-      sums([&](float x, int) { return exact(x); });
-      out.total = total(mine, before);
-    }
+    uint64_t least = 0, key, incl, mine, before, S = 0;
     if (fl.top_k > 0 && select<true>((uint64_t)fl.top_k, 0, key, incl)) least = key;
     if (fl.top_p < 1.0f) {
-      uint64_t mass = out.total;
-      if (least) {
-        sums([&](float x, int id) { return rank_key(x, (uint32_t)id) >= least ? exact(x) : 0; });
-        mass = total(mine, before);
-      }
+      sums([&](float x, int id) { return rank_key(x, (uint32_t)id) >= least ? exact(x) : 0; });
+      const uint64_t mass = total(mine, before);
       const uint64_t target = max(1ull, (unsigned long long)part_of<true>(mass, fmaxf(fl.top_p, 0.0f)));
       if (select<false>(target, least, key, incl)) least = max(least, key);
     }
@@ -1273,54 +1334,102 @@ struct Team {
       least = max(least, min_p_key(weight.m, sh.edge));
     }
     auto kept = [&](float x, int id) { return x != neg_inf() && rank_key(x, (uint32_t)id) >= least ? exact(x) : 0; };
-    sums(kept);
-    out.kept = total(mine, before);
-    if (!filtered) out.total = out.kept;
+    sums([&](float x, int id) {
+      const uint64_t w = exact(x);
+      S += w;
+      return x != neg_inf() && rank_key(x, (uint32_t)id) >= least ? w : 0;
+    });
+    out.kept = out.total = total(mine, before);
+    if (filtered) {
+      uint64_t part, all, none;
+      scan(S, part);
+      share(part, 0, all, none);
+      out.total = warp_sum64(all);
+    }
     const uint64_t target = part_of<false>(out.kept, fl.u);
     return find(min((unsigned long long)target, (unsigned long long)out.kept - 1), mine, before, kept);
   }
 };
+
+// Without branches, so that the weights of a vector are formed side by side: an
+// exponent out of range is held at -44, where only its own bits are used, and the
+// result dropped.
+template <typename E>
+__device__ __forceinline__ uint64_t Team<E>::Exact::operator()(float x) const {
+  const float d = x - m;
+  const float p0 = __fmul_rn(d, ch), p = fmaxf(p0, -44.0f);
+  const float b = d - x, lost = (x - (d - b)) + (-m - b);
+  const float e = fmaf(lost, ch, fmaf(d, cl, fmaf(d, ch, -p0)));
+  const float z = p + 12288.0f;  // 1.5 2^13: steps of 1/1024
+  const int i = __float_as_int(z) - __float_as_int(12288.0f);
+  const float q = (p - (z - 12288.0f)) + e;
+  const int n = __float2int_rn(q * fmaf(q, fmaf(q, 0x1p40f * 0.0555041087f, 0x1p40f * 0.240226507f), 0x1p40f * 0.69314718f));
+  const uint64_t t = power[i & 1023];
+  const uint64_t w = (t + (uint64_t)(((int64_t)n * (int64_t)(t >> 32)) >> 8)) >> (62 - s - (i >> 10));
+  return (p0 - kMinExponent) + e >= 0.0f ? w : 0;
+}
 
 template <typename E>
 __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs a) {
   extern __shared__ uint4 smem[];
   TeamWork& work = *reinterpret_cast<TeamWork*>(smem);
   TeamShared& sh = *reinterpret_cast<TeamShared*>(&work + 1);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = (int)blockIdx.x % kTeam;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = (int)blockIdx.x % kTeam;
   const int64_t teams = gridDim.x / kTeam;
+  // alone with a row only where its groups have room
+  const bool alone_fits = a.V / Row<E>::kVec <= kTeamGroups * 32;
   bool ready = false;
   int turn = 0, scan_turn = 0;
   begin_kernel();
-  for (int64_t t0 = blockIdx.x / kTeam; t0 < a.T; t0 += 32 * teams) {
-    const int64_t mine = t0 + lane * teams;
-    const int flag = mine < a.T ? a.tokens[mine] : 0;
-    uint32_t open = __ballot_sync(0xFFFFFFFFu, flag <= kOpen);
-    if (open && !ready) {
+  int64_t next = blockIdx.x / kTeam;
+  while (next < a.T) {
+    // the next open rows of this cluster, the same for its blocks: none is closed
+    // before all blocks have listed it
+    int rows = 0;
+    while (next < a.T && rows < kTeamRows) {
+      const int64_t mine = next + lane * teams;
+      const int flag = mine < a.T ? a.tokens[mine] : 0;
+      uint32_t open = __ballot_sync(0xFFFFFFFFu, flag <= kOpen);
+      int step = 32;
+      for (; open; open &= open - 1) {
+        const int who = __ffs(open) - 1;
+        if (rows == kTeamRows) {
+          step = who;  // from here on the next time
+          break;
+        }
+        if (threadIdx.x == (unsigned)who) work.row[rows] = mine, work.flag[rows] = flag;
+        ++rows;
+      }
+      next += step * teams;
+    }
+    if (rows == 0) break;
+    if (!ready) {
       load_exp2(sh);
       __syncthreads();
-      Weights one;  // 2^((j - 1024) / 1024) 2^52, for the powers
+      Weights one;  // 2^(j / 1024 - 1), of unit 2^-61
       one.m = 1024.0f, one.ch = 0x1p-10f, one.cl = 0.0f, one.s = 61, one.exp2 = sh.exp2;
       for (int j = threadIdx.x; j < 1024; j += kTeamThreads) work.power[j] = one.exact((float)j) << 2;
-      __syncthreads();
       ready = true;
     }
-    for (; open; open &= open - 1) {
-      const int who = __ffs(open) - 1;
-      const int64_t t = t0 + who * teams;
-      const int log_s = kOpen - __shfl_sync(0xFFFFFFFFu, flag, who);
+    cluster_arrive();
+    cluster_wait();
+    const int size = rows >= kTeamAlone && alone_fits ? 1 : kTeam, rank = size == 1 ? 0 : me, lg = size == 1 ? 0 : kTeamLog;
+    for (int at = size == 1 ? me : 0; at < rows; at += size == 1 ? kTeam : 1) {
+      const int64_t t = work.row[at];
+      const int log_s = kOpen - work.flag[at];
       const E* logits = static_cast<const E*>(a.logits) + t * a.ld;
       const Row<E> whole(logits, a.V);
-      const int v0 = whole.part(rank, kTeamLog), v1 = whole.part(rank + 1, kTeamLog);
+      const int v0 = whole.part(rank, lg), v1 = whole.part(rank + 1, lg);
       const int id0 = rank == 0 ? 0 : whole.head + v0 * Row<E>::kVec;
-      const int id1 = rank == kTeam - 1 ? a.V : whole.head + v1 * Row<E>::kVec;
+      const int id1 = rank == size - 1 ? a.V : whole.head + v1 * Row<E>::kVec;
       const Row<E> r(logits + id0, id1 - id0);
-      Team<E> team = {r, id0, rank, turn, scan_turn, (r.nvec + 31) / 32, Weights(), sh, work};
+      Team<E> team = {r, id0, rank, size, turn, scan_turn, (r.nvec + 31) / 32, Weights(), sh, work};
       bool params;
       const Filters fl = filters_of(a, t, params);
-      // the row's maximum, in the order of rank_value
-      uint32_t top = 0;
-      team.each([&](float x, int) { top = max(top, rank_value(x)); });
-      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      // the row's maximum, a number
+      float high = neg_inf();
+      team.each([&](float x, int) { high = fmaxf(high, x); });
+      uint32_t top = __reduce_max_sync(0xFFFFFFFFu, rank_value(high));
       if (lane == 0) sh.scan[0][warp] = top;
       __syncthreads();
       top = __reduce_max_sync(0xFFFFFFFFu, lane < kTeamWarps ? (uint32_t)sh.scan[0][lane] : 0u);
@@ -1335,11 +1444,13 @@ __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs
         put_drawn(a, t, out, fl.inv_t, team.weight.m, team.weight.s);
       }
       __syncthreads();
-      turn = team.turn, scan_turn = team.scan_turn;
+      scan_turn = team.scan_turn;
+      turn = team.turn;
     }
+    turn = 0;
+    cluster_arrive();  // no block goes on, or ends, while another reads its shared memory
+    cluster_wait();
   }
-  cluster_arrive();  // no block ends while another reads its shared memory
-  cluster_wait();
 }
 
 template <int TH>
