@@ -857,13 +857,20 @@ constexpr int kTeamAlone = 3;      // from this many on, each block takes one al
 
 struct TeamWork {
   uint64_t power[1024];             // 2^(j/1024) 2^62
-  uint64_t list[kTeamList], weight[kTeamList];
+  union {
+    struct {
+      uint64_t list[kTeamList], weight[kTeamList];
+    };
+    uint64_t table[kTeamBins];      // BF16: the weight of each bin's one value
+  };
   uint64_t group[kTeamGroups + 2];  // the elements before the vectors, 32 vectors in a row each, the elements after
+  uint64_t ties[kTeamGroups + 2];
   uint32_t lo[kTeamBins], hi[kTeamBins];
   uint64_t box[2][2];               // what the blocks tell one another, in turn
   int64_t row[kTeamRows];           // open rows, and their flags
   int flag[kTeamRows];
   uint64_t base, key, incl;
+  int edge;
 };
 
 // Bins of the ranks at and below the row's maximum's, `top`: by 1/128 of a power
@@ -996,9 +1003,10 @@ struct Team {
     turn ^= 1;
   }
   // The groups' sums over the team, and this block's and those before it.
-  __device__ __forceinline__ uint64_t total(uint64_t& mine, uint64_t& before) {
+  __device__ __forceinline__ uint64_t total(uint64_t& mine, uint64_t& before) { return total(work.group, mine, before); }
+  __device__ __forceinline__ uint64_t total(const uint64_t* group, uint64_t& mine, uint64_t& before) {
     uint64_t v = 0, all, none;
-    for (int g = threadIdx.x; g < groups + 2; g += kTeamThreads) v += work.group[g];
+    for (int g = threadIdx.x; g < groups + 2; g += kTeamThreads) v += group[g];
     scan(v, mine);
     share(mine, 0, all, none);
     before = warp_sum64((int)(threadIdx.x & 31) < rank ? all : 0);
@@ -1008,16 +1016,20 @@ struct Team {
   // given: true for the block that has it, sh.id (within the row) and sh.x.
   template <typename F>
   __device__ __forceinline__ bool find(uint64_t target, uint64_t mine, uint64_t before, F f) {
+    return find(work.group, target, mine, before, f);
+  }
+  template <typename F>
+  __device__ __forceinline__ bool find(const uint64_t* group, uint64_t target, uint64_t mine, uint64_t before, F f) {
     if (target < before || target >= before + mine) return false;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = groups + 2;
     const int each = (n + kTeamThreads - 1) / kTeamThreads, g0 = (int)threadIdx.x * each;
     const uint64_t left = target - before;
     uint64_t sum = 0, all;
-    for (int g = g0; g < min(g0 + each, n); ++g) sum += work.group[g];
+    for (int g = g0; g < min(g0 + each, n); ++g) sum += group[g];
     uint64_t b = scan(sum, all);
     if (b <= left && left < b + sum) {
       int g = g0;
-      while (b + work.group[g] <= left) b += work.group[g++];
+      while (b + group[g] <= left) b += group[g++];
       sh.at = g, sh.left = b;
     }
     __syncthreads();
@@ -1315,10 +1327,245 @@ struct Team {
     return true;
   }
 
+  // ---- BF16: a bin per value ----
+  // The 16 bits in the order of the values, by distance below the maximum's: 2048
+  // values (sixteen powers of two), one bin for all down to -2^-10, 2046 values (16
+  // powers of two) below that, and a bin for the rest.
+  static constexpr int kMid = kTeamNear, kLast = kTeamBins - 1;
+  struct Bins {
+    uint32_t top;  // rank of the maximum, in both halves
+    int below;     // distance of a value below -2^-10, less its bin
+    __device__ __forceinline__ static uint32_t rank(uint32_t pair) {
+      uint32_t sign;
+      asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(sign) : "r"(pair));  // each half its sign bit
+      return pair ^ (sign | 0x80008000u);
+    }
+    __device__ __forceinline__ Bins(float m) {
+      const uint32_t t = rank_value(m) >> 16;  // of 0, not -0
+      top = t << 16 | t;
+      below = (int)t - 0x457F - kMid;  // -2^-10 has rank 0x457F and lies in bin kMid
+    }
+    __device__ __forceinline__ int at(uint32_t d) const {
+      return d < (uint32_t)kTeamNear ? (int)d : max(kMid, min((int)d - below, kLast));
+    }
+    __device__ __forceinline__ int of(float x) const {
+      const uint32_t r = rank(__float_as_uint(x) >> 16) & 0xFFFFu, t = top & 0xFFFFu;
+      return at(t > r ? t - r : 0u);
+    }
+    // The value of a bin that has one.
+    __device__ __forceinline__ float value(int b) const {
+      const int r = (int)(top & 0xFFFFu) - (b < kTeamNear ? b : b + below);
+      if (r <= 0x7F) return neg_inf();  // none
+      const uint32_t bits = r & 0x8000 ? (uint32_t)r ^ 0x8000u : ~(uint32_t)r & 0xFFFFu;
+      return __uint_as_float(bits << 16);
+    }
+  };
+  // f(bin) on this thread's elements, end(group) as in each; and several(x, bin) on
+  // the elements of the bins of several values, which are few: a vector is looked
+  // through only where it has one.
+  template <typename F, typename S, typename G>
+  __device__ __forceinline__ void each_bin(const Bins& bins, F f, S several, G end) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Row<E> r = this->r;
+    const int groups = this->groups;
+    auto one = [&](uint32_t bits) {
+      const float x = __uint_as_float(bits << 16);
+      const int b = bins.of(x);
+      f(b);
+      if (b == kMid || b == kLast) several(x, b);
+    };
+    for (int g0 = warp; g0 < groups; g0 += kTeamU * kTeamWarps) {
+      uint4 v[kTeamU];
+#pragma unroll
+      for (int u = 0; u < kTeamU; ++u) v[u] = r.vec()[min((g0 + u * kTeamWarps) * 32 + lane, r.nvec - 1)];
+#pragma unroll
+      for (int u = 0; u < kTeamU; ++u) {
+        const int g = g0 + u * kTeamWarps;
+        if (g >= groups) break;
+        if (g * 32 + lane < r.nvec) {
+          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          bool any = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t d = bins.top - Bins::rank(w[k]);  // of both halves: none borrows, the maximum is at the top
+            const int a = bins.at(d & 0xFFFFu), b = bins.at(d >> 16);
+            f(a);
+            f(b);
+            any |= a == kMid || a == kLast || b == kMid || b == kLast;
+          }
+          if (any) {
+            uint64_t lo = w[0] | (uint64_t)w[1] << 32, hi = w[2] | (uint64_t)w[3] << 32;
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+              const float x = __uint_as_float((uint32_t)lo << 16);
+              const int b = bins.of(x);
+              if (b == kMid || b == kLast) several(x, b);
+              lo = lo >> 16 | hi << 48, hi >>= 16;
+            }
+          }
+        }
+        end(g + 1);
+      }
+    }
+    if (warp == 0) {
+      if (lane < r.head) one(r.p[lane]);
+      end(0);
+      if (lane < r.tail) one(r.p[r.tail_start() + lane]);
+      end(groups + 1);
+    }
+  }
+  // The bin in which the sum over the bins of n(b) reaches target, with what comes
+  // before it: shared with the team.  `before`: in front of this thread's bins.
+  template <typename N>
+  __device__ __forceinline__ int reach_bin(uint64_t target, uint64_t before, N n, uint64_t& at) {
+    const int each = kTeamBins / size / kTeamThreads, b0 = (rank * kTeamThreads + (int)threadIdx.x) * each;
+    if (threadIdx.x == 0) work.key = work.incl = 0;
+    __syncthreads();
+    for (int b = b0; b < b0 + each && before < target; ++b) {
+      const uint64_t v = n(b);
+      if (target <= before + v) work.key = 1 + b, work.incl = before;
+      before += v;
+    }
+    __syncthreads();
+    uint64_t all, none;
+    share(work.key, work.incl, all, none);
+    at = warp_sum64(none);
+    return (int)warp_sum64(all) - 1;
+  }
+
+  // All filters from one histogram of the values, whose weights are exact.  False,
+  // without a result, where what is kept ends in a bin of several values.
+  __device__ __noinline__ bool draw_bf16(const Filters& fl, int V, Drawn& out, bool& owner) {
+    const bool filtered = fl.top_k > 0 || fl.top_p < 1.0f || fl.min_p > 0.0f;
+    const Exact exact = exact_weights();
+    const Bins bins(weight.m);
+    // 0 and -0, which are equal, and -inf lie in bins of several values but below
+    // a maximum of less than 2^-111 or of the lowest values
+    const uint32_t first_rank = bins.top & 0xFFFFu;
+    if (first_rank - 0x8000u < (uint32_t)kTeamNear || first_rank < 0x80u + kTeamNear) return false;
+    uint64_t* table = work.table;
+    for (int b = threadIdx.x; b < kTeamBins; b += kTeamThreads)
+      table[b] = b == kMid || b == kLast ? 0 : exact(bins.value(b));
+    int last = kTeamBins;       // kept are the elements of the bins before `last`
+    uint64_t take = 0, all, none;  // and the first `take` of it
+    if (filtered) {
+      uint32_t* lo = work.lo;
+      uint64_t mid = 0, rest = 0;  // weights of the bins of several values
+      clear(false);
+      uint32_t masked = 0;
+      each_bin(bins, [&](int b) { atomicAdd(&lo[b], 1u); }, [&](float x, int b) {
+        const uint64_t w = exact(x);
+        (b == kMid ? mid : rest) += w;
+        masked += x == neg_inf();
+      }, [](int) {});
+      __syncthreads();
+      if (masked) atomicSub(&lo[kLast], masked);
+      uint64_t a, b;
+      scan(mid, a);
+      scan(rest, b);
+      share(a, b, all, none);
+      mid = warp_sum64(all), rest = warp_sum64(none);
+      const int each = kTeamBins / size / kTeamThreads, b0 = (rank * kTeamThreads + (int)threadIdx.x) * each;
+      auto number = [&](int at) { return bin(at, false); };
+      auto mass = [&](int at) { return at == kMid ? mid : at == kLast ? rest : table[at] * bin(at, false); };
+      uint64_t n = 0, w = 0, mine_n, mine_w;
+      for (int at = b0; at < b0 + each; ++at) n += number(at), w += mass(at);
+      uint64_t n0 = scan(n, mine_n), w0 = scan(w, mine_w);
+      share(mine_n, mine_w, all, none);
+      const int lane = threadIdx.x & 31;
+      n0 += warp_sum64(lane < rank ? all : 0), w0 += warp_sum64(lane < rank ? none : 0);
+      uint64_t kept = out.total = warp_sum64(none), at;
+      if (fl.top_k > 0) {
+        const int found = reach_bin((uint64_t)fl.top_k, n0, number, at);
+        if (found == kMid || found == kLast) return false;
+        if (found >= 0) {
+          last = found, take = (uint64_t)fl.top_k - at;
+          if (fl.top_p < 1.0f) {  // the weight up to there
+            if (threadIdx.x == 0) work.incl = 0;
+            __syncthreads();
+            if (found >= b0 && found < b0 + each) {
+              uint64_t before = w0;
+              for (int k = b0; k < found; ++k) before += mass(k);
+              work.incl = before;
+            }
+            __syncthreads();
+            share(work.incl, 0, all, none);
+            kept = warp_sum64(all) + take * table[found];
+          }
+        }
+      }
+      if (fl.top_p < 1.0f) {
+        const uint64_t target = max(1ull, (unsigned long long)part_of<true>(kept, fmaxf(fl.top_p, 0.0f)));
+        const int found = reach_bin(target, w0, mass, at);
+        if (found == kMid || found == kLast || found < 0) return false;
+        last = found, take = (target - at + table[found] - 1) / table[found];
+      }
+      if (fl.min_p > 0.0f) {  // the first bin below the edge
+        if (threadIdx.x == 0) min_p_edge(fl, sh.edge), work.edge = kTeamBins;
+        __syncthreads();
+        const uint32_t edge = (uint32_t)(min_p_key(weight.m, sh.edge) >> 32);
+        for (int k = threadIdx.x; k < kTeamBins; k += kTeamThreads)
+          if (k != kMid && k != kLast && rank_value(bins.value(k)) < edge) {
+            atomicMin(&work.edge, k);
+            break;
+          }
+        __syncthreads();
+        const int first = work.edge;
+        // among the values of the one bin, or those of the other where they count
+        if (first < last || (first == last && take > 0)) {
+          if (first == kMid + 1 || (first == kTeamBins && rest)) return false;
+          last = first, take = 0;
+        }
+        __syncthreads();
+      }
+    }
+    // weights before `last`, and elements of it
+    uint64_t v = 0;
+    uint32_t ties = 0;
+    __syncthreads();
+    each_bin(bins, [&](int b) {
+      v += b < last ? table[b] : 0;
+      ties += b == last ? 1 : 0;
+    }, [&](float x, int b) { v += b < last ? exact(x) : 0; }, [&](int g) {
+      v = warp_sum64(v);
+      ties = __reduce_add_sync(0xFFFFFFFFu, ties);
+      if ((threadIdx.x & 31) == 0) work.group[g] = v, work.ties[g] = ties;
+      v = 0, ties = 0;
+    });
+    __syncthreads();
+    uint64_t mine, before, key = 0;
+    if (take > 0) {
+      total(work.ties, mine, before);
+      const int n = groups + 2, each = (n + kTeamThreads - 1) / kTeamThreads, g0 = (int)threadIdx.x * each;
+      uint64_t sum = 0, part;
+      for (int g = g0; g < min(g0 + each, n); ++g) sum += work.ties[g];
+      uint64_t at = scan(sum, part) + before;
+      for (int g = g0; g < min(g0 + each, n) && at < take; at += work.ties[g++])
+        work.group[g] += table[last] * min((unsigned long long)work.ties[g], (unsigned long long)(take - at));
+      __syncthreads();
+      if (find(work.ties, take - 1, mine, before, [&](float x, int) { return (uint64_t)(bins.of(x) == last); }))
+        key = rank_key(sh.x, (uint32_t)sh.id);
+      share(key, 0, all, none);
+      key = warp_sum64(all);
+    }
+    out.kept = total(mine, before);
+    if (!filtered) out.total = out.kept;
+    owner = find(min((unsigned long long)part_of<false>(out.kept, fl.u), (unsigned long long)out.kept - 1), mine, before,
+                 [&](float x, int id) -> uint64_t {
+                   const int b = bins.of(x);
+                   if (b == kMid || b == kLast) return b < last ? exact(x) : 0;
+                   return b < last || (b == last && take > 0 && rank_key(x, (uint32_t)id) >= key) ? table[b] : 0;
+                 });
+    return true;
+  }
+
   __device__ __forceinline__ bool draw(const Filters& fl, int V, int log_s, Drawn& out) {
     const bool filtered = fl.top_k > 0 || fl.top_p < 1.0f || fl.min_p > 0.0f;
     const Exact exact = exact_weights();
     bool owner;
+    if constexpr (sizeof(E) == 2) {
+      if (draw_bf16(fl, V, out, owner)) return owner;
+    }
     if (fl.top_k == 0 && fl.top_p < 1.0f && !(fl.min_p > 0.0f) && draw_top_p(fl, V, log_s, out, owner)) return owner;
     uint64_t least = 0, key, incl, mine, before, S = 0;
     if (fl.top_k > 0 && select<true>((uint64_t)fl.top_k, 0, key, incl)) least = key;
@@ -1461,7 +1708,9 @@ static int launch_sample(const SampleArgs& a, cudaStream_t s) {
   return launch_kernel(f, (unsigned)(a.T < most ? a.T : most), TH, kSaSmem<TH>, 1, s, a);
 }
 int launch_sample_tokens(const SampleArgs& a, cudaStream_t s) {
-  const int rc = launch_sample<512>(a, s);
+  // Two blocks of 512 threads per SM while each row has one at once; else four of
+  // 256, whose ends the others cover.
+  const int rc = a.T <= 2 * gemm_num_ctas() ? launch_sample<512>(a, s) : launch_sample<256>(a, s);
   if (rc != 0) return rc;
   constexpr int smem = (int)(sizeof(TeamWork) + sizeof(TeamShared));
   auto f = a.dtype == MOE_DTYPE_BF16 ? sample_open_kernel<uint16_t> : sample_open_kernel<float>;
