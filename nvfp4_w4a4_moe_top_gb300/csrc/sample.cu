@@ -56,7 +56,7 @@ __device__ __forceinline__ uint64_t fixed(float w, int s) {
 
 template <int TH>
 struct SampleShared {
-  static constexpr int NW = TH / 32, kList = TH < 512 ? 4 * TH : TH < 1024 ? 2 * TH : TH;
+  static constexpr int NW = TH / 32, kList = 1536;  // weighed elements: top_k of 1000 among them
   uint64_t exp2[64];               // 2^(j/64) 2^62
   uint64_t part[kSaRuns + 2][NW];  // sums of the runs by warp; the row's ends
   uint64_t sums[kSaRuns + 2];      // of all warps
@@ -72,8 +72,8 @@ struct SampleShared {
 // What shares its memory with the ring that the logits come through.
 template <int TH>
 struct SampleWork {
-  static constexpr int kHot = 1024;
-  uint64_t list[SampleShared<TH>::kList], weight[SampleShared<TH>::kList];
+  static constexpr int kHot = TH * kSaRuns, kListed = 2048;
+  uint64_t list[kListed], weight[SampleShared<TH>::kList];
   union {
     struct {
       uint32_t lo[kSaNear], hi[kSaNear];
@@ -289,9 +289,11 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t& total, Samp
 // the sum of f(x, id) is above `left`; `first`: the sum before the part.  sh.id
 // (-1 if the elements do not reach it), sh.x, and the sum over the row before and
 // with that element, sh.before, sh.after.
-template <typename E, int TH, typename F>
+// (-1 too if the sums of vectors and the elements differ.)  of_vector: the sum of
+// f over the elements of a vector.
+template <typename E, int TH, typename F, typename H>
 __device__ __forceinline__ void pick_in(const SampleRow<E, TH>& row, int e, uint64_t left, uint64_t first, F f,
-                                        SampleShared<TH>& sh, uint64_t* group, int& turn) {
+                                        H of_vector, SampleShared<TH>& sh, uint64_t* group, int& turn) {
   constexpr int NW = TH / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto walk = [&](float x, int id, uint64_t& before, bool& done) {
@@ -323,9 +325,7 @@ __device__ __forceinline__ void pick_in(const SampleRow<E, TH>& row, int e, uint
     for (int u = 0; u < kSaU; ++u) v[u] = row.r.vec()[min(i0 + u * TH, row.r.nvec - 1)];
 #pragma unroll
     for (int u = 0; u < kSaU; ++u) {
-      uint64_t w = 0;
-      if (i0 + u * TH < row.r.nvec) row.vector(v[u], i0 + u * TH, [&](float x, int id) { w += f(x, id); });
-      w = warp_sum64(w);
+      const uint64_t w = warp_sum64(i0 + u * TH < row.r.nvec ? of_vector(v[u]) : 0);
       if (lane == 0) group[(j + u) * NW + warp] = w;
     }
   }
@@ -402,29 +402,24 @@ __device__ __forceinline__ void sum_ends(const SampleRow<E, TH>& row, F f, Sampl
   if (threadIdx.x == 0) sh.part[0][0] = a, sh.part[row.runs + 1][0] = b;
 }
 
-// The first id up to which the sum of whole numbers over the row is above
-// target_of(sum over the row), as pick_in gives it, with the target in
-// sh.target.  own(q): this thread's sum of run q; f(x, id) one element's; group:
-// room for the sums within a run, in use by nobody.  Returns the sum over the
-// row, which is not 0.
-template <typename E, int TH, typename S, typename F, typename G>
-__device__ __forceinline__ uint64_t pick(const SampleRow<E, TH>& row, S own, F f, G target_of, SampleShared<TH>& sh,
+// The first id up to which the sum of f over the row is above part u of all of
+// it, as pick_in gives it, with the target in sh.target.  sh.part has the runs'
+// sums.  group: room for the sums within a run, in use by nobody.  Returns the sum
+// over the row, which is not 0.
+template <typename E, int TH, typename F, typename H>
+__device__ __forceinline__ uint64_t pick(const SampleRow<E, TH>& row, float u, F f, H of_vector, SampleShared<TH>& sh,
                                          uint64_t* group, int& turn) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int q = 0; q < row.runs; ++q) {
-    const uint64_t v = warp_sum64(own(q));
-    if (lane == 0) sh.part[q + 1][warp] = v;
-  }
   sum_ends<E, TH>(row, f, sh);
   __syncthreads();
   const uint64_t total = sum_parts<E, TH>(row, sh);
-  const uint64_t target = min((unsigned long long)target_of(total), (unsigned long long)total - 1);
+  const uint64_t target = min((unsigned long long)part_of<false>(total, u), (unsigned long long)total - 1);
   uint64_t first;
   const int e = find_part<E, TH>(row, target, first, sh);
   if (threadIdx.x == 0) sh.target = target;
-  pick_in<E, TH>(row, e, target - first, first, f, sh, group, turn);
+  pick_in<E, TH>(row, e, target - first, first, f, of_vector, sh, group, turn);
   return total;
 }
+
 // n distinct keys, descending, in list (room for the next power of two).
 template <int TH>
 __device__ __noinline__ void sort_list(uint64_t* list, int n) {
@@ -457,7 +452,7 @@ __device__ __noinline__ void sort_list(uint64_t* list, int n) {
 // Sums of the n <= LIST weights up to and with each, in their place.
 template <int LIST, int TH>
 __device__ __forceinline__ void sum_list(uint64_t* weight, int n, SampleShared<TH>& sh, int& turn) {
-  constexpr int PER = LIST / TH;
+  constexpr int PER = (LIST + TH - 1) / TH;
   uint64_t w[PER], v = 0, total;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -600,7 +595,6 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
     auto run_float = [&](int q) {  // at most 2^10
       return sums[q * TH] * exp2_fast(RunSum::shift_of(highs[q * TH], c) - M) * to_m;
     };
-    auto run_sum = [&](int q) { return fixed(run_float(q), weight.s); };
     const bool shift_ok = fabsf(mc) <= kShiftLimit;
     const bool filtered = fl.top_k > 0 || fl.top_p < 1.0f || fl.min_p > 0.0f;
     uint64_t edge = 0;  // keys below have less than min_p
@@ -609,7 +603,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
     uint64_t sum = 0, err, weight_err;  // errors of sums of the pass, and of weights by themselves
     const float unit = ldexpf(1.0f, -weight.s);
     int e = 0;  // the part of the row with the token
-    if (!shift_ok) {  // the pass's weights are out of range
+    if (filtered && !shift_ok) {  // the pass's weights are out of range
       row.all(0, [&](float x, int) { sum += weight.fast(x); });
       block_scan<TH>(sum, out.total, sh, turn);
     } else if (filtered) {
@@ -621,26 +615,53 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
       block_scan<TH>(sum, out.total, sh, turn);
     }
     if (!filtered) {
-      out.total = out.kept = pick<E, TH>(row, [&](int q) {
-        uint64_t v = 0;
-        if (shift_ok) v = run_sum(q);
-        else row.run(q, [&](float x, int) { v += weight.fast(x); });
-        return v;
-      }, [&](float x, int) { return weight.fast(x); }, [&](uint64_t all) { return part_of<false>(all, fl.u); }, sh,
-                                         work.group, turn);
+      // the warp's sums of the eight runs: lane l ends with run l / 4's
+      float w[kSaRuns];
+#pragma unroll
+      for (int q = 0; q < kSaRuns; ++q) {
+        w[q] = 0.0f;
+        if (q < row.runs) {
+          if (shift_ok) w[q] = run_float(q);
+          else row.run(q, [&](float x, int) { w[q] += weight.ratio(x); });
+        }
+      }
+#pragma unroll
+      for (int h = 4, o = 16; h > 0; h /= 2, o /= 2)
+#pragma unroll
+        for (int q = 0; q < h; ++q) {
+          const float keep = lane & o ? w[q + h] : w[q], give = lane & o ? w[q] : w[q + h];
+          w[q] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+        }
+      w[0] += __shfl_xor_sync(0xFFFFFFFFu, w[0], 2);
+      w[0] += __shfl_xor_sync(0xFFFFFFFFu, w[0], 1);
+      if ((lane & 3) == 0 && lane / 4 < row.runs) sh.part[lane / 4 + 1][warp] = fixed(w[0], weight.s);
+      out.total = out.kept = pick<E, TH>(row, fl.u, [&](float x, int) { return weight.fast(x); }, [&](const uint4& v) {
+        constexpr int N = Row<E>::kVec;
+        float x[N];
+        unpack(v, x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = weight.ratio(x[e]);
+#pragma unroll
+        for (int h = N / 2; h > 0; h /= 2)
+#pragma unroll
+          for (int e = 0; e < h; ++e) x[e] += x[e + h];
+        return fixed(x[0], weight.s);
+      }, sh, work.group, turn);
       out.id = sh.id, out.x = sh.x;
       uint64_t first;
       e = find_part<E, TH>(row, sh.target, first, sh);
     }
     {
       // in the pass 3 additions per sum of pairs, 3 to join them, one per batch of
-      // a run, a product with to_m; with the filters 8 for the thread's runs, and
-      // to_m's own error, which is otherwise the same for all
+      // a run, a product with to_m; then 5 over the warp, or, with the filters, 8
+      // for the thread's runs, and to_m's own error, which is otherwise the same
+      // for all.  Weights by themselves: 3 in a vector, and with the range of the
+      // pass exceeded as many as a run has elements, and 5 over the warp.
       const float S = (float)out.total * unit;
-      const float near = sum_error(S, a.V, cl_ch, 2, 0);
+      const float near = sum_error(S, a.V, cl_ch, 2, 3);
       weight_err = (uint64_t)((float)(filtered ? out.total : sh.sums[e]) * (near + 0x1p-22f));
-      err = shift_ok ? (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 1, 7 + row.per / kSaU + (filtered ? 12 : 0)))
-                     : (uint64_t)((float)out.total * near);
+      err = shift_ok ? (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 1, 7 + row.per / kSaU + (filtered ? 12 : 5)))
+                     : (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 2, filtered ? 0 : row.per * Row<E>::kVec + 5));
     }
     const int open = kOpen - (64 - __clzll((long long)out.total) - weight.s);
     bool done = false;
@@ -710,7 +731,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
         auto offer = [&](float x, int id) {
           if (rank_value(x) >= skip && x != neg_inf()) {
             const uint32_t at = atomicAdd(&sh.listed, 1u);
-            if (at < (uint32_t)kList) work.list[at] = rank_key(x, (uint32_t)id);
+            if (at < (uint32_t)SampleWork<TH>::kListed) work.list[at] = rank_key(x, (uint32_t)id);
           }
         };
         // the runs that have any, read by all threads together
@@ -734,7 +755,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
           row.back(offer);
         }
         __syncthreads();
-        few &= sh.listed <= (uint32_t)kList;
+        few &= sh.listed <= (uint32_t)SampleWork<TH>::kListed && (sh.listed <= (uint32_t)kList || (by_count && fl.top_k <= kList));
       }
       if (few) {
         int n = (int)sh.listed;
@@ -775,7 +796,7 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
         }
         out.kept = work.weight[n - 1];
         const uint64_t target = part_of<false>(out.kept, fl.u);
-        if (n <= 256 && n <= TH) {  // each by the weight of the lower ids
+        if (n <= 128) {  // each by the weight of the lower ids
           if ((int)threadIdx.x < ((n + 31) & ~31)) {
             const int j = threadIdx.x;
             const uint32_t mine = j < n ? (uint32_t)work.list[j] : 0;  // larger for lower ids
@@ -791,41 +812,44 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
             }
           }
           __syncthreads();
-        } else {  // sorted by id
-          constexpr int PER = kList / TH;
-          uint64_t mine[PER], w[PER];
-          uint32_t value[PER];
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int j = threadIdx.x + i * TH;
-            mine[i] = j < n ? work.list[j] : 0;
-            w[i] = j < n ? work.weight[j] - (j ? work.weight[j - 1] : 0) : 0;
-            value[i] = (uint32_t)(mine[i] >> 32);
+        } else {  // by the weights of 1024 ranges of ids, then within one
+          const int shift = max(0, 32 - __clz(a.V - 1) - 10);
+          for (int b = threadIdx.x; b < kSaNear; b += TH) work.lo[b] = work.hi[b] = 0;
+          if (threadIdx.x == 0) sh.listed = 0;
+          __syncthreads();
+          auto weight_of = [&](int j) { return work.weight[j] - (j ? work.weight[j - 1] : 0); };
+          for (int j = threadIdx.x; j < n; j += TH) {
+            const int b = rank_id(work.list[j]) >> shift;
+            add64(&work.lo[b], &work.hi[b], weight_of(j));
           }
           __syncthreads();
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int j = threadIdx.x + i * TH;
-            if (j < n) work.list[j] = mine[i] << 32 | (uint32_t)j, work.weight[j] = w[i], work.lo[j] = value[i];
-          }
-          __syncthreads();
-          sort_list<TH>(work.list, n);
+          constexpr int PER = kSaNear / TH;
           uint64_t own = 0, all;
+          auto bin = [&](int i) {
+            const int b = threadIdx.x * PER + i;
+            return (uint64_t)work.hi[b] << 32 | work.lo[b];
+          };
 #pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int j = threadIdx.x * PER + i;
-            w[i] = j < n ? work.weight[(uint32_t)work.list[j]] : 0;
-            own += w[i];
-          }
+          for (int i = 0; i < PER; ++i) own += bin(i);
           uint64_t before = block_scan<TH>(own, all, sh, turn);
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int j = threadIdx.x * PER + i;
-            if (before <= target && target < before + w[i]) {
-              sh.id = rank_id(work.list[j] >> 32);
-              sh.x = rank_logit((uint64_t)work.lo[(uint32_t)work.list[j]] << 32);
-            }
-            before += w[i];
+          if (before <= target && target < before + own) {
+            int i = 0;
+            while (before + bin(i) <= target) before += bin(i++);
+            sh.bin = threadIdx.x * PER + i, sh.left = before;
+          }
+          __syncthreads();
+          for (int j = threadIdx.x; j < n; j += TH)
+            if (rank_id(work.list[j]) >> shift == sh.bin)
+              work.group[atomicAdd(&sh.listed, 1u)] = work.list[j] << 32 | (uint32_t)j;  // larger for lower ids
+          __syncthreads();
+          const int in = (int)sh.listed;
+          for (int i = threadIdx.x; i < in; i += TH) {
+            const uint64_t mine = work.group[i];
+            uint64_t b = sh.left;
+            for (int k = 0; k < in; ++k)
+              if (work.group[k] > mine) b += weight_of((int)(uint32_t)work.group[k]);
+            const int j = (int)(uint32_t)mine;
+            if (b <= target && target < b + weight_of(j)) sh.id = rank_id(work.list[j]), sh.x = rank_logit(work.list[j]);
           }
           __syncthreads();
         }
@@ -842,9 +866,9 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
 }
 
 // ---- rows that are left open: a team of blocks per row, a part of it each, and
-// weights to 2^-34.  The team is a cluster of eight blocks, or, where a cluster
-// has several rows, one block: eight are sooner done with one row, but wait for
-// one another. ----
+// weights to 2^-34.  The team is a cluster of eight blocks, or, where there are many
+// open rows, one block: eight are sooner done with one row, but wait for one
+// another.  The sums are whole numbers, so the results are the same. ----
 constexpr int kTeam = 8, kTeamLog = 3;
 constexpr int kTeamThreads = 512, kTeamWarps = kTeamThreads / 32;
 constexpr int kTeamList = 2048;
@@ -852,8 +876,7 @@ constexpr int kTeamBins = 4096;
 constexpr int kTeamGroups = 1024;  // of 32 vectors: (2^20 / 4 / 8) / 32
 using TeamShared = SampleShared<kTeamThreads>;
 constexpr int kTeamU = 4;          // vectors read together
-constexpr int kTeamRows = 8;       // rows that are listed before they are worked on
-constexpr int kTeamAlone = 3;      // from this many on, each block takes one alone
+constexpr int kClaimed = -(1 << 30);  // in tokens: an open row that a block works on
 
 struct TeamWork {
   uint64_t power[1024];             // 2^(j/1024) 2^62
@@ -867,8 +890,9 @@ struct TeamWork {
   uint64_t ties[kTeamGroups + 2];
   uint32_t lo[kTeamBins], hi[kTeamBins];
   uint64_t box[2][2];               // what the blocks tell one another, in turn
-  int64_t row[kTeamRows];           // open rows, and their flags
-  int flag[kTeamRows];
+  int64_t row, claimed;             // a row that a block takes
+  uint32_t claim;
+  int flag, first;
   uint64_t base, key, incl;
   int edge;
 };
@@ -1616,54 +1640,94 @@ __device__ __forceinline__ uint64_t Team<E>::Exact::operator()(float x) const {
   return (p0 - kMinExponent) + e >= 0.0f ? w : 0;
 }
 
+__device__ __forceinline__ bool is_open(int token) { return token <= kOpen && token > kClaimed; }
+
+// The next open row from place `seen` on of the rows taken in turn from `start`
+// on, or -1; taken by marking its token, so that no other block has it.
+__device__ __noinline__ int64_t claim(const SampleArgs& a, int64_t start, int64_t& seen, int& flag, TeamWork& work) {
+  while (seen < a.T) {
+    const int64_t place = seen + threadIdx.x;
+    int64_t t = place + start;
+    if (t >= a.T) t -= a.T;
+    const int token = place < a.T ? __ldcg(&a.tokens[t]) : 0;
+    if (threadIdx.x == 0) work.first = kTeamThreads;
+    if (!__syncthreads_or(is_open(token))) {
+      seen += kTeamThreads;
+      continue;
+    }
+    if (is_open(token)) atomicMin(&work.first, (int)threadIdx.x);
+    __syncthreads();
+    if ((int)threadIdx.x == work.first) {
+      work.claimed = atomicCAS(&a.tokens[t], token, kClaimed) == token ? t : -1;
+      work.flag = token;
+    }
+    __syncthreads();
+    const int64_t got = work.claimed;
+    flag = work.flag;
+    __syncthreads();
+    if (got >= 0) return got;
+  }
+  return -1;
+}
+
 template <typename E>
 __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs a) {
   extern __shared__ uint4 smem[];
   TeamWork& work = *reinterpret_cast<TeamWork*>(smem);
   TeamShared& sh = *reinterpret_cast<TeamShared*>(&work + 1);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = (int)blockIdx.x % kTeam;
-  const int64_t teams = gridDim.x / kTeam;
-  // alone with a row only where its groups have room
-  const bool alone_fits = a.V / Row<E>::kVec <= kTeamGroups * 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank_in_cluster = (int)blockIdx.x % kTeam;
+  const int64_t teams = gridDim.x / kTeam, cluster = blockIdx.x / kTeam;
   bool ready = false;
   int turn = 0, scan_turn = 0;
   begin_kernel();
-  int64_t next = blockIdx.x / kTeam;
-  while (next < a.T) {
-    // the next open rows of this cluster, the same for its blocks: none is closed
-    // before all blocks have listed it
-    int rows = 0;
-    while (next < a.T && rows < kTeamRows) {
-      const int64_t mine = next + lane * teams;
-      const int flag = mine < a.T ? a.tokens[mine] : 0;
-      uint32_t open = __ballot_sync(0xFFFFFFFFu, flag <= kOpen);
-      int step = 32;
-      for (; open; open &= open - 1) {
-        const int who = __ffs(open) - 1;
-        if (rows == kTeamRows) {
-          step = who;  // from here on the next time
-          break;
-        }
-        if (threadIdx.x == (unsigned)who) work.row[rows] = mine, work.flag[rows] = flag;
-        ++rows;
-      }
-      next += step * teams;
+  // Alone where there are more open rows than two per team, and where a block's
+  // groups have room for a row.  The count may be short of rows that others have
+  // taken; any mode is right.
+  int64_t from = 0;
+  int rows = 0;
+  if (rank_in_cluster == 0)
+    for (; from < a.T && rows <= 2 * teams; from += kTeamThreads) {
+      const int64_t t = from + threadIdx.x;
+      rows += __syncthreads_count(t < a.T && is_open(__ldcg(&a.tokens[t])));
     }
-    if (rows == 0) break;
+  if (threadIdx.x == 0) work.claim = rows;
+  cluster_arrive();
+  cluster_wait();
+  rows = (int)cluster_load(&work.claim, 0);
+  cluster_arrive();
+  cluster_wait();
+  if (rows == 0) return;
+  const bool alone = rows > 2 * teams && a.V / Row<E>::kVec <= kTeamGroups * 32;
+  const int size = alone ? 1 : kTeam, rank = alone ? 0 : rank_in_cluster, lg = alone ? 0 : kTeamLog;
+  // The search for a row begins at a place of the block's or cluster's own.
+  const int64_t start = a.T * (alone ? (int64_t)blockIdx.x : cluster * kTeam) / gridDim.x;
+  int64_t seen = 0;
+  for (;;) {
+    int64_t t = -1;
+    int flag = 0;
+    if (rank == 0) t = claim(a, start, seen, flag, work);
+    if (!alone) {  // the first block tells the others
+      if (threadIdx.x == 0) work.row = t, work.claim = (uint32_t)flag;
+      cluster_arrive();
+      cluster_wait();
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(&work.row);
+      t = (int64_t)(cluster_load(p, 0) | (uint64_t)cluster_load(p + 1, 0) << 32);
+      flag = (int)cluster_load(&work.claim, 0);
+      cluster_arrive();
+      cluster_wait();
+    }
+    if (t < 0) break;
     if (!ready) {
       load_exp2(sh);
       __syncthreads();
       Weights one;  // 2^(j / 1024 - 1), of unit 2^-61
       one.m = 1024.0f, one.ch = 0x1p-10f, one.cl = 0.0f, one.s = 61, one.exp2 = sh.exp2;
       for (int j = threadIdx.x; j < 1024; j += kTeamThreads) work.power[j] = one.exact((float)j) << 2;
+      __syncthreads();
       ready = true;
     }
-    cluster_arrive();
-    cluster_wait();
-    const int size = rows >= kTeamAlone && alone_fits ? 1 : kTeam, rank = size == 1 ? 0 : me, lg = size == 1 ? 0 : kTeamLog;
-    for (int at = size == 1 ? me : 0; at < rows; at += size == 1 ? kTeam : 1) {
-      const int64_t t = work.row[at];
-      const int log_s = kOpen - work.flag[at];
+    {
+      const int log_s = kOpen - flag;
       const E* logits = static_cast<const E*>(a.logits) + t * a.ld;
       const Row<E> whole(logits, a.V);
       const int v0 = whole.part(rank, lg), v1 = whole.part(rank + 1, lg);
@@ -1694,9 +1758,6 @@ __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs
       scan_turn = team.scan_turn;
       turn = team.turn;
     }
-    turn = 0;
-    cluster_arrive();  // no block goes on, or ends, while another reads its shared memory
-    cluster_wait();
   }
 }
 
