@@ -65,11 +65,13 @@ int launch_embed_tokens(const EmbedArgs& a, cudaStream_t s) {
 }
 
 // ---- gradient ----
-// The tokens are sorted by id (stable, so ascending t within an id) with a
-// radix sort of up to 9 bits a pass; tiles of the sorted tokens are then summed
-// run by run.  A run inside one tile goes to the table at once; the parts of a
-// run that crosses tiles go to the workspace and are added in the order of the
+// Up to kFewTokens tokens: one launch, in which each token's first occurrence sums
+// all of them.  More: the tokens are sorted by id (stable, so ascending t within an
+// id) with a radix sort of up to 9 bits a pass; tiles of the sorted tokens are then
+// summed run by run.  A run inside one tile goes to the table at once; the parts of
+// a run that crosses tiles go to the workspace and are added in the order of the
 // tiles by a last launch.  Ids out of range sort behind all others, as V.
+constexpr int kFewTokens = 1024;
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBits = 9, kBins = 1 << kMaxBits;
@@ -83,13 +85,14 @@ struct SortPlan {
 };
 
 static SortPlan sort_plan(int T, int V, int d) {
-  SortPlan p;
+  SortPlan p = {};
+  if (T <= kFewTokens) return p;
   int n = 1;
   while ((int64_t(1) << n) <= V) ++n;  // ids up to V
   p.passes = (n + kMaxBits - 1) / kMaxBits;
   p.bits = (n + p.passes - 1) / p.passes;
   p.items = 1;
-  while (p.items < 32 && (int64_t)p.items * kSortThreads * 128 < T) p.items *= 2;
+  while (p.items < 32 && (int64_t)p.items * kSortThreads * 64 < T) p.items *= 2;
   const int chunk = p.items * kSortThreads;
   p.blocks = (T + chunk - 1) / chunk;
   p.tile = 4;
@@ -109,7 +112,10 @@ static SortPlan sort_plan(int T, int V, int d) {
   p.bytes = at;
   return p;
 }
-size_t embed_tokens_backward_ws(int T, int V, int d) { return sort_plan(T, V, d).bytes; }
+size_t embed_tokens_backward_ws(int T, int V, int d) {
+  const size_t n = sort_plan(T, V, d).bytes;
+  return n ? n : 8 * (size_t)kFewTokens;  // not used
+}
 
 __device__ __forceinline__ int sort_key(int id, int V) { return (unsigned)id < (unsigned)V ? id : V; }
 
@@ -157,6 +163,7 @@ __global__ void __launch_bounds__(kSortThreads)
   begin_kernel();
   // tokens of smaller digits, and of this digit in earlier chunks
   uint32_t before = 0, total = 0;
+#pragma unroll 16
   for (int b = 0; b < (int)gridDim.x; ++b) {
     const uint32_t c = hist[(int64_t)b * kBins + k];
     before += b < (int)blockIdx.x ? c : 0;
@@ -205,12 +212,43 @@ __global__ void __launch_bounds__(kSortThreads)
       key_out[at] = key;
       val_out[at] = val;
       if (next_hist) atomicAdd(&next_hist[(int64_t)(at / chunk) * kBins + ((key >> (shift + bits)) & mask)], 1u);
-      if (!key_in && key < V) atomicOr(&bitmap[key >> 5], 1u << (key & 31));
+    }
+    if (!key_in) {  // one atomic per word of the bit map and warp: frequent ids are many
+      const bool named = key >= 0 && key < V;
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, named ? key >> 5 : -1);
+      const uint32_t bits = __reduce_or_sync(peers, named ? 1u << (key & 31) : 0u);
+      if (named && lane == __ffs(peers) - 1) atomicOr(&bitmap[key >> 5], bits);
     }
     __syncwarp();
     if (key >= 0 && lane == __ffs(same) - 1) place[warp][digit] += __popc(same);
     __syncwarp();
   }
+}
+
+// Eight values, as one store where the address allows it.
+__device__ __forceinline__ void store8(float* p, const float4& lo, const float4& hi) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.cs.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(lo.x), "f"(lo.y), "f"(lo.z),
+                 "f"(lo.w), "f"(hi.x), "f"(hi.y), "f"(hi.z), "f"(hi.w)
+                 : "memory");
+  } else {
+    __stcs(reinterpret_cast<float4*>(p), lo);
+    __stcs(reinterpret_cast<float4*>(p) + 1, hi);
+  }
+}
+__device__ __forceinline__ void put8(float* p, const float (&x)[8], float scale, bool add) {
+  float4 lo = make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale);
+  float4 hi = make_float4(x[4] * scale, x[5] * scale, x[6] * scale, x[7] * scale);
+  if (add) {
+    const float4 a = reinterpret_cast<float4*>(p)[0], b = reinterpret_cast<float4*>(p)[1];
+    lo.x += a.x, lo.y += a.y, lo.z += a.z, lo.w += a.w;
+    hi.x += b.x, hi.y += b.y, hi.z += b.z, hi.w += b.w;
+  }
+  store8(p, lo, hi);
+}
+__device__ __forceinline__ void zero8(float* p) {
+  const float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  store8(p, z, z);
 }
 
 struct SumArgs {
@@ -219,21 +257,8 @@ struct SumArgs {
   const int32_t* val;
   const uint32_t* bitmap;
   float* part;
-  int tile, tiles, sum_blocks, zero_rows;
+  int tile, tiles, sum_blocks;
 };
-
-__device__ __forceinline__ void put8(float* p, const float (&x)[8], float scale, bool add) {
-  float4 lo = make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale);
-  float4 hi = make_float4(x[4] * scale, x[5] * scale, x[6] * scale, x[7] * scale);
-  float4* q = reinterpret_cast<float4*>(p);
-  if (add) {
-    const float4 a = q[0], b = q[1];
-    lo.x += a.x, lo.y += a.y, lo.z += a.z, lo.w += a.w;
-    hi.x += b.x, hi.y += b.y, hi.z += b.z, hi.w += b.w;
-  }
-  __stcs(q, lo);
-  __stcs(q + 1, hi);
-}
 
 // Blocks 0 .. sum_blocks - 1: 256 / TX tiles of sorted tokens each.  The rest:
 // zeros into the rows of the table that no token names.
@@ -244,13 +269,12 @@ __global__ void __launch_bounds__(kEmThreads) embed_sum_kernel(SumArgs s, int tx
   begin_kernel();
   if (c >= a.d) return;
   if ((int)blockIdx.x >= s.sum_blocks) {
-    const int v0 = ((int)blockIdx.x - s.sum_blocks) * s.zero_rows, v1 = min(a.V, v0 + s.zero_rows);
-    for (int v = v0 + ty; v < v1; v += rows)
-      if (!(s.bitmap[v >> 5] >> (v & 31) & 1)) {
-        float4* q = reinterpret_cast<float4*>(a.dtable + (int64_t)v * a.d + c);
-        __stcs(q, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-        __stcs(q + 1, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-      }
+    // 32 rows, a word of the bit map, per group of threads
+    const int v0 = (((int)blockIdx.x - s.sum_blocks) * rows + ty) * 32, n = min(a.V - v0, 32);
+    if (n <= 0) return;
+    const uint32_t named = s.bitmap[v0 >> 5];
+    for (int i = 0; i < n; ++i)
+      if (!(named >> i & 1)) zero8(a.dtable + (int64_t)(v0 + i) * a.d + c);
     return;
   }
   const int64_t tile = (int64_t)blockIdx.x * rows + ty;
@@ -295,31 +319,183 @@ __global__ void __launch_bounds__(kEmThreads) embed_sum_kernel(SumArgs s, int tx
 }
 
 // The parts of each run that begins in a tile and ends in a later one, added in
-// the order of the tiles.
-__global__ void __launch_bounds__(kEmThreads) embed_join_kernel(SumArgs s, int tx_log) {
+// the order of the tiles, for 128 columns: a warp per tile; a frequent token's run,
+// which crosses a hundred tiles, by the block's eight warps, a consecutive eighth
+// each, and the eighths in turn.
+constexpr int kJoinWarps = kEmThreads / 32;
+__global__ void __launch_bounds__(kEmThreads) embed_join_kernel(SumArgs s) {
+  __shared__ int64_t length[kJoinWarps];
+  __shared__ float4 sums[kJoinWarps][32];
   const EmbedBwdArgs& a = s.a;
-  const int tx = 1 << tx_log, rows = kEmThreads >> tx_log;
-  const int c = (blockIdx.y * tx + (threadIdx.x & (tx - 1))) * 8;
-  const int64_t tile = (int64_t)blockIdx.x * rows + (threadIdx.x >> tx_log);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.y * 128 + lane * 4;
+  const int64_t first = (int64_t)blockIdx.x * kJoinWarps, tile = first + warp;
   begin_kernel();
-  if (c >= a.d || tile + 1 >= s.tiles) return;
-  const int64_t p0 = tile * s.tile, p1 = p0 + s.tile;
-  const int id = s.key[p1 - 1];
-  if (id >= a.V || s.key[p1] != id) return;                        // no run goes on into the next tile
-  if (s.key[p0] == id && p0 > 0 && s.key[p0 - 1] == id) return;    // it began in an earlier one
-  float acc[8];
-  const float* own = s.part + (tile * 2 + 1) * a.d + c;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = own[e];
-  for (int64_t j = tile + 1; j < s.tiles && s.key[j * s.tile] == id; ++j) {
-    const float* p = s.part + j * 2 * a.d + c;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] += p[e];
+  const bool in = c < a.d;
+  // the tiles after this one that the run goes on in, if it begins here
+  int64_t n = 0;
+  int id = -1;
+  if (tile + 1 < s.tiles) {
+    const int64_t p0 = tile * s.tile, p1 = p0 + s.tile;
+    id = s.key[p1 - 1];
+    if (id < a.V && s.key[p1] == id && !(s.key[p0] == id && p0 > 0 && s.key[p0 - 1] == id))
+      for (;;) {
+        const int64_t next = tile + 1 + n + lane;
+        const uint32_t others = __ballot_sync(0xFFFFFFFFu, next >= s.tiles || s.key[next * s.tile] != id);
+        n += others ? __ffs(others) - 1 : 32;
+        if (others) break;
+      }
   }
-  put8(a.dtable + (int64_t)id * a.d + c, acc, a.scale, a.accumulate);
+  // the sum of parts [j0, j1) of the run that begins in tile t
+  auto sum = [&](int64_t t, int64_t j0, int64_t j1) {
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int64_t j = j0; j < j1; j += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t slot = j + i == 0 ? t * 2 + 1 : (t + j + i) * 2;
+        v[i] = in && j + i < j1 ? *reinterpret_cast<const float4*>(s.part + slot * a.d + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j + i < j1) acc.x += v[i].x, acc.y += v[i].y, acc.z += v[i].z, acc.w += v[i].w;
+    }
+    return acc;
+  };
+  auto put = [&](float4 acc, int id) {
+    if (!in) return;
+    float4* out = reinterpret_cast<float4*>(a.dtable + (int64_t)id * a.d + c);
+    acc.x *= a.scale, acc.y *= a.scale, acc.z *= a.scale, acc.w *= a.scale;
+    if (a.accumulate) {
+      const float4 o = *out;
+      acc.x += o.x, acc.y += o.y, acc.z += o.z, acc.w += o.w;
+    }
+    __stcs(out, acc);
+  };
+  constexpr int kAlone = 16;
+  if (n > 0 && n < kAlone) put(sum(tile, 0, n + 1), id);
+  if (lane == 0) length[warp] = n;
+  __syncthreads();
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const int64_t m = length[w] + 1;
+    if (m <= kAlone) continue;
+    const int64_t t = first + w;
+    sums[warp][lane] = sum(t, m * warp / kJoinWarps, m * (warp + 1) / kJoinWarps);
+    __syncthreads();
+    if (warp == 0) {
+      float4 acc = sums[0][lane];
+      for (int i = 1; i < kJoinWarps; ++i) {
+        const float4 v = sums[i][lane];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+      }
+      put(acc, s.key[(t + 1) * s.tile]);
+    }
+    __syncthreads();
+  }
+}
+
+// Few tokens.  Blocks 0 .. T * parts - 1: a token and 256 columns; the block of
+// the id's first occurrence lists all of them in order, its eight warps sum a
+// consecutive eighth each, and the eighths are added in turn.  The rest: zeros
+// into the rows that no token names, `zero_rows` of them per block.
+__global__ void __launch_bounds__(kEmThreads) embed_few_kernel(EmbedBwdArgs a, int parts, int zero_rows) {
+  constexpr int kIds = kFewTokens / kEmThreads, kZeroWords = 8;
+  __shared__ int list[kFewTokens];
+  __shared__ int counts[kEmThreads / 32];
+  __shared__ float sums[kEmThreads / 32][256];
+  __shared__ uint32_t named[kZeroWords];
+  const int k = threadIdx.x, lane = k & 31, warp = k >> 5;
+  if (k < kZeroWords) named[k] = 0;
+  begin_kernel();
+  __syncthreads();
+  const int64_t zero = (int64_t)blockIdx.x - (int64_t)a.T * parts;
+  if (zero >= 0) {
+    const int v0 = (int)zero * zero_rows, n = min(a.V - v0, zero_rows);  // at most 32 kZeroWords rows
+    for (int t = k; t < a.T; t += kEmThreads) {
+      const uint32_t at = (uint32_t)(a.ids[t] - v0);
+      if (a.ids[t] >= v0 && at < (uint32_t)n) atomicOr(&named[at >> 5], 1u << (at & 31));
+    }
+    __syncthreads();
+    const int vecs = a.d / 8;
+    for (int i = k; i < n * vecs; i += kEmThreads) {
+      const int v = i / vecs;
+      if (!(named[v >> 5] >> (v & 31) & 1)) zero8(a.dtable + (int64_t)(v0 + v) * a.d + (i - v * vecs) * 8);
+    }
+    return;
+  }
+  const int t = (int)blockIdx.x / parts, c = ((int)blockIdx.x % parts) * 256 + lane * 8;
+  // this thread's consecutive tokens
+  int mine[kIds], n = 0;
+  bool earlier = false;
+  const int id = a.ids[t];
+#pragma unroll
+  for (int i = 0; i < kIds; ++i) {
+    const int j = k * kIds + i;
+    mine[i] = j < a.T && a.ids[j] == id;
+    earlier |= mine[i] && j < t;
+    n += mine[i];
+  }
+  if (id >= a.V && k == 0 && c == 0) set_status(a.status, MOE_STATUS_BAD_TOKEN);
+  if (__syncthreads_or(earlier) || id < 0 || id >= a.V) return;
+  int at = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, at, o);
+    if (lane >= o) at += v;
+  }
+  if (lane == 31) counts[warp] = at;
+  __syncthreads();
+  at -= n;
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kEmThreads / 32; ++w) {
+    if (w < warp) at += counts[w];
+    total += counts[w];
+  }
+#pragma unroll
+  for (int i = 0; i < kIds; ++i)
+    if (mine[i]) list[at++] = k * kIds + i;
+  __syncthreads();
+  // one warp is enough for a few
+  const int warps = total <= 8 ? 1 : kEmThreads / 32, p0 = total * warp / warps, p1 = warp < warps ? total * (warp + 1) / warps : p0;
+  if (warp >= warps) return;
+  float acc[8] = {};
+  if (c < a.d)
+    for (int p = p0; p < p1; p += 8) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = p + i < p1 ? __ldcs(reinterpret_cast<const uint4*>(a.dy + (int64_t)list[p + i] * a.ldy + c)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float x[8];
+        unpack(v[i], x);
+        if (p + i < p1) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] += x[e];
+        }
+      }
+    }
+  if (warps > 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[warp][lane * 8 + e] = acc[e];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 1; w < kEmThreads / 32; ++w)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += sums[w][lane * 8 + e];
+  }
+  if (c < a.d) put8(a.dtable + (int64_t)id * a.d + c, acc, a.scale, a.accumulate);
 }
 
 int launch_embed_tokens_backward(const EmbedBwdArgs& a, cudaStream_t s) {
+  if (a.T <= kFewTokens) {
+    const int parts = (a.d + 255) / 256;
+    // zeros: some 32 KB per block, and 256 rows at most
+    const int rows = a.d >= 8192 ? 1 : 8192 / a.d > 256 ? 256 : 8192 / a.d;
+    const unsigned zero = a.accumulate ? 0u : ((unsigned)a.V + rows - 1) / rows;
+    return launch_kernel(embed_few_kernel, (unsigned)(a.T * parts) + zero, kEmThreads, 0, 1, s, a, parts, rows);
+  }
   const SortPlan p = sort_plan(a.T, a.V, a.d);
   auto ints = [&](size_t o) { return reinterpret_cast<int32_t*>(a.ws + o); };
   auto words = [&](size_t o) { return reinterpret_cast<uint32_t*>(a.ws + o); };
@@ -335,12 +511,13 @@ int launch_embed_tokens_backward(const EmbedBwdArgs& a, cudaStream_t s) {
   if (rc != 0) return rc;
   const int last = (p.passes - 1) & 1, l = threads_along(a.d / 8), rows = kEmThreads >> l;
   SumArgs m = {a, ints(p.key[last]), ints(p.val[last]), words(p.bitmap), reinterpret_cast<float*>(a.ws + p.part),
-               p.tile, p.tiles, (p.tiles + rows - 1) / rows, 32 * rows};
+               p.tile, p.tiles, (p.tiles + rows - 1) / rows};
   const unsigned cols = (unsigned)((a.d / 8 + (1 << l) - 1) >> l);
-  const unsigned zero = a.accumulate ? 0u : (unsigned)((a.V + (int64_t)m.zero_rows - 1) / m.zero_rows);
+  const unsigned zero = a.accumulate ? 0u : (unsigned)((a.V + 32ll * rows - 1) / (32 * rows));
   rc = launch_kernel(embed_sum_kernel, dim3((unsigned)m.sum_blocks + zero, cols), kEmThreads, 0, 1, s, m, l);
   if (rc != 0) return rc;
-  return launch_kernel(embed_join_kernel, dim3((unsigned)m.sum_blocks, cols), kEmThreads, 0, 1, s, m, l);
+  return launch_kernel(embed_join_kernel, dim3((unsigned)(p.tiles + kJoinWarps - 1) / kJoinWarps, (unsigned)(a.d + 127) / 128),
+                       kEmThreads, 0, 1, s, m);
 }
 
 }  // namespace moe
