@@ -97,7 +97,7 @@ static SortPlan sort_plan(int T, int V, int d) {
   p.blocks = (T + chunk - 1) / chunk;
   p.tile = 4;
   const int64_t cols = (d / 8 + 255) / 256;
-  while (p.tile < 32 && T / p.tile * cols > 2048) p.tile *= 2;
+  while (p.tile < 64 && T / p.tile * cols > 1024) p.tile *= 2;
   p.tiles = (T + p.tile - 1) / p.tile;
   size_t at = 0;
   auto take = [&](size_t n) {
