@@ -865,6 +865,13 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
   }
 }
 
+// 4 bytes to shared address p of block `rank` of the cluster.
+__device__ __forceinline__ void cluster_store(const void* p, uint32_t rank, uint32_t v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 // ---- rows that are left open: a team of blocks per row, a part of it each, and
 // weights to 2^-34.  The team is a cluster of eight blocks, or, where there are many
 // open rows, one block: eight are sooner done with one row, but wait for one
@@ -981,6 +988,27 @@ struct Team {
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     each(f, [](int) {}, [](const auto&, int, int) {});
+  }
+  // The largest of this thread's elements.
+  __device__ __forceinline__ float high() const {
+    float m = neg_inf();
+    if constexpr (sizeof(E) == 4) {
+      each([&](float x, int) { m = fmaxf(m, x); });
+    } else {
+      uint32_t w = 0xFF80FF80u;
+      for (int i0 = threadIdx.x; i0 < r.nvec; i0 += kTeamU * kTeamThreads) {
+        uint4 v[kTeamU];
+#pragma unroll
+        for (int u = 0; u < kTeamU; ++u) v[u] = r.vec()[min(i0 + u * kTeamThreads, r.nvec - 1)];
+#pragma unroll
+        for (int u = 0; u < kTeamU; ++u)
+          w = max_nan_bf16x2(w, max_nan_bf16x2(max_nan_bf16x2(v[u].x, v[u].y), max_nan_bf16x2(v[u].z, v[u].w)));
+      }
+      m = fmaxf(bf16_lo(w), bf16_hi(w));
+      if ((int)threadIdx.x < r.head) m = fmaxf(m, to_f32(r.p[threadIdx.x]));
+      if ((int)threadIdx.x < r.tail) m = fmaxf(m, to_f32(r.p[r.tail_start() + threadIdx.x]));
+    }
+    return m;
   }
   // f's sums into the groups
   template <typename F, typename H>
@@ -1357,8 +1385,10 @@ struct Team {
   // powers of two) below that, and a bin for the rest.
   static constexpr int kMid = kTeamNear, kLast = kTeamBins - 1;
   struct Bins {
-    uint32_t top;  // rank of the maximum, in both halves
-    int below;     // distance of a value below -2^-10, less its bin
+    uint32_t top;      // rank of the maximum, in both halves
+    int below;         // distance of a value below -2^-10, less its bin; 0 under a
+                       // negative maximum, where the bins go on to kLast
+    uint32_t low, off; // below + kMid and below, in both halves
     __device__ __forceinline__ static uint32_t rank(uint32_t pair) {
       uint32_t sign;
       asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(sign) : "r"(pair));  // each half its sign bit
@@ -1367,18 +1397,23 @@ struct Team {
     __device__ __forceinline__ Bins(float m) {
       const uint32_t t = rank_value(m) >> 16;  // of 0, not -0
       top = t << 16 | t;
-      below = (int)t - 0x457F - kMid;  // -2^-10 has rank 0x457F and lies in bin kMid
+      below = max(0, (int)t - 0x457F - kMid);  // -2^-10 has rank 0x457F and lies in bin kMid
+      low = (uint32_t)(below + kMid) * 0x10001u, off = (uint32_t)below * 0x10001u;
     }
-    __device__ __forceinline__ int at(uint32_t d) const {
-      return d < (uint32_t)kTeamNear ? (int)d : max(kMid, min((int)d - below, kLast));
+    // Of a pair of values: the bins of the first part up to kMid, and of the second
+    // from kMid on.
+    __device__ __forceinline__ uint32_t pair(uint32_t values) const {
+      const uint32_t d = top - rank(values);  // no half borrows: the maximum is at the top
+      return __vminu2(d, kMid * 0x10001u) + __vminu2(__vmaxu2(d, low) - off, kLast * 0x10001u) - kMid * 0x10001u;
     }
     __device__ __forceinline__ int of(float x) const {
-      const uint32_t r = rank(__float_as_uint(x) >> 16) & 0xFFFFu, t = top & 0xFFFFu;
-      return at(t > r ? t - r : 0u);
+      const uint32_t v = __float_as_uint(x) >> 16;
+      const uint32_t t = top & 0xFFFFu, r = rank(v) & 0xFFFFu;
+      return t < r ? 0 : (int)(pair(v | v << 16) & 0xFFFFu);  // -0 under 0 is above it in rank
     }
     // The value of a bin that has one.
     __device__ __forceinline__ float value(int b) const {
-      const int r = (int)(top & 0xFFFFu) - (b < kTeamNear ? b : b + below);
+      const int r = (int)(top & 0xFFFFu) - (b < kMid ? b : b + below);
       if (r <= 0x7F) return neg_inf();  // none
       const uint32_t bits = r & 0x8000 ? (uint32_t)r ^ 0x8000u : ~(uint32_t)r & 0xFFFFu;
       return __uint_as_float(bits << 16);
@@ -1411,8 +1446,8 @@ struct Team {
           bool any = false;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t d = bins.top - Bins::rank(w[k]);  // of both halves: none borrows, the maximum is at the top
-            const int a = bins.at(d & 0xFFFFu), b = bins.at(d >> 16);
+            const uint32_t pair = bins.pair(w[k]);
+            const int a = (int)(pair & 0xFFFFu), b = (int)(pair >> 16);
             f(a);
             f(b);
             any |= a == kMid || a == kLast || b == kMid || b == kLast;
@@ -1464,9 +1499,9 @@ struct Team {
     const Exact exact = exact_weights();
     const Bins bins(weight.m);
     // 0 and -0, which are equal, and -inf lie in bins of several values but below
-    // a maximum of less than 2^-111 or of the lowest values
+    // a maximum of less than 2^-95 or of the lowest values
     const uint32_t first_rank = bins.top & 0xFFFFu;
-    if (first_rank - 0x8000u < (uint32_t)kTeamNear || first_rank < 0x80u + kTeamNear) return false;
+    if (first_rank - 0x8000u < (uint32_t)kTeamBins || first_rank < 0x80u + kTeamBins) return false;
     uint64_t* table = work.table;
     for (int b = threadIdx.x; b < kTeamBins; b += kTeamThreads)
       table[b] = b == kMid || b == kLast ? 0 : exact(bins.value(b));
@@ -1679,6 +1714,8 @@ __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs
   const int64_t teams = gridDim.x / kTeam, cluster = blockIdx.x / kTeam;
   bool ready = false;
   int turn = 0, scan_turn = 0;
+  cluster_arrive();  // all blocks run: their shared memory may be written
+  cluster_wait();
   begin_kernel();
   // Alone where there are more open rows than two per team, and where a block's
   // groups have room for a row.  The count may be short of rows that others have
@@ -1690,12 +1727,10 @@ __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs
       const int64_t t = from + threadIdx.x;
       rows += __syncthreads_count(t < a.T && is_open(__ldcg(&a.tokens[t])));
     }
-  if (threadIdx.x == 0) work.claim = rows;
+  if (rank_in_cluster == 0 && threadIdx.x < kTeam) cluster_store(&work.claim, threadIdx.x, (uint32_t)rows);
   cluster_arrive();
   cluster_wait();
-  rows = (int)cluster_load(&work.claim, 0);
-  cluster_arrive();
-  cluster_wait();
+  rows = (int)work.claim;
   if (rows == 0) return;
   const bool alone = rows > 2 * teams && a.V / Row<E>::kVec <= kTeamGroups * 32;
   const int size = alone ? 1 : kTeam, rank = alone ? 0 : rank_in_cluster, lg = alone ? 0 : kTeamLog;
@@ -1738,8 +1773,7 @@ __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs
       bool params;
       const Filters fl = filters_of(a, t, params);
       // the row's maximum, a number
-      float high = neg_inf();
-      team.each([&](float x, int) { high = fmaxf(high, x); });
+      const float high = team.high();
       uint32_t top = __reduce_max_sync(0xFFFFFFFFu, rank_value(high));
       if (lane == 0) sh.scan[0][warp] = top;
       __syncthreads();
