@@ -525,9 +525,311 @@ __device__ __forceinline__ void put_drawn(const SampleArgs& a, int64_t t, const 
   if (a.kept_logprob) a.kept_logprob[t] = z - log1pf((float)((int64_t)d.kept - one) * unit);
 }
 
+// The end of a row, from its runs' maxima and sums: the token and its numbers
+// written, 0; or what marks the row as open.  own: this thread's maximum; highs,
+// sums: its runs', TH apart.
+template <typename E, int TH>
+__device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const SampleRow<E, TH>& row, const Filters& fl,
+                                       bool params, Weights weight, float own, const float* highs, const float* sums,
+                                       SampleShared<TH>& sh, SampleWork<TH>& work, int& turn) {
+  constexpr int NW = TH / 32, kList = SampleShared<TH>::kList;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float c = weight.ch;
+  float m = own;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if (lane == 0) sh.wmax[warp] = m;
+  __syncthreads();
+  m = lane < NW ? sh.wmax[lane] : neg_inf();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if (!params || !(m <= 3.402823466e+38f) || m == neg_inf()) {
+    if (threadIdx.x == 0) {
+      const bool none = params && m == neg_inf();
+      a.tokens[t] = -1;
+      if (a.logprob) a.logprob[t] = none ? neg_inf() : quiet_nan();
+      if (a.kept_logprob) a.kept_logprob[t] = none ? neg_inf() : quiet_nan();
+      if (!params) set_status(a.status, MOE_STATUS_BAD_SAMPLING);
+      if (!(m <= 3.402823466e+38f)) set_status(a.status, MOE_STATUS_NONFINITE_LOGITS);
+    }
+    __syncthreads();
+    return 0;
+  }
+  weight.m = m;
+  // the runs' sums from their own shifts to the maximum, of unit 2^-s
+  const float mc = __fmul_rn(m, c), M = fmaxf(ceilf(mc), -kShiftLimit), cl_ch = fabsf(weight.cl) / weight.ch;
+  const float to_m = exp2_fast((M - mc) - fmaf(m, c, -mc));
+  auto run_float = [&](int q) {  // at most 2^10
+    return sums[q * TH] * exp2_fast(RunSum::shift_of(highs[q * TH], c) - M) * to_m;
+  };
+  const bool shift_ok = fabsf(mc) <= kShiftLimit;
+  const bool filtered = fl.top_k > 0 || fl.top_p < 1.0f || fl.min_p > 0.0f;
+  uint64_t edge = 0;  // keys below have less than min_p
+  if (fl.min_p > 0.0f) edge = min_p_key(m, sh.edge);
+  Drawn out;
+  uint64_t sum = 0, err, weight_err;  // errors of sums of the pass, and of weights by themselves
+  const float unit = ldexpf(1.0f, -weight.s);
+  int e = 0;  // the part of the row with the token
+  if (filtered && !shift_ok) {  // the pass's weights are out of range
+    row.all(0, [&](float x, int) { sum += weight.fast(x); });
+    block_scan<TH>(sum, out.total, sh, turn);
+  } else if (filtered) {
+    float w = 0.0f;
+    for (int q = 0; q < row.runs; ++q) w += run_float(q);
+    sum = fixed(w, weight.s);
+    row.front([&](float x, int) { sum += weight.fast(x); });
+    row.back([&](float x, int) { sum += weight.fast(x); });
+    block_scan<TH>(sum, out.total, sh, turn);
+  }
+  if (!filtered) {
+    // the warp's sums of the eight runs: lane l ends with run l / 4's
+    float w[kSaRuns];
+#pragma unroll
+    for (int q = 0; q < kSaRuns; ++q) {
+      w[q] = 0.0f;
+      if (q < row.runs) {
+        if (shift_ok) w[q] = run_float(q);
+        else row.run(q, [&](float x, int) { w[q] += weight.ratio(x); });
+      }
+    }
+#pragma unroll
+    for (int h = 4, o = 16; h > 0; h /= 2, o /= 2)
+#pragma unroll
+      for (int q = 0; q < h; ++q) {
+        const float keep = lane & o ? w[q + h] : w[q], give = lane & o ? w[q] : w[q + h];
+        w[q] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+      }
+    w[0] += __shfl_xor_sync(0xFFFFFFFFu, w[0], 2);
+    w[0] += __shfl_xor_sync(0xFFFFFFFFu, w[0], 1);
+    if ((lane & 3) == 0 && lane / 4 < row.runs) sh.part[lane / 4 + 1][warp] = fixed(w[0], weight.s);
+    out.total = out.kept = pick<E, TH>(row, fl.u, [&](float x, int) { return weight.fast(x); }, [&](const uint4& v) {
+      constexpr int N = Row<E>::kVec;
+      float x[N];
+      unpack(v, x);
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[e] = weight.ratio(x[e]);
+#pragma unroll
+      for (int h = N / 2; h > 0; h /= 2)
+#pragma unroll
+        for (int e = 0; e < h; ++e) x[e] += x[e + h];
+      return fixed(x[0], weight.s);
+    }, sh, work.group, turn);
+    out.id = sh.id, out.x = sh.x;
+    uint64_t first;
+    e = find_part<E, TH>(row, sh.target, first, sh);
+  }
+  {
+    // in the pass 3 additions per sum of pairs, 3 to join them, one per batch of
+    // a run, a product with to_m; then 5 over the warp, or, with the filters, 8
+    // for the thread's runs, and to_m's own error, which is otherwise the same
+    // for all.  Weights by themselves: 3 in a vector, and with the range of the
+    // pass exceeded as many as a run has elements, and 5 over the warp.
+    const float S = (float)out.total * unit;
+    const float near = sum_error(S, a.V, cl_ch, 2, 3);
+    weight_err = (uint64_t)((float)(filtered ? out.total : sh.sums[e]) * (near + 0x1p-22f));
+    err = shift_ok ? (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 1, 7 + row.per / kSaU + (filtered ? 12 : 5)))
+                   : (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 2, filtered ? 0 : row.per * Row<E>::kVec + 5));
+  }
+  const int open = kOpen - (64 - __clzll((long long)out.total) - weight.s);
+  bool done = false;
+  if (!filtered) {
+    err += weight_err;  // of the run with the token
+    done = sh.id >= 0 && (sh.before == 0 || sh.target - sh.before > err) &&
+           (sh.after >= out.total || sh.after - sh.target > err);
+  } else {
+    // ---- a lower bound of what is kept, from the maxima ----
+    const uint32_t top = rank_value(m);
+    uint32_t skip = (uint32_t)(edge >> 32);
+    const bool by_count = fl.top_k > 0, by_mass = !by_count && fl.top_p < 1.0f;
+    if (by_count && fl.top_p < 1.0f) skip = 0;  // all of the top_k count for top_p
+    if (threadIdx.x == 0) sh.found = 0, sh.listed = 0, sh.hot = 0;
+    bool few = true;
+    if (by_count || by_mass) {
+      for (int b = threadIdx.x; b < kSaNear; b += TH) work.lo[b] = 0, work.hi[b] = 0;
+      __syncthreads();
+      auto offer = [&](float x, uint64_t w) {
+        const uint32_t d = top - rank_value(x);
+        if (d >= 1u << 27 || x == neg_inf()) return;
+        if (by_count) atomicAdd(&work.lo[d >> 17], 1u);
+        else add64(&work.lo[d >> 17], &work.hi[d >> 17], w);
+      };
+      if (by_count && fl.top_k <= TH / 4) {
+        offer(own, 0);
+      } else if (by_count) {
+        for (int q = 0; q < row.runs; ++q) offer(highs[q * TH], 0);
+      } else {
+        // the weights that matter: all others together are below a quarter of
+        // what top_p leaves out
+        const float least = (1.0f - fl.top_p) * (float)out.total * unit * 0.25f / (float)(TH * kSaRuns);
+        auto heavy = [&](float x) {
+          const float w = weight.ratio(x);
+          if (w >= least) offer(x, fixed(w, weight.s));
+        };
+        for (int q = 0; q < row.runs; ++q) heavy(highs[q * TH]);
+        row.front([&](float x, int) { heavy(x); });
+        row.back([&](float x, int) { heavy(x); });
+      }
+      __syncthreads();
+      constexpr int PER = kSaNear / TH;
+      uint64_t n = 0, all;
+      auto bin = [&](int i) {
+        const int b = threadIdx.x * PER + i;
+        return (uint64_t)work.hi[b] << 32 | work.lo[b];
+      };
+#pragma unroll
+      for (int i = 0; i < PER; ++i) n += bin(i);
+      uint64_t need = fl.top_k;
+      if (by_mass) need = part_of<true>(out.total, fmaxf(fl.top_p, 0.0f)), need += (need >> 14) + 1;  // the weights' errors
+      uint64_t n0 = block_scan<TH>(n, all, sh, turn);
+      if (n0 < need && need <= n0 + n) {
+        int i = 0;
+        while (i < PER - 1 && n0 + bin(i) < need) n0 += bin(i++);
+        sh.found = 1, sh.bin = threadIdx.x * PER + i;
+      }
+      __syncthreads();
+      // (work.lo is read no more: the list of runs shares its memory)
+      if (sh.found) skip = max(skip, top - min(top, ((uint32_t)(sh.bin + 1) << 17) - 1));
+      else few = skip > 0;  // min_p's bound alone
+    } else {
+      __syncthreads();
+    }
+    // ---- the elements from there on, if they are few ----
+    if (few) {
+      auto offer = [&](float x, int id) {
+        if (rank_value(x) >= skip && x != neg_inf()) {
+          const uint32_t at = atomicAdd(&sh.listed, 1u);
+          if (at < (uint32_t)SampleWork<TH>::kListed) work.list[at] = rank_key(x, (uint32_t)id);
+        }
+      };
+      // the runs that have any, read by all threads together
+      constexpr int kHot = SampleWork<TH>::kHot;
+      if (rank_value(own) >= skip)
+        for (int q = 0; q < row.runs; ++q)
+          if (row.has(q, skip)) {
+            const uint32_t at = atomicAdd(&sh.hot, 1u);
+            if (at < (uint32_t)kHot) work.hot[at] = threadIdx.x | (uint32_t)q << 16;
+          }
+      __syncthreads();
+      few = sh.hot <= (uint32_t)kHot;
+      if (few) {
+        const int items = (int)sh.hot * row.per;
+        for (int j = threadIdx.x; j < items; j += TH) {
+          const uint32_t who = work.hot[j / row.per];
+          const int i = ((int)(who >> 16) * row.per + j % row.per) * TH + (int)(who & 0xFFFFu);
+          if (i < row.r.nvec) row.vector(row.r.vec()[i], i, offer);
+        }
+        row.front(offer);
+        row.back(offer);
+      }
+      __syncthreads();
+      few &= sh.listed <= (uint32_t)SampleWork<TH>::kListed && (sh.listed <= (uint32_t)kList || (by_count && fl.top_k <= kList));
+    }
+    if (few) {
+      int n = (int)sh.listed;
+      sort_list<TH>(work.list, n);
+      if (fl.top_k > 0) n = min(n, fl.top_k);
+      for (int j = threadIdx.x; j < n; j += TH) work.weight[j] = weight.exact(rank_logit(work.list[j]));
+      __syncthreads();
+      sum_list<kList, TH>(work.weight, n, sh, turn);
+      if (fl.top_p < 1.0f) {
+        const uint64_t mass = by_count ? work.weight[n - 1] : out.total, near = by_count ? 0 : err;
+        {
+          const uint64_t target = max(1ull, (unsigned long long)part_of<true>(mass, fmaxf(fl.top_p, 0.0f)));
+          const uint64_t all = work.weight[n - 1];  // below the target where min_p ends the list before top_p does
+          if (threadIdx.x == 0) sh.kept = n, sh.found = near && all < target && target - all <= near;
+          __syncthreads();
+          for (int j = threadIdx.x; j < n; j += TH) {
+            const uint64_t before = j ? work.weight[j - 1] : 0, incl = work.weight[j];
+            if (before < target && target <= incl) {
+              sh.kept = j + 1;
+              sh.found = near && ((j && target - before <= near) || incl - target < near);
+            }
+          }
+          __syncthreads();
+        }
+        if (sh.found) {  // too close for the fast sum of the row
+          __syncthreads();
+          return open;
+        }
+        n = sh.kept;
+      }
+      if (edge) {
+        __syncthreads();
+        for (int j = threadIdx.x; j < n; j += TH)
+          if (work.list[j] >= edge && (j == n - 1 || work.list[j + 1] < edge)) sh.kept = j + 1;
+        __syncthreads();
+        n = sh.kept;
+      }
+      out.kept = work.weight[n - 1];
+      const uint64_t target = part_of<false>(out.kept, fl.u);
+      if (n <= 128) {  // each by the weight of the lower ids
+        if ((int)threadIdx.x < ((n + 31) & ~31)) {
+          const int j = threadIdx.x;
+          const uint32_t mine = j < n ? (uint32_t)work.list[j] : 0;  // larger for lower ids
+          uint64_t before = 0, last = 0;
+          for (int i = 0; i < n; ++i) {
+            const uint64_t upto = work.weight[i];
+            if ((uint32_t)work.list[i] > mine) before += upto - last;
+            last = upto;
+          }
+          if (j < n) {
+            const uint64_t w = work.weight[j] - (j ? work.weight[j - 1] : 0);
+            if (before <= target && target < before + w) sh.id = rank_id(work.list[j]), sh.x = rank_logit(work.list[j]);
+          }
+        }
+        __syncthreads();
+      } else {  // by the weights of 1024 ranges of ids, then within one
+        const int shift = max(0, 32 - __clz(a.V - 1) - 10);
+        for (int b = threadIdx.x; b < kSaNear; b += TH) work.lo[b] = work.hi[b] = 0;
+        if (threadIdx.x == 0) sh.listed = 0;
+        __syncthreads();
+        auto weight_of = [&](int j) { return work.weight[j] - (j ? work.weight[j - 1] : 0); };
+        for (int j = threadIdx.x; j < n; j += TH) {
+          const int b = rank_id(work.list[j]) >> shift;
+          add64(&work.lo[b], &work.hi[b], weight_of(j));
+        }
+        __syncthreads();
+        constexpr int PER = kSaNear / TH;
+        uint64_t own = 0, all;
+        auto bin = [&](int i) {
+          const int b = threadIdx.x * PER + i;
+          return (uint64_t)work.hi[b] << 32 | work.lo[b];
+        };
+#pragma unroll
+        for (int i = 0; i < PER; ++i) own += bin(i);
+        uint64_t before = block_scan<TH>(own, all, sh, turn);
+        if (before <= target && target < before + own) {
+          int i = 0;
+          while (before + bin(i) <= target) before += bin(i++);
+          sh.bin = threadIdx.x * PER + i, sh.left = before;
+        }
+        __syncthreads();
+        for (int j = threadIdx.x; j < n; j += TH)
+          if (rank_id(work.list[j]) >> shift == sh.bin)
+            work.group[atomicAdd(&sh.listed, 1u)] = work.list[j] << 32 | (uint32_t)j;  // larger for lower ids
+        __syncthreads();
+        const int in = (int)sh.listed;
+        for (int i = threadIdx.x; i < in; i += TH) {
+          const uint64_t mine = work.group[i];
+          uint64_t b = sh.left;
+          for (int k = 0; k < in; ++k)
+            if (work.group[k] > mine) b += weight_of((int)(uint32_t)work.group[k]);
+          const int j = (int)(uint32_t)mine;
+          if (b <= target && target < b + weight_of(j)) sh.id = rank_id(work.list[j]), sh.x = rank_logit(work.list[j]);
+        }
+        __syncthreads();
+      }
+      out.id = sh.id, out.x = sh.x;
+      done = true;
+    }
+  }
+  if (done && threadIdx.x == 0) put_drawn(a, t, out, fl.inv_t, m, weight.s);
+  __syncthreads();
+  return done ? 0 : open;
+}
+
 template <typename E, int TH>
 __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs a) {
-  constexpr int NW = TH / 32, kList = SampleShared<TH>::kList;
   extern __shared__ uint4 smem[];
   uint4* ring = smem;
   SampleWork<TH>& work = *reinterpret_cast<SampleWork<TH>*>(smem);
@@ -536,7 +838,6 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
   float* highs = reinterpret_cast<float*>(reinterpret_cast<char*>(smem) + kSaSmem<TH> - sizeof(SampleShared<TH>) -
                                           TH * kSaRuns * 8) + threadIdx.x;
   float* sums = highs + TH * kSaRuns;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   load_exp2(sh);
   begin_kernel();
   int turn = 0;
@@ -546,9 +847,9 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
     bool params;
     const Filters fl = filters_of(a, t, params);
     // ---- one pass: maximum and sum of each run ----
-    Weights weight = weights_of(fl.inv_t, 0.0f, a.V, sh.exp2);
+    const Weights weight = weights_of(fl.inv_t, 0.0f, a.V, sh.exp2);
     const float c = weight.ch;
-    float m = neg_inf(), own;
+    float m = neg_inf();
     {
       auto part = [&](int64_t) { return Part{row.r.vec(), row.r.nvec}; };
       Stream<TH, kSaU, kSaD, 1, E, decltype(part)> stream(part, ring + threadIdx.x, TH, threadIdx.x, t, 1, t + 1);
@@ -568,300 +869,8 @@ __global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs
     }
     row.front([&](float x, int) { m = max_nan(m, x); });
     row.back([&](float x, int) { m = max_nan(m, x); });
-    own = m;  // this thread's maximum
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (lane == 0) sh.wmax[warp] = m;
-    __syncthreads();
-    m = lane < NW ? sh.wmax[lane] : neg_inf();
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (!params || !(m <= 3.402823466e+38f) || m == neg_inf()) {
-      if (threadIdx.x == 0) {
-        const bool none = params && m == neg_inf();
-        a.tokens[t] = -1;
-        if (a.logprob) a.logprob[t] = none ? neg_inf() : quiet_nan();
-        if (a.kept_logprob) a.kept_logprob[t] = none ? neg_inf() : quiet_nan();
-        if (!params) set_status(a.status, MOE_STATUS_BAD_SAMPLING);
-        if (!(m <= 3.402823466e+38f)) set_status(a.status, MOE_STATUS_NONFINITE_LOGITS);
-      }
-      __syncthreads();
-      continue;
-    }
-    weight.m = m;
-    // the runs' sums from their own shifts to the maximum, of unit 2^-s
-    const float mc = __fmul_rn(m, c), M = fmaxf(ceilf(mc), -kShiftLimit), cl_ch = fabsf(weight.cl) / weight.ch;
-    const float to_m = exp2_fast((M - mc) - fmaf(m, c, -mc));
-    auto run_float = [&](int q) {  // at most 2^10
-      return sums[q * TH] * exp2_fast(RunSum::shift_of(highs[q * TH], c) - M) * to_m;
-    };
-    const bool shift_ok = fabsf(mc) <= kShiftLimit;
-    const bool filtered = fl.top_k > 0 || fl.top_p < 1.0f || fl.min_p > 0.0f;
-    uint64_t edge = 0;  // keys below have less than min_p
-    if (fl.min_p > 0.0f) edge = min_p_key(m, sh.edge);
-    Drawn out;
-    uint64_t sum = 0, err, weight_err;  // errors of sums of the pass, and of weights by themselves
-    const float unit = ldexpf(1.0f, -weight.s);
-    int e = 0;  // the part of the row with the token
-    if (filtered && !shift_ok) {  // the pass's weights are out of range
-      row.all(0, [&](float x, int) { sum += weight.fast(x); });
-      block_scan<TH>(sum, out.total, sh, turn);
-    } else if (filtered) {
-      float w = 0.0f;
-      for (int q = 0; q < row.runs; ++q) w += run_float(q);
-      sum = fixed(w, weight.s);
-      row.front([&](float x, int) { sum += weight.fast(x); });
-      row.back([&](float x, int) { sum += weight.fast(x); });
-      block_scan<TH>(sum, out.total, sh, turn);
-    }
-    if (!filtered) {
-      // the warp's sums of the eight runs: lane l ends with run l / 4's
-      float w[kSaRuns];
-#pragma unroll
-      for (int q = 0; q < kSaRuns; ++q) {
-        w[q] = 0.0f;
-        if (q < row.runs) {
-          if (shift_ok) w[q] = run_float(q);
-          else row.run(q, [&](float x, int) { w[q] += weight.ratio(x); });
-        }
-      }
-#pragma unroll
-      for (int h = 4, o = 16; h > 0; h /= 2, o /= 2)
-#pragma unroll
-        for (int q = 0; q < h; ++q) {
-          const float keep = lane & o ? w[q + h] : w[q], give = lane & o ? w[q] : w[q + h];
-          w[q] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
-        }
-      w[0] += __shfl_xor_sync(0xFFFFFFFFu, w[0], 2);
-      w[0] += __shfl_xor_sync(0xFFFFFFFFu, w[0], 1);
-      if ((lane & 3) == 0 && lane / 4 < row.runs) sh.part[lane / 4 + 1][warp] = fixed(w[0], weight.s);
-      out.total = out.kept = pick<E, TH>(row, fl.u, [&](float x, int) { return weight.fast(x); }, [&](const uint4& v) {
-        constexpr int N = Row<E>::kVec;
-        float x[N];
-        unpack(v, x);
-#pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = weight.ratio(x[e]);
-#pragma unroll
-        for (int h = N / 2; h > 0; h /= 2)
-#pragma unroll
-          for (int e = 0; e < h; ++e) x[e] += x[e + h];
-        return fixed(x[0], weight.s);
-      }, sh, work.group, turn);
-      out.id = sh.id, out.x = sh.x;
-      uint64_t first;
-      e = find_part<E, TH>(row, sh.target, first, sh);
-    }
-    {
-      // in the pass 3 additions per sum of pairs, 3 to join them, one per batch of
-      // a run, a product with to_m; then 5 over the warp, or, with the filters, 8
-      // for the thread's runs, and to_m's own error, which is otherwise the same
-      // for all.  Weights by themselves: 3 in a vector, and with the range of the
-      // pass exceeded as many as a run has elements, and 5 over the warp.
-      const float S = (float)out.total * unit;
-      const float near = sum_error(S, a.V, cl_ch, 2, 3);
-      weight_err = (uint64_t)((float)(filtered ? out.total : sh.sums[e]) * (near + 0x1p-22f));
-      err = shift_ok ? (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 1, 7 + row.per / kSaU + (filtered ? 12 : 5)))
-                     : (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 2, filtered ? 0 : row.per * Row<E>::kVec + 5));
-    }
-    const int open = kOpen - (64 - __clzll((long long)out.total) - weight.s);
-    bool done = false;
-    if (!filtered) {
-      err += weight_err;  // of the run with the token
-      done = sh.id >= 0 && (sh.before == 0 || sh.target - sh.before > err) &&
-             (sh.after >= out.total || sh.after - sh.target > err);
-    } else {
-      // ---- a lower bound of what is kept, from the maxima ----
-      const uint32_t top = rank_value(m);
-      uint32_t skip = (uint32_t)(edge >> 32);
-      const bool by_count = fl.top_k > 0, by_mass = !by_count && fl.top_p < 1.0f;
-      if (by_count && fl.top_p < 1.0f) skip = 0;  // all of the top_k count for top_p
-      if (threadIdx.x == 0) sh.found = 0, sh.listed = 0, sh.hot = 0;
-      bool few = true;
-      if (by_count || by_mass) {
-        for (int b = threadIdx.x; b < kSaNear; b += TH) work.lo[b] = 0, work.hi[b] = 0;
-        __syncthreads();
-        auto offer = [&](float x, uint64_t w) {
-          const uint32_t d = top - rank_value(x);
-          if (d >= 1u << 27 || x == neg_inf()) return;
-          if (by_count) atomicAdd(&work.lo[d >> 17], 1u);
-          else add64(&work.lo[d >> 17], &work.hi[d >> 17], w);
-        };
-        if (by_count && fl.top_k <= TH / 4) {
-          offer(own, 0);
-        } else if (by_count) {
-          for (int q = 0; q < row.runs; ++q) offer(highs[q * TH], 0);
-        } else {
-          // the weights that matter: all others together are below a quarter of
-          // what top_p leaves out
-          const float least = (1.0f - fl.top_p) * (float)out.total * unit * 0.25f / (float)(TH * kSaRuns);
-          auto heavy = [&](float x) {
-            const float w = weight.ratio(x);
-            if (w >= least) offer(x, fixed(w, weight.s));
-          };
-          for (int q = 0; q < row.runs; ++q) heavy(highs[q * TH]);
-          row.front([&](float x, int) { heavy(x); });
-          row.back([&](float x, int) { heavy(x); });
-        }
-        __syncthreads();
-        constexpr int PER = kSaNear / TH;
-        uint64_t n = 0, all;
-        auto bin = [&](int i) {
-          const int b = threadIdx.x * PER + i;
-          return (uint64_t)work.hi[b] << 32 | work.lo[b];
-        };
-#pragma unroll
-        for (int i = 0; i < PER; ++i) n += bin(i);
-        uint64_t need = fl.top_k;
-        if (by_mass) need = part_of<true>(out.total, fmaxf(fl.top_p, 0.0f)), need += (need >> 14) + 1;  // the weights' errors
-        uint64_t n0 = block_scan<TH>(n, all, sh, turn);
-        if (n0 < need && need <= n0 + n) {
-          int i = 0;
-          while (i < PER - 1 && n0 + bin(i) < need) n0 += bin(i++);
-          sh.found = 1, sh.bin = threadIdx.x * PER + i;
-        }
-        __syncthreads();
-        // (work.lo is read no more: the list of runs shares its memory)
-        if (sh.found) skip = max(skip, top - min(top, ((uint32_t)(sh.bin + 1) << 17) - 1));
-        else few = skip > 0;  // min_p's bound alone
-      } else {
-        __syncthreads();
-      }
-      // ---- the elements from there on, if they are few ----
-      if (few) {
-        auto offer = [&](float x, int id) {
-          if (rank_value(x) >= skip && x != neg_inf()) {
-            const uint32_t at = atomicAdd(&sh.listed, 1u);
-            if (at < (uint32_t)SampleWork<TH>::kListed) work.list[at] = rank_key(x, (uint32_t)id);
-          }
-        };
-        // the runs that have any, read by all threads together
-        constexpr int kHot = SampleWork<TH>::kHot;
-        if (rank_value(own) >= skip)
-          for (int q = 0; q < row.runs; ++q)
-            if (row.has(q, skip)) {
-              const uint32_t at = atomicAdd(&sh.hot, 1u);
-              if (at < (uint32_t)kHot) work.hot[at] = threadIdx.x | (uint32_t)q << 16;
-            }
-        __syncthreads();
-        few = sh.hot <= (uint32_t)kHot;
-        if (few) {
-          const int items = (int)sh.hot * row.per;
-          for (int j = threadIdx.x; j < items; j += TH) {
-            const uint32_t who = work.hot[j / row.per];
-            const int i = ((int)(who >> 16) * row.per + j % row.per) * TH + (int)(who & 0xFFFFu);
-            if (i < row.r.nvec) row.vector(row.r.vec()[i], i, offer);
-          }
-          row.front(offer);
-          row.back(offer);
-        }
-        __syncthreads();
-        few &= sh.listed <= (uint32_t)SampleWork<TH>::kListed && (sh.listed <= (uint32_t)kList || (by_count && fl.top_k <= kList));
-      }
-      if (few) {
-        int n = (int)sh.listed;
-        sort_list<TH>(work.list, n);
-        if (fl.top_k > 0) n = min(n, fl.top_k);
-        for (int j = threadIdx.x; j < n; j += TH) work.weight[j] = weight.exact(rank_logit(work.list[j]));
-        __syncthreads();
-        sum_list<kList, TH>(work.weight, n, sh, turn);
-        if (fl.top_p < 1.0f) {
-          const uint64_t mass = by_count ? work.weight[n - 1] : out.total, near = by_count ? 0 : err;
-          {
-            const uint64_t target = max(1ull, (unsigned long long)part_of<true>(mass, fmaxf(fl.top_p, 0.0f)));
-            const uint64_t all = work.weight[n - 1];  // below the target where min_p ends the list before top_p does
-            if (threadIdx.x == 0) sh.kept = n, sh.found = near && all < target && target - all <= near;
-            __syncthreads();
-            for (int j = threadIdx.x; j < n; j += TH) {
-              const uint64_t before = j ? work.weight[j - 1] : 0, incl = work.weight[j];
-              if (before < target && target <= incl) {
-                sh.kept = j + 1;
-                sh.found = near && ((j && target - before <= near) || incl - target < near);
-              }
-            }
-            __syncthreads();
-          }
-          if (sh.found) {  // too close for the fast sum of the row
-            if (threadIdx.x == 0) a.tokens[t] = open;
-            __syncthreads();
-            continue;
-          }
-          n = sh.kept;
-        }
-        if (edge) {
-          __syncthreads();
-          for (int j = threadIdx.x; j < n; j += TH)
-            if (work.list[j] >= edge && (j == n - 1 || work.list[j + 1] < edge)) sh.kept = j + 1;
-          __syncthreads();
-          n = sh.kept;
-        }
-        out.kept = work.weight[n - 1];
-        const uint64_t target = part_of<false>(out.kept, fl.u);
-        if (n <= 128) {  // each by the weight of the lower ids
-          if ((int)threadIdx.x < ((n + 31) & ~31)) {
-            const int j = threadIdx.x;
-            const uint32_t mine = j < n ? (uint32_t)work.list[j] : 0;  // larger for lower ids
-            uint64_t before = 0, last = 0;
-            for (int i = 0; i < n; ++i) {
-              const uint64_t upto = work.weight[i];
-              if ((uint32_t)work.list[i] > mine) before += upto - last;
-              last = upto;
-            }
-            if (j < n) {
-              const uint64_t w = work.weight[j] - (j ? work.weight[j - 1] : 0);
-              if (before <= target && target < before + w) sh.id = rank_id(work.list[j]), sh.x = rank_logit(work.list[j]);
-            }
-          }
-          __syncthreads();
-        } else {  // by the weights of 1024 ranges of ids, then within one
-          const int shift = max(0, 32 - __clz(a.V - 1) - 10);
-          for (int b = threadIdx.x; b < kSaNear; b += TH) work.lo[b] = work.hi[b] = 0;
-          if (threadIdx.x == 0) sh.listed = 0;
-          __syncthreads();
-          auto weight_of = [&](int j) { return work.weight[j] - (j ? work.weight[j - 1] : 0); };
-          for (int j = threadIdx.x; j < n; j += TH) {
-            const int b = rank_id(work.list[j]) >> shift;
-            add64(&work.lo[b], &work.hi[b], weight_of(j));
-          }
-          __syncthreads();
-          constexpr int PER = kSaNear / TH;
-          uint64_t own = 0, all;
-          auto bin = [&](int i) {
-            const int b = threadIdx.x * PER + i;
-            return (uint64_t)work.hi[b] << 32 | work.lo[b];
-          };
-#pragma unroll
-          for (int i = 0; i < PER; ++i) own += bin(i);
-          uint64_t before = block_scan<TH>(own, all, sh, turn);
-          if (before <= target && target < before + own) {
-            int i = 0;
-            while (before + bin(i) <= target) before += bin(i++);
-            sh.bin = threadIdx.x * PER + i, sh.left = before;
-          }
-          __syncthreads();
-          for (int j = threadIdx.x; j < n; j += TH)
-            if (rank_id(work.list[j]) >> shift == sh.bin)
-              work.group[atomicAdd(&sh.listed, 1u)] = work.list[j] << 32 | (uint32_t)j;  // larger for lower ids
-          __syncthreads();
-          const int in = (int)sh.listed;
-          for (int i = threadIdx.x; i < in; i += TH) {
-            const uint64_t mine = work.group[i];
-            uint64_t b = sh.left;
-            for (int k = 0; k < in; ++k)
-              if (work.group[k] > mine) b += weight_of((int)(uint32_t)work.group[k]);
-            const int j = (int)(uint32_t)mine;
-            if (b <= target && target < b + weight_of(j)) sh.id = rank_id(work.list[j]), sh.x = rank_logit(work.list[j]);
-          }
-          __syncthreads();
-        }
-        out.id = sh.id, out.x = sh.x;
-        done = true;
-      }
-    }
-    if (threadIdx.x == 0) {
-      if (done) put_drawn(a, t, out, fl.inv_t, m, weight.s);
-      else a.tokens[t] = open;
-    }
-    __syncthreads();
+    const int open = end_row<E, TH>(a, t, row, fl, params, weight, m, highs, sums, sh, work, turn);
+    if (open && threadIdx.x == 0) a.tokens[t] = open;
   }
 }
 
@@ -902,6 +911,19 @@ struct TeamWork {
   int flag, first;
   uint64_t base, key, incl;
   int edge;
+};
+
+// Shared memory of a block that works on few rows.
+struct FewWork {
+  TeamShared sh;
+  union {
+    TeamWork team;
+    struct {
+      SampleWork<kTeamThreads> work;
+      float highs[kTeamThreads * kSaRuns], sums[kTeamThreads * kSaRuns];
+    };
+  };
+  uint32_t open;
 };
 
 // Bins of the ranks at and below the row's maximum's, `top`: by 1/128 of a power
@@ -1675,6 +1697,113 @@ __device__ __forceinline__ uint64_t Team<E>::Exact::operator()(float x) const {
   return (p0 - kMinExponent) + e >= 0.0f ? w : 0;
 }
 
+// The powers of 2^(1/1024) for exact weights.
+__device__ __forceinline__ void load_powers(TeamShared& sh, TeamWork& work) {
+  load_exp2(sh);
+  __syncthreads();
+  Weights one;  // 2^(j / 1024 - 1), of unit 2^-61
+  one.m = 1024.0f, one.ch = 0x1p-10f, one.cl = 0.0f, one.s = 61, one.exp2 = sh.exp2;
+  for (int j = threadIdx.x; j < 1024; j += kTeamThreads) work.power[j] = one.exact((float)j) << 2;
+  __syncthreads();
+}
+
+// An open row's token by its team of `size` blocks.
+template <typename E>
+__device__ __forceinline__ void open_row(const SampleArgs& a, int64_t t, int flag, int rank, int size, int& turn,
+                                         int& scan_turn, TeamShared& sh, TeamWork& work) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = size == 1 ? 0 : kTeamLog;
+  const int log_s = kOpen - flag;
+  const E* logits = static_cast<const E*>(a.logits) + t * a.ld;
+  const Row<E> whole(logits, a.V);
+  const int v0 = whole.part(rank, lg), v1 = whole.part(rank + 1, lg);
+  const int id0 = rank == 0 ? 0 : whole.head + v0 * Row<E>::kVec;
+  const int id1 = rank == size - 1 ? a.V : whole.head + v1 * Row<E>::kVec;
+  const Row<E> r(logits + id0, id1 - id0);
+  Team<E> team = {r, id0, rank, size, turn, scan_turn, (r.nvec + 31) / 32, Weights(), sh, work};
+  bool params;
+  const Filters fl = filters_of(a, t, params);
+  // the row's maximum, a number
+  const float high = team.high();
+  uint32_t top = __reduce_max_sync(0xFFFFFFFFu, rank_value(high));
+  if (lane == 0) sh.scan[0][warp] = top;
+  __syncthreads();
+  top = __reduce_max_sync(0xFFFFFFFFu, lane < kTeamWarps ? (uint32_t)sh.scan[0][lane] : 0u);
+  __syncthreads();
+  uint64_t all, none;
+  team.share(top, 0, all, none);
+  top = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)all);
+  team.weight = weights_of(fl.inv_t, rank_logit((uint64_t)top << 32), a.V, sh.exp2);
+  Drawn out;
+  if (team.draw(fl, a.V, log_s, out) && threadIdx.x == 0) {
+    out.id = sh.id, out.x = sh.x;
+    put_drawn(a, t, out, fl.inv_t, team.weight.m, team.weight.s);
+  }
+  __syncthreads();
+  scan_turn = team.scan_turn;
+  turn = team.turn;
+}
+
+// Few rows: a cluster of eight blocks per row, each of which reads one of the runs
+// that a block's threads have; the first block ends the row, and if it stays open
+// all eight decide it at once.
+template <typename E>
+__global__ void __launch_bounds__(kTeamThreads, 1) sample_few_kernel(SampleArgs a) {
+  constexpr int TH = kTeamThreads;
+  static_assert(kTeam == kSaRuns, "a run per block");
+  extern __shared__ uint4 smem[];
+  FewWork& few = *reinterpret_cast<FewWork*>(smem);
+  TeamWork& work = few.team;
+  TeamShared& sh = few.sh;
+  const int rank = (int)blockIdx.x % kTeam;
+  const int64_t clusters = gridDim.x / kTeam;
+  float *highs = few.highs + threadIdx.x, *sums = few.sums + threadIdx.x;
+  int turn = 0, team_turn = 0;
+  load_exp2(sh);
+  cluster_arrive();  // all blocks run: their shared memory may be written
+  cluster_wait();
+  begin_kernel();
+  for (int64_t t = blockIdx.x / kTeam; t < a.T; t += clusters) {
+    const SampleRow<E, TH> row(static_cast<const E*>(a.logits) + t * a.ld, a.V, highs);
+    bool params;
+    const Filters fl = filters_of(a, t, params);
+    const Weights weight = weights_of(fl.inv_t, 0.0f, a.V, sh.exp2);
+    if (rank < row.runs) {
+      RunSum acc;
+      for (int j = 0; j < row.per; j += kSaU) {
+        const int i0 = (rank * row.per + j) * TH + (int)threadIdx.x;
+        uint4 v[kSaU];
+#pragma unroll
+        for (int u = 0; u < kSaU; ++u) {
+          v[u] = Stream<TH, 1, 1, 1, E, int>::none(E());
+          if (i0 + u * TH < row.r.nvec) v[u] = row.r.vec()[i0 + u * TH];
+        }
+        acc.add(v, weight.ch, E());
+      }
+      cluster_store(&highs[rank * TH], 0, __float_as_uint(acc.m));
+      cluster_store(&sums[rank * TH], 0, __float_as_uint(acc.s));
+    }
+    if (rank == 0 && fl.min_p > 0.0f && threadIdx.x == TH - 1) min_p_edge(fl, sh.edge);
+    cluster_arrive();
+    cluster_wait();
+    if (rank == 0) {
+      float m = neg_inf();
+      for (int q = 0; q < row.runs; ++q) m = max_nan(m, highs[q * TH]);
+      row.front([&](float x, int) { m = max_nan(m, x); });
+      row.back([&](float x, int) { m = max_nan(m, x); });
+      const int open = end_row<E, TH>(a, t, row, fl, params, weight, m, highs, sums, sh, few.work, turn);
+      if (threadIdx.x < kTeam) cluster_store(&few.open, threadIdx.x, (uint32_t)open);
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (few.open) {
+      load_powers(sh, work);
+      open_row<E>(a, t, (int)few.open, rank, kTeam, team_turn, turn, sh, work);
+    }
+    cluster_arrive();  // the first block's maxima and sums are read no more
+    cluster_wait();
+  }
+}
+
 __device__ __forceinline__ bool is_open(int token) { return token <= kOpen && token > kClaimed; }
 
 // The next open row from place `seen` on of the rows taken in turn from `start`
@@ -1710,7 +1839,7 @@ __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs
   extern __shared__ uint4 smem[];
   TeamWork& work = *reinterpret_cast<TeamWork*>(smem);
   TeamShared& sh = *reinterpret_cast<TeamShared*>(&work + 1);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank_in_cluster = (int)blockIdx.x % kTeam;
+  const int rank_in_cluster = (int)blockIdx.x % kTeam;
   const int64_t teams = gridDim.x / kTeam, cluster = blockIdx.x / kTeam;
   bool ready = false;
   int turn = 0, scan_turn = 0;
@@ -1733,7 +1862,7 @@ __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs
   rows = (int)work.claim;
   if (rows == 0) return;
   const bool alone = rows > 2 * teams && a.V / Row<E>::kVec <= kTeamGroups * 32;
-  const int size = alone ? 1 : kTeam, rank = alone ? 0 : rank_in_cluster, lg = alone ? 0 : kTeamLog;
+  const int size = alone ? 1 : kTeam, rank = alone ? 0 : rank_in_cluster;
   // The search for a row begins at a place of the block's or cluster's own.
   const int64_t start = a.T * (alone ? (int64_t)blockIdx.x : cluster * kTeam) / gridDim.x;
   int64_t seen = 0;
@@ -1753,44 +1882,11 @@ __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs
     }
     if (t < 0) break;
     if (!ready) {
-      load_exp2(sh);
-      __syncthreads();
-      Weights one;  // 2^(j / 1024 - 1), of unit 2^-61
-      one.m = 1024.0f, one.ch = 0x1p-10f, one.cl = 0.0f, one.s = 61, one.exp2 = sh.exp2;
-      for (int j = threadIdx.x; j < 1024; j += kTeamThreads) work.power[j] = one.exact((float)j) << 2;
-      __syncthreads();
+      load_powers(sh, work);
       ready = true;
     }
     {
-      const int log_s = kOpen - flag;
-      const E* logits = static_cast<const E*>(a.logits) + t * a.ld;
-      const Row<E> whole(logits, a.V);
-      const int v0 = whole.part(rank, lg), v1 = whole.part(rank + 1, lg);
-      const int id0 = rank == 0 ? 0 : whole.head + v0 * Row<E>::kVec;
-      const int id1 = rank == size - 1 ? a.V : whole.head + v1 * Row<E>::kVec;
-      const Row<E> r(logits + id0, id1 - id0);
-      Team<E> team = {r, id0, rank, size, turn, scan_turn, (r.nvec + 31) / 32, Weights(), sh, work};
-      bool params;
-      const Filters fl = filters_of(a, t, params);
-      // the row's maximum, a number
-      const float high = team.high();
-      uint32_t top = __reduce_max_sync(0xFFFFFFFFu, rank_value(high));
-      if (lane == 0) sh.scan[0][warp] = top;
-      __syncthreads();
-      top = __reduce_max_sync(0xFFFFFFFFu, lane < kTeamWarps ? (uint32_t)sh.scan[0][lane] : 0u);
-      __syncthreads();
-      uint64_t all, none;
-      team.share(top, 0, all, none);
-      top = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)all);
-      team.weight = weights_of(fl.inv_t, rank_logit((uint64_t)top << 32), a.V, sh.exp2);
-      Drawn out;
-      if (team.draw(fl, a.V, log_s, out) && threadIdx.x == 0) {
-        out.id = sh.id, out.x = sh.x;
-        put_drawn(a, t, out, fl.inv_t, team.weight.m, team.weight.s);
-      }
-      __syncthreads();
-      scan_turn = team.scan_turn;
-      turn = team.turn;
+      open_row<E>(a, t, flag, rank, size, turn, scan_turn, sh, work);
     }
   }
 }
@@ -1803,6 +1899,11 @@ static int launch_sample(const SampleArgs& a, cudaStream_t s) {
   return launch_kernel(f, (unsigned)(a.T < most ? a.T : most), TH, kSaSmem<TH>, 1, s, a);
 }
 int launch_sample_tokens(const SampleArgs& a, cudaStream_t s) {
+  if (a.T <= gemm_num_ctas() / kTeam) {
+    auto f = a.dtype == MOE_DTYPE_BF16 ? sample_few_kernel<uint16_t> : sample_few_kernel<float>;
+    if (!allow_smem((const void*)f, (int)sizeof(FewWork), (int)sizeof(FewWork))) return -1;
+    return launch_kernel(f, (unsigned)(a.T * kTeam), kTeamThreads, sizeof(FewWork), kTeam, s, a);
+  }
   // Two blocks of 512 threads per SM while each row has one at once; else four of
   // 256, whose ends the others cover.
   const int rc = a.T <= 2 * gemm_num_ctas() ? launch_sample<512>(a, s) : launch_sample<256>(a, s);
