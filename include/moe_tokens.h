@@ -50,14 +50,15 @@ int moe_embed_tokens(const int32_t* ids, const void* table, int dtype,
                      int64_t ldt, int T, int V, int d, float scale,
                      uint16_t* out, int64_t ldo, int* status, void* stream);
 
-/* Workspace of moe_embed_tokens_backward: the tokens sorted by id, and the
- * parts of the sums of ids that many tokens name.  0 for sizes out of range. */
+/* Workspace of moe_embed_tokens_backward: the tokens sorted by id, a bit map of
+ * the ids, and the parts of the sums of ids that many tokens name.  0 for sizes
+ * out of range.  Calls that may run at the same time need their own. */
 size_t moe_embed_tokens_backward_workspace_bytes(int T, int V, int d);
 
 /* The gradient of moe_embed_tokens with respect to the table:
  *   dtable_v = scale * sum over the t with ids_t = v of dy_t  (+ dtable_v)
- * summed in FP32 in a fixed order (ascending t within tiles of the tokens
- * sorted by id, the tiles in turn), multiplied by scale once.
+ * summed in FP32 in an order that follows from the sizes and the ids alone, and
+ * multiplied by scale once.
  *   dy      bf16 [T] rows of d, ldy elements apart
  *   ids     as in the forward: negative ids and ids >= V contribute nothing,
  *           the latter set MOE_STATUS_BAD_TOKEN
@@ -66,7 +67,8 @@ size_t moe_embed_tokens_backward_workspace_bytes(int T, int V, int d);
  *           others are neither read nor written.
  *   dtable  f32 [V][d]
  *   ws      moe_embed_tokens_backward_workspace_bytes(T, V, d) bytes
- * Limits as moe_embed_tokens; T <= 2^24, ldy >= d and a multiple of 8. */
+ * Limits as moe_embed_tokens; T <= 2^24, ldy >= d and a multiple of 8.  One
+ * launch up to 1024 tokens, four to six beyond. */
 int moe_embed_tokens_backward(const uint16_t* dy, int64_t ldy,
                               const int32_t* ids, int T, int V, int d,
                               float scale, int accumulate, float* dtable,
@@ -87,8 +89,9 @@ int moe_embed_tokens_backward(const uint16_t* dy, int64_t ldy,
  *   4. the token is the first kept id, in the order of the ids, up to which
  *      the kept weight is above u times all of it.
  * The token is the one of these formulas in exact arithmetic unless a border
- * lies within some 2^-36 of the row's weight: rows whose decision FP32 weights
- * leave open are decided by weights of that precision.
+ * lies within some 2^-33 of the row's weight: FP32 weights decide where their
+ * error bound allows it, and weights of that precision where it does not.  Equal
+ * logits have equal weights, and sums of weights 1 are exact.
  *   logits   [T] rows of V, ld elements apart, MOE_DTYPE_BF16 or MOE_DTYPE_F32
  *   inv_temperature  f32 [T], each 1e-6 to 1e6, or NULL for 1
  *   top_k    i32 [T], or NULL; < 1 or >= V: off
@@ -104,7 +107,12 @@ int moe_embed_tokens_backward(const uint16_t* dy, int64_t ldy,
  * +inf token -1, NaN twice and MOE_STATUS_NONFINITE_LOGITS; a row whose
  * inv_temperature or u is out of range or whose top_p or min_p is NaN token
  * -1, NaN twice and MOE_STATUS_BAD_SAMPLING.
- * Needs 1 <= V <= MOE_SAMPLE_MAX_V, ld >= V.  One launch. */
+ * The tokens do not depend on the other rows; the log-probabilities may differ
+ * in their last bits with T.  Between its launches the call marks rows in tokens,
+ * which nothing else may write or read meanwhile.
+ * Needs 1 <= V <= MOE_SAMPLE_MAX_V, ld >= V.  One launch for few rows (a cluster
+ * of blocks each), else two: the second decides rows that the first leaves open,
+ * which are few where the weight of each row lies in few ids. */
 int moe_sample_tokens(const void* logits, int dtype, int64_t ld, int T, int V,
                       const float* inv_temperature, const int32_t* top_k,
                       const float* top_p, const float* min_p, const float* u,

@@ -422,7 +422,7 @@ __device__ __forceinline__ uint64_t pick(const SampleRow<E, TH>& row, float u, F
 
 // n distinct keys, descending, in list (room for the next power of two).
 template <int TH>
-__device__ __noinline__ void sort_list(uint64_t* list, int n) {
+__device__ __forceinline__ void sort_list(uint64_t* list, int n) {
   const int k = threadIdx.x;
   if (n <= 256 && n <= TH) {  // each key's place by counting the larger ones
     const uint64_t key = k < n ? list[k] : 0;
@@ -629,6 +629,7 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
     weight_err = (uint64_t)((float)(filtered ? out.total : sh.sums[e]) * (near + 0x1p-22f));
     err = shift_ok ? (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 1, 7 + row.per / kSaU + (filtered ? 12 : 5)))
                    : (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 2, filtered ? 0 : row.per * Row<E>::kVec + 5));
+    err += (uint64_t)a.V << (weight.s - 42);  // weights below 2^-42, which the pass adds
   }
   const int open = kOpen - (64 - __clzll((long long)out.total) - weight.s);
   bool done = false;
@@ -1733,6 +1734,7 @@ __device__ __forceinline__ void open_row(const SampleArgs& a, int64_t t, int fla
   team.share(top, 0, all, none);
   top = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)all);
   team.weight = weights_of(fl.inv_t, rank_logit((uint64_t)top << 32), a.V, sh.exp2);
+  team.weight.s = min(52, 62 - log_s);  // as fine as the row's own sum allows
   Drawn out;
   if (team.draw(fl, a.V, log_s, out) && threadIdx.x == 0) {
     out.id = sh.id, out.x = sh.x;
