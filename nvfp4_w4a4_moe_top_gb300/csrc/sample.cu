@@ -56,7 +56,8 @@ __device__ __forceinline__ uint64_t fixed(float w, int s) {
 
 template <int TH>
 struct SampleShared {
-  static constexpr int NW = TH / 32, kList = 1536;  // weighed elements: top_k of 1000 among them
+  static constexpr int NW = TH / 32;
+  static constexpr int kList = TH < 256 ? 512 : 1536;  // weighed elements: top_k of 1000 among them
   uint64_t exp2[64];               // 2^(j/64) 2^62
   uint64_t part[kSaRuns + 2][NW];  // sums of the runs by warp; the row's ends
   uint64_t sums[kSaRuns + 2];      // of all warps
@@ -72,7 +73,7 @@ struct SampleShared {
 // What shares its memory with the ring that the logits come through.
 template <int TH>
 struct SampleWork {
-  static constexpr int kHot = TH * kSaRuns, kListed = 2048;
+  static constexpr int kHot = TH * kSaRuns, kListed = TH < 256 ? 512 : 2048;
   uint64_t list[kListed], weight[SampleShared<TH>::kList];
   union {
     struct {
@@ -886,26 +887,36 @@ __device__ __forceinline__ void cluster_store(const void* p, uint32_t rank, uint
 // weights to 2^-34.  The team is a cluster of eight blocks, or, where there are many
 // open rows, one block: eight are sooner done with one row, but wait for one
 // another.  The sums are whole numbers, so the results are the same. ----
-constexpr int kTeam = 8, kTeamLog = 3;
-constexpr int kTeamThreads = 512, kTeamWarps = kTeamThreads / 32;
-constexpr int kTeamList = 2048;
-constexpr int kTeamBins = 4096;
-constexpr int kTeamGroups = 1024;  // of 32 vectors: (2^20 / 4 / 8) / 32
-using TeamShared = SampleShared<kTeamThreads>;
+// Sizes of a team's work: threads of a block, bins, listed elements, groups of 32
+// vectors, and blocks.
+template <int THREADS, int BINS, int LIST, int GROUPS, int TEAM>
+struct TeamSizes {
+  static constexpr int kThreads = THREADS, kWarps = THREADS / 32, kBins = BINS, kList = LIST, kGroups = GROUPS;
+  static constexpr int kTeam = TEAM, kTeamLog = TEAM == 8 ? 3 : 0;
+  static constexpr int kNear = BINS / 2, kNearShift = BINS == 4096 ? 16 : 18;  // kNear << kNearShift = 2^27
+  static constexpr bool kValues = BINS == 4096;                                // a bin per BF16 value
+  static_assert(kNear << kNearShift == 1 << 27, "sixteen powers of two");
+};
+using LongTeam = TeamSizes<512, 4096, 2048, 1024, 8>;  // groups: (2^20 / 4 / 8) / 32
+// Rows of up to kShortV ids, by one small block: many rows on the way, which wait
+// for their own barriers only.
+using ShortTeam = TeamSizes<128, 1024, 512, 64, 1>;
+constexpr int kShortV = 8192;
 constexpr int kTeamU = 4;          // vectors read together
 constexpr int kClaimed = -(1 << 30);  // in tokens: an open row that a block works on
 
+template <typename C>
 struct TeamWork {
   uint64_t power[1024];             // 2^(j/1024) 2^62
   union {
     struct {
-      uint64_t list[kTeamList], weight[kTeamList];
+      uint64_t list[C::kList], weight[C::kList];
     };
-    uint64_t table[kTeamBins];      // BF16: the weight of each bin's one value
+    uint64_t table[C::kBins];      // BF16: the weight of each bin's one value
   };
-  uint64_t group[kTeamGroups + 2];  // the elements before the vectors, 32 vectors in a row each, the elements after
-  uint64_t ties[kTeamGroups + 2];
-  uint32_t lo[kTeamBins], hi[kTeamBins];
+  uint64_t group[C::kGroups + 2];  // the elements before the vectors, 32 vectors in a row each, the elements after
+  uint64_t ties[C::kGroups + 2];
+  uint32_t lo[C::kBins], hi[C::kBins];
   uint64_t box[2][2];               // what the blocks tell one another, in turn
   int64_t row, claimed;             // a row that a block takes
   uint32_t claim;
@@ -916,42 +927,43 @@ struct TeamWork {
 
 // Shared memory of a block that works on few rows.
 struct FewWork {
-  TeamShared sh;
+  SampleShared<LongTeam::kThreads> sh;
   union {
-    TeamWork team;
+    TeamWork<LongTeam> team;
     struct {
-      SampleWork<kTeamThreads> work;
-      float highs[kTeamThreads * kSaRuns], sums[kTeamThreads * kSaRuns];
+      SampleWork<LongTeam::kThreads> work;
+      float highs[LongTeam::kThreads * kSaRuns], sums[LongTeam::kThreads * kSaRuns];
     };
   };
   uint32_t open;
 };
 
-// Bins of the ranks at and below the row's maximum's, `top`: by 1/128 of a power
-// of two over sixteen of them, then one bin down to -2^-10, then by 1/64 of a
-// power of two over 32 of them, and the rest.
-constexpr int kTeamNear = 2048;
+// Bins of the ranks at and below the row's maximum's, `top`: by 1/128 (1/32) of a
+// power of two over sixteen of them, then one bin down to -2^-10, then by 1/64
+// (1/16) of a power of two over 32 of them, and the rest.
 constexpr uint32_t kNegative = 0x7FFFFFFFu - 0x3A800000u;  // rank of -2^-10
+template <typename C>
 __device__ __forceinline__ int first_bin(uint32_t top, uint32_t rank) {
   const uint32_t d = top - rank;
-  if (d < 1u << 27) return (int)(d >> 16);
-  return rank >= kNegative ? kTeamNear : min(kTeamBins - 1, kTeamNear + 1 + (int)((kNegative - 1 - rank) >> 17));
+  if (d < 1u << 27) return (int)(d >> C::kNearShift);
+  return rank >= kNegative ? C::kNear : min(C::kBins - 1, C::kNear + 1 + (int)((kNegative - 1 - rank) >> (C::kNearShift + 1)));
 }
 // First distance below `top` that is not in a bin before b.
+template <typename C>
 __device__ __forceinline__ uint32_t first_bin_start(uint32_t top, int b) {
-  if (b <= kTeamNear) return (uint32_t)b << 16;
-  const int64_t d = (int64_t)top - (int64_t)kNegative + 1 + ((int64_t)(b - kTeamNear - 1) << 17);
-  return b >= kTeamBins ? 0xFFFFFFFFu : (uint32_t)max((long long)d, 1ll << 27);
+  if (b <= C::kNear) return (uint32_t)b << C::kNearShift;
+  const int64_t d = (int64_t)top - (int64_t)kNegative + 1 + ((int64_t)(b - C::kNear - 1) << (C::kNearShift + 1));
+  return b >= C::kBins ? 0xFFFFFFFFu : (uint32_t)max((long long)d, 1ll << 27);
 }
 
 // A block's part of a row, ids from id0 on, and what the block and its team know.
-template <typename E>
+template <typename E, typename C>
 struct Team {
   Row<E> r;
   int id0, rank, size, turn, scan_turn, groups;
   Weights weight;
-  TeamShared& sh;
-  TeamWork& work;
+  SampleShared<C::kThreads>& sh;
+  TeamWork<C>& work;
 
   // Weights to 2^-34 as Weights::exact, but with the powers of 2^(1/1024): the
   // rest's series has three terms, and its one FP32 number is good to 2^-35.  A
@@ -973,13 +985,13 @@ struct Team {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Row<E> r = this->r;
     const int id0 = this->id0, groups = this->groups;
-    for (int g0 = warp; g0 < groups; g0 += kTeamU * kTeamWarps) {
+    for (int g0 = warp; g0 < groups; g0 += kTeamU * C::kWarps) {
       uint4 v[kTeamU];
 #pragma unroll
-      for (int u = 0; u < kTeamU; ++u) v[u] = r.vec()[min((g0 + u * kTeamWarps) * 32 + lane, r.nvec - 1)];
+      for (int u = 0; u < kTeamU; ++u) v[u] = r.vec()[min((g0 + u * C::kWarps) * 32 + lane, r.nvec - 1)];
 #pragma unroll
       for (int u = 0; u < kTeamU; ++u) {
-        const int g = g0 + u * kTeamWarps, i = g * 32 + lane;
+        const int g = g0 + u * C::kWarps, i = g * 32 + lane;
         if (g >= groups) break;
         if (i < r.nvec) {
           float x[N];
@@ -1019,10 +1031,10 @@ struct Team {
       each([&](float x, int) { m = fmaxf(m, x); });
     } else {
       uint32_t w = 0xFF80FF80u;
-      for (int i0 = threadIdx.x; i0 < r.nvec; i0 += kTeamU * kTeamThreads) {
+      for (int i0 = threadIdx.x; i0 < r.nvec; i0 += kTeamU * C::kThreads) {
         uint4 v[kTeamU];
 #pragma unroll
-        for (int u = 0; u < kTeamU; ++u) v[u] = r.vec()[min(i0 + u * kTeamThreads, r.nvec - 1)];
+        for (int u = 0; u < kTeamU; ++u) v[u] = r.vec()[min(i0 + u * C::kThreads, r.nvec - 1)];
 #pragma unroll
         for (int u = 0; u < kTeamU; ++u)
           w = max_nan_bf16x2(w, max_nan_bf16x2(max_nan_bf16x2(v[u].x, v[u].y), max_nan_bf16x2(v[u].z, v[u].w)));
@@ -1050,10 +1062,10 @@ struct Team {
     sums(f, [](const auto&, int, int) {});
   }
   __device__ __forceinline__ uint64_t scan(uint64_t v, uint64_t& total) {
-    return block_scan<kTeamThreads>(v, total, sh, scan_turn);
+    return block_scan<C::kThreads>(v, total, sh, scan_turn);
   }
   __device__ __forceinline__ void sync() const {
-    if (size == 1) {
+    if (C::kTeam == 1 || size == 1) {
       __syncthreads();
     } else {
       cluster_arrive();
@@ -1068,9 +1080,9 @@ struct Team {
     if (threadIdx.x == 0) box[0] = a, box[1] = b;
     sync();
     va = vb = 0;
-    if (size == 1) {
+    if (C::kTeam == 1 || size == 1) {
       if (lane == 0) va = box[0], vb = box[1];
-    } else if (lane < kTeam) {
+    } else if (lane < C::kTeam) {
       const uint32_t* p = reinterpret_cast<const uint32_t*>(box);
       va = cluster_load(p, lane) | (uint64_t)cluster_load(p + 1, lane) << 32;
       vb = cluster_load(p + 2, lane) | (uint64_t)cluster_load(p + 3, lane) << 32;
@@ -1081,7 +1093,7 @@ struct Team {
   __device__ __forceinline__ uint64_t total(uint64_t& mine, uint64_t& before) { return total(work.group, mine, before); }
   __device__ __forceinline__ uint64_t total(const uint64_t* group, uint64_t& mine, uint64_t& before) {
     uint64_t v = 0, all, none;
-    for (int g = threadIdx.x; g < groups + 2; g += kTeamThreads) v += group[g];
+    for (int g = threadIdx.x; g < groups + 2; g += C::kThreads) v += group[g];
     scan(v, mine);
     share(mine, 0, all, none);
     before = warp_sum64((int)(threadIdx.x & 31) < rank ? all : 0);
@@ -1097,7 +1109,7 @@ struct Team {
   __device__ __forceinline__ bool find(const uint64_t* group, uint64_t target, uint64_t mine, uint64_t before, F f) {
     if (target < before || target >= before + mine) return false;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = groups + 2;
-    const int each = (n + kTeamThreads - 1) / kTeamThreads, g0 = (int)threadIdx.x * each;
+    const int each = (n + C::kThreads - 1) / C::kThreads, g0 = (int)threadIdx.x * each;
     const uint64_t left = target - before;
     uint64_t sum = 0, all;
     for (int g = g0; g < min(g0 + each, n); ++g) sum += group[g];
@@ -1151,7 +1163,7 @@ struct Team {
     int at = (int)__shfl_sync(0xFFFFFFFFu, counts, 0);
     for (int q = 1; q < size; ++q) {
       const int n = (int)__shfl_sync(0xFFFFFFFFu, counts, q);
-      for (int j = threadIdx.x; j < n; j += kTeamThreads) {
+      for (int j = threadIdx.x; j < n; j += C::kThreads) {
         const uint32_t* p = reinterpret_cast<const uint32_t*>(&work.list[j]);
         work.list[at + j] = cluster_load(p, q) | (uint64_t)cluster_load(p + 1, q) << 32;
       }
@@ -1164,12 +1176,12 @@ struct Team {
   // if none does, or base alone.
   __device__ __forceinline__ void reach(int n, uint64_t base, uint64_t target) {
     const Exact exact = exact_weights();
-    sort_list<kTeamThreads>(work.list, n);
-    for (int j = threadIdx.x; j < n; j += kTeamThreads) work.weight[j] = exact(rank_logit(work.list[j]));
+    sort_list<C::kThreads>(work.list, n);
+    for (int j = threadIdx.x; j < n; j += C::kThreads) work.weight[j] = exact(rank_logit(work.list[j]));
     if (threadIdx.x == 0) work.key = work.incl = 0;
     __syncthreads();
-    sum_list<kTeamList, kTeamThreads>(work.weight, n, sh, scan_turn);
-    for (int j = threadIdx.x; j < n; j += kTeamThreads) {
+    sum_list<C::kList, C::kThreads>(work.weight, n, sh, scan_turn);
+    for (int j = threadIdx.x; j < n; j += C::kThreads) {
       const uint64_t before = base + (j ? work.weight[j - 1] : 0), upto = base + work.weight[j];
       if (before < target && target <= upto) work.key = work.list[j], work.incl = upto;
     }
@@ -1177,10 +1189,10 @@ struct Team {
   }
   __device__ __forceinline__ void list(float x, int id) {
     const uint32_t at = atomicAdd(&sh.listed, 1u);
-    if (at < (uint32_t)kTeamList) work.list[at] = rank_key(x, (uint32_t)id);
+    if (at < (uint32_t)C::kList) work.list[at] = rank_key(x, (uint32_t)id);
   }
   __device__ __forceinline__ void clear(bool both) {
-    for (int b = threadIdx.x; b < kTeamBins; b += kTeamThreads) {
+    for (int b = threadIdx.x; b < C::kBins; b += C::kThreads) {
       work.lo[b] = 0;
       if (both) work.hi[b] = 0;
     }
@@ -1191,7 +1203,7 @@ struct Team {
   // thread's bins, and the sum of all.  Barriers of the team.
   __device__ __forceinline__ uint64_t slice(bool both, uint64_t& sum) {
     sync();
-    const int each = kTeamBins / size / kTeamThreads, b0 = (rank * kTeamThreads + (int)threadIdx.x) * each;
+    const int each = C::kBins / size / C::kThreads, b0 = (rank * C::kThreads + (int)threadIdx.x) * each;
     uint64_t n = 0, mine, all, none;
     for (int i = 0; i < each; ++i) n += bin(b0 + i, both);
     uint64_t before = scan(n, mine);
@@ -1201,10 +1213,10 @@ struct Team {
     return before;
   }
   __device__ __forceinline__ uint64_t bin(int b, bool both) const {
-    if (size == 1) return work.lo[b] + (both ? (uint64_t)work.hi[b] << 32 : 0);
+    if (C::kTeam == 1 || size == 1) return work.lo[b] + (both ? (uint64_t)work.hi[b] << 32 : 0);
     uint64_t n = 0;
 #pragma unroll
-    for (int q = 0; q < kTeam; ++q) {
+    for (int q = 0; q < C::kTeam; ++q) {
       n += cluster_load(&work.lo[b], q);
       if (both) n += (uint64_t)cluster_load(&work.hi[b], q) << 32;
     }
@@ -1213,7 +1225,7 @@ struct Team {
   // The bin in which the sum over the bins, `before` in front of this thread's,
   // reaches target (1 .. the sum): true for its thread.
   __device__ __forceinline__ bool bin_at(uint64_t target, uint64_t before, bool both, int& b, uint64_t& at) const {
-    const int each = kTeamBins / size / kTeamThreads, b0 = (rank * kTeamThreads + (int)threadIdx.x) * each;
+    const int each = C::kBins / size / C::kThreads, b0 = (rank * C::kThreads + (int)threadIdx.x) * each;
     at = before;
     if (target <= at) return false;
     for (b = b0; b < b0 + each; ++b) {
@@ -1236,13 +1248,13 @@ struct Team {
     uint64_t base = 0, all, none;  // elements or weight before these distances
     for (int level = 0;; ++level) {
       int shift = 0;
-      while (((d1 - d0) >> shift) >= (uint32_t)kTeamBins) ++shift;
+      while (((d1 - d0) >> shift) >= (uint32_t)C::kBins) ++shift;
       clear(true);
       each([&](float x, int id) {
         const uint64_t key = rank_key(x, (uint32_t)id);
         const uint32_t d = top - (uint32_t)(key >> 32);
         if (x == neg_inf() || key < least || d < d0 || d > d1) return;
-        const int b = level == 0 ? first_bin(top, top - d) : (int)((d - d0) >> shift);
+        const int b = level == 0 ? first_bin<C>(top, top - d) : (int)((d - d0) >> shift);
         if (COUNT) {
           atomicAdd(&lo[b], 1u);
         } else {
@@ -1262,8 +1274,8 @@ struct Team {
       if (bin < 0) return false;
       base = warp_sum64(none);
       if (level == 0) {
-        d0 = first_bin_start(top, bin);
-        d1 = bin + 1 < kTeamBins ? first_bin_start(top, bin + 1) - 1 : 0xFFFFFFFFu;
+        d0 = first_bin_start<C>(top, bin);
+        d1 = bin + 1 < C::kBins ? first_bin_start<C>(top, bin + 1) - 1 : 0xFFFFFFFFu;
       } else {
         const uint32_t start = d0 + ((uint32_t)bin << shift), rest = d1 - start, width = (1u << shift) - 1;
         d0 = start;
@@ -1277,12 +1289,12 @@ struct Team {
       __syncthreads();
       share(sh.listed, 0, all, none);
       const uint64_t in = warp_sum64(all);
-      if (in <= (uint64_t)kTeamList) {  // the first block decides
+      if (in <= (uint64_t)C::kList) {  // the first block decides
         uint64_t key = 0, incl = 0;
         if (rank == 0) {
           gather(all);
           if (COUNT) {
-            sort_list<kTeamThreads>(work.list, (int)in);
+            sort_list<C::kThreads>(work.list, (int)in);
             key = work.list[target - base - 1];
           } else {
             reach((int)in, base, target);
@@ -1321,7 +1333,7 @@ struct Team {
     // Bins of the FP32 exponent, which never rises where the logit falls: equal
     // logits share a bin, and a bin's logits are above the next one's.
     auto bin_of = [](float t) {
-      return min((uint32_t)(__float_as_int(fmaf(t, -97.5f, 12582912.0f)) - 0x4B400000), (uint32_t)kTeamBins - 1);
+      return min((uint32_t)(__float_as_int(fmaf(t, -(C::kBins - 1) / 42.0f, 12582912.0f)) - 0x4B400000), (uint32_t)C::kBins - 1);
     };
     clear(false);
     each([&](float x, int) {
@@ -1365,16 +1377,16 @@ struct Team {
     scan(S, part);
     share(part, (uint64_t)listed, all, none);
     S = warp_sum64(all);
-    if (warp_sum64(none) > (uint64_t)kTeamList) return false;
+    if (warp_sum64(none) > (uint64_t)C::kList) return false;
     uint64_t mine, before;
     const uint64_t base = total(mine, before);
     const uint64_t target = max(1ull, (unsigned long long)part_of<true>(S, fmaxf(fl.top_p, 0.0f)));
     uint64_t key = 0, kept = 0;
     // the own list, before the first block mixes it with the others'
-    constexpr int PER = kTeamList / kTeamThreads;
+    constexpr int PER = C::kList / C::kThreads;
     uint64_t own[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) own[i] = (int)threadIdx.x + i * kTeamThreads < listed ? work.list[threadIdx.x + i * kTeamThreads] : 0;
+    for (int i = 0; i < PER; ++i) own[i] = (int)threadIdx.x + i * C::kThreads < listed ? work.list[threadIdx.x + i * C::kThreads] : 0;
     if (rank == 0) {
       __syncthreads();
       gather(none);
@@ -1406,7 +1418,7 @@ struct Team {
   // The 16 bits in the order of the values, by distance below the maximum's: 2048
   // values (sixteen powers of two), one bin for all down to -2^-10, 2046 values (16
   // powers of two) below that, and a bin for the rest.
-  static constexpr int kMid = kTeamNear, kLast = kTeamBins - 1;
+  static constexpr int kMid = C::kNear, kLast = C::kBins - 1;
   struct Bins {
     uint32_t top;      // rank of the maximum, in both halves
     int below;         // distance of a value below -2^-10, less its bin; 0 under a
@@ -1456,13 +1468,13 @@ struct Team {
       f(b);
       if (b == kMid || b == kLast) several(x, b);
     };
-    for (int g0 = warp; g0 < groups; g0 += kTeamU * kTeamWarps) {
+    for (int g0 = warp; g0 < groups; g0 += kTeamU * C::kWarps) {
       uint4 v[kTeamU];
 #pragma unroll
-      for (int u = 0; u < kTeamU; ++u) v[u] = r.vec()[min((g0 + u * kTeamWarps) * 32 + lane, r.nvec - 1)];
+      for (int u = 0; u < kTeamU; ++u) v[u] = r.vec()[min((g0 + u * C::kWarps) * 32 + lane, r.nvec - 1)];
 #pragma unroll
       for (int u = 0; u < kTeamU; ++u) {
-        const int g = g0 + u * kTeamWarps;
+        const int g = g0 + u * C::kWarps;
         if (g >= groups) break;
         if (g * 32 + lane < r.nvec) {
           const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
@@ -1500,7 +1512,7 @@ struct Team {
   // before it: shared with the team.  `before`: in front of this thread's bins.
   template <typename N>
   __device__ __forceinline__ int reach_bin(uint64_t target, uint64_t before, N n, uint64_t& at) {
-    const int each = kTeamBins / size / kTeamThreads, b0 = (rank * kTeamThreads + (int)threadIdx.x) * each;
+    const int each = C::kBins / size / C::kThreads, b0 = (rank * C::kThreads + (int)threadIdx.x) * each;
     if (threadIdx.x == 0) work.key = work.incl = 0;
     __syncthreads();
     for (int b = b0; b < b0 + each && before < target; ++b) {
@@ -1524,11 +1536,11 @@ struct Team {
     // 0 and -0, which are equal, and -inf lie in bins of several values but below
     // a maximum of less than 2^-95 or of the lowest values
     const uint32_t first_rank = bins.top & 0xFFFFu;
-    if (first_rank - 0x8000u < (uint32_t)kTeamBins || first_rank < 0x80u + kTeamBins) return false;
+    if (first_rank - 0x8000u < (uint32_t)C::kBins || first_rank < 0x80u + C::kBins) return false;
     uint64_t* table = work.table;
-    for (int b = threadIdx.x; b < kTeamBins; b += kTeamThreads)
+    for (int b = threadIdx.x; b < C::kBins; b += C::kThreads)
       table[b] = b == kMid || b == kLast ? 0 : exact(bins.value(b));
-    int last = kTeamBins;       // kept are the elements of the bins before `last`
+    int last = C::kBins;       // kept are the elements of the bins before `last`
     uint64_t take = 0, all, none;  // and the first `take` of it
     if (filtered) {
       uint32_t* lo = work.lo;
@@ -1547,7 +1559,7 @@ struct Team {
       scan(rest, b);
       share(a, b, all, none);
       mid = warp_sum64(all), rest = warp_sum64(none);
-      const int each = kTeamBins / size / kTeamThreads, b0 = (rank * kTeamThreads + (int)threadIdx.x) * each;
+      const int each = C::kBins / size / C::kThreads, b0 = (rank * C::kThreads + (int)threadIdx.x) * each;
       auto number = [&](int at) { return bin(at, false); };
       auto mass = [&](int at) { return at == kMid ? mid : at == kLast ? rest : table[at] * bin(at, false); };
       uint64_t n = 0, w = 0, mine_n, mine_w;
@@ -1583,10 +1595,10 @@ struct Team {
         last = found, take = (target - at + table[found] - 1) / table[found];
       }
       if (fl.min_p > 0.0f) {  // the first bin below the edge
-        if (threadIdx.x == 0) min_p_edge(fl, sh.edge), work.edge = kTeamBins;
+        if (threadIdx.x == 0) min_p_edge(fl, sh.edge), work.edge = C::kBins;
         __syncthreads();
         const uint32_t edge = (uint32_t)(min_p_key(weight.m, sh.edge) >> 32);
-        for (int k = threadIdx.x; k < kTeamBins; k += kTeamThreads)
+        for (int k = threadIdx.x; k < C::kBins; k += C::kThreads)
           if (k != kMid && k != kLast && rank_value(bins.value(k)) < edge) {
             atomicMin(&work.edge, k);
             break;
@@ -1595,7 +1607,7 @@ struct Team {
         const int first = work.edge;
         // among the values of the one bin, or those of the other where they count
         if (first < last || (first == last && take > 0)) {
-          if (first == kMid + 1 || (first == kTeamBins && rest)) return false;
+          if (first == kMid + 1 || (first == C::kBins && rest)) return false;
           last = first, take = 0;
         }
         __syncthreads();
@@ -1618,7 +1630,7 @@ struct Team {
     uint64_t mine, before, key = 0;
     if (take > 0) {
       total(work.ties, mine, before);
-      const int n = groups + 2, each = (n + kTeamThreads - 1) / kTeamThreads, g0 = (int)threadIdx.x * each;
+      const int n = groups + 2, each = (n + C::kThreads - 1) / C::kThreads, g0 = (int)threadIdx.x * each;
       uint64_t sum = 0, part;
       for (int g = g0; g < min(g0 + each, n); ++g) sum += work.ties[g];
       uint64_t at = scan(sum, part) + before;
@@ -1645,7 +1657,7 @@ struct Team {
     const bool filtered = fl.top_k > 0 || fl.top_p < 1.0f || fl.min_p > 0.0f;
     const Exact exact = exact_weights();
     bool owner;
-    if constexpr (sizeof(E) == 2) {
+    if constexpr (sizeof(E) == 2 && C::kValues) {
       if (draw_bf16(fl, V, out, owner)) return owner;
     }
     if (fl.top_k == 0 && fl.top_p < 1.0f && !(fl.min_p > 0.0f) && draw_top_p(fl, V, log_s, out, owner)) return owner;
@@ -1683,8 +1695,8 @@ struct Team {
 // Without branches, so that the weights of a vector are formed side by side: an
 // exponent out of range is held at -44, where only its own bits are used, and the
 // result dropped.
-template <typename E>
-__device__ __forceinline__ uint64_t Team<E>::Exact::operator()(float x) const {
+template <typename E, typename C>
+__device__ __forceinline__ uint64_t Team<E, C>::Exact::operator()(float x) const {
   const float d = x - m;
   const float p0 = __fmul_rn(d, ch), p = fmaxf(p0, -44.0f);
   const float b = d - x, lost = (x - (d - b)) + (-m - b);
@@ -1699,20 +1711,21 @@ __device__ __forceinline__ uint64_t Team<E>::Exact::operator()(float x) const {
 }
 
 // The powers of 2^(1/1024) for exact weights.
-__device__ __forceinline__ void load_powers(TeamShared& sh, TeamWork& work) {
+template <typename C>
+__device__ __forceinline__ void load_powers(SampleShared<C::kThreads>& sh, TeamWork<C>& work) {
   load_exp2(sh);
   __syncthreads();
   Weights one;  // 2^(j / 1024 - 1), of unit 2^-61
   one.m = 1024.0f, one.ch = 0x1p-10f, one.cl = 0.0f, one.s = 61, one.exp2 = sh.exp2;
-  for (int j = threadIdx.x; j < 1024; j += kTeamThreads) work.power[j] = one.exact((float)j) << 2;
+  for (int j = threadIdx.x; j < 1024; j += C::kThreads) work.power[j] = one.exact((float)j) << 2;
   __syncthreads();
 }
 
 // An open row's token by its team of `size` blocks.
-template <typename E>
+template <typename E, typename C>
 __device__ __forceinline__ void open_row(const SampleArgs& a, int64_t t, int flag, int rank, int size, int& turn,
-                                         int& scan_turn, TeamShared& sh, TeamWork& work) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = size == 1 ? 0 : kTeamLog;
+                                         int& scan_turn, SampleShared<C::kThreads>& sh, TeamWork<C>& work) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = size == 1 ? 0 : C::kTeamLog;
   const int log_s = kOpen - flag;
   const E* logits = static_cast<const E*>(a.logits) + t * a.ld;
   const Row<E> whole(logits, a.V);
@@ -1720,7 +1733,7 @@ __device__ __forceinline__ void open_row(const SampleArgs& a, int64_t t, int fla
   const int id0 = rank == 0 ? 0 : whole.head + v0 * Row<E>::kVec;
   const int id1 = rank == size - 1 ? a.V : whole.head + v1 * Row<E>::kVec;
   const Row<E> r(logits + id0, id1 - id0);
-  Team<E> team = {r, id0, rank, size, turn, scan_turn, (r.nvec + 31) / 32, Weights(), sh, work};
+  Team<E, C> team = {r, id0, rank, size, turn, scan_turn, (r.nvec + 31) / 32, Weights(), sh, work};
   bool params;
   const Filters fl = filters_of(a, t, params);
   // the row's maximum, a number
@@ -1728,7 +1741,7 @@ __device__ __forceinline__ void open_row(const SampleArgs& a, int64_t t, int fla
   uint32_t top = __reduce_max_sync(0xFFFFFFFFu, rank_value(high));
   if (lane == 0) sh.scan[0][warp] = top;
   __syncthreads();
-  top = __reduce_max_sync(0xFFFFFFFFu, lane < kTeamWarps ? (uint32_t)sh.scan[0][lane] : 0u);
+  top = __reduce_max_sync(0xFFFFFFFFu, lane < C::kWarps ? (uint32_t)sh.scan[0][lane] : 0u);
   __syncthreads();
   uint64_t all, none;
   team.share(top, 0, all, none);
@@ -1749,22 +1762,23 @@ __device__ __forceinline__ void open_row(const SampleArgs& a, int64_t t, int fla
 // that a block's threads have; the first block ends the row, and if it stays open
 // all eight decide it at once.
 template <typename E>
-__global__ void __launch_bounds__(kTeamThreads, 1) sample_few_kernel(SampleArgs a) {
-  constexpr int TH = kTeamThreads;
-  static_assert(kTeam == kSaRuns, "a run per block");
+__global__ void __launch_bounds__(LongTeam::kThreads, 1) sample_few_kernel(SampleArgs a) {
+  using C = LongTeam;
+  constexpr int TH = C::kThreads;
+  static_assert(C::kTeam == kSaRuns, "a run per block");
   extern __shared__ uint4 smem[];
   FewWork& few = *reinterpret_cast<FewWork*>(smem);
-  TeamWork& work = few.team;
-  TeamShared& sh = few.sh;
-  const int rank = (int)blockIdx.x % kTeam;
-  const int64_t clusters = gridDim.x / kTeam;
+  TeamWork<C>& work = few.team;
+  SampleShared<C::kThreads>& sh = few.sh;
+  const int rank = (int)blockIdx.x % C::kTeam;
+  const int64_t clusters = gridDim.x / C::kTeam;
   float *highs = few.highs + threadIdx.x, *sums = few.sums + threadIdx.x;
   int turn = 0, team_turn = 0;
   load_exp2(sh);
   cluster_arrive();  // all blocks run: their shared memory may be written
   cluster_wait();
   begin_kernel();
-  for (int64_t t = blockIdx.x / kTeam; t < a.T; t += clusters) {
+  for (int64_t t = blockIdx.x / C::kTeam; t < a.T; t += clusters) {
     const SampleRow<E, TH> row(static_cast<const E*>(a.logits) + t * a.ld, a.V, highs);
     bool params;
     const Filters fl = filters_of(a, t, params);
@@ -1793,13 +1807,13 @@ __global__ void __launch_bounds__(kTeamThreads, 1) sample_few_kernel(SampleArgs 
       row.front([&](float x, int) { m = max_nan(m, x); });
       row.back([&](float x, int) { m = max_nan(m, x); });
       const int open = end_row<E, TH>(a, t, row, fl, params, weight, m, highs, sums, sh, few.work, turn);
-      if (threadIdx.x < kTeam) cluster_store(&few.open, threadIdx.x, (uint32_t)open);
+      if (threadIdx.x < C::kTeam) cluster_store(&few.open, threadIdx.x, (uint32_t)open);
     }
     cluster_arrive();
     cluster_wait();
     if (few.open) {
       load_powers(sh, work);
-      open_row<E>(a, t, (int)few.open, rank, kTeam, team_turn, turn, sh, work);
+      open_row<E, C>(a, t, (int)few.open, rank, C::kTeam, team_turn, turn, sh, work);
     }
     cluster_arrive();  // the first block's maxima and sums are read no more
     cluster_wait();
@@ -1810,15 +1824,16 @@ __device__ __forceinline__ bool is_open(int token) { return token <= kOpen && to
 
 // The next open row from place `seen` on of the rows taken in turn from `start`
 // on, or -1; taken by marking its token, so that no other block has it.
-__device__ __noinline__ int64_t claim(const SampleArgs& a, int64_t start, int64_t& seen, int& flag, TeamWork& work) {
+template <typename C>
+__device__ __noinline__ int64_t claim(const SampleArgs& a, int64_t start, int64_t& seen, int& flag, TeamWork<C>& work) {
   while (seen < a.T) {
     const int64_t place = seen + threadIdx.x;
     int64_t t = place + start;
     if (t >= a.T) t -= a.T;
     const int token = place < a.T ? __ldcg(&a.tokens[t]) : 0;
-    if (threadIdx.x == 0) work.first = kTeamThreads;
+    if (threadIdx.x == 0) work.first = C::kThreads;
     if (!__syncthreads_or(is_open(token))) {
-      seen += kTeamThreads;
+      seen += C::kThreads;
       continue;
     }
     if (is_open(token)) atomicMin(&work.first, (int)threadIdx.x);
@@ -1837,12 +1852,13 @@ __device__ __noinline__ int64_t claim(const SampleArgs& a, int64_t start, int64_
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(SampleArgs a) {
+  using C = LongTeam;
   extern __shared__ uint4 smem[];
-  TeamWork& work = *reinterpret_cast<TeamWork*>(smem);
-  TeamShared& sh = *reinterpret_cast<TeamShared*>(&work + 1);
-  const int rank_in_cluster = (int)blockIdx.x % kTeam;
-  const int64_t teams = gridDim.x / kTeam, cluster = blockIdx.x / kTeam;
+  TeamWork<C>& work = *reinterpret_cast<TeamWork<C>*>(smem);
+  SampleShared<C::kThreads>& sh = *reinterpret_cast<SampleShared<C::kThreads>*>(&work + 1);
+  const int rank_in_cluster = (int)blockIdx.x % C::kTeam;
+  const int64_t teams = gridDim.x / C::kTeam, cluster = blockIdx.x / C::kTeam;
   bool ready = false;
   int turn = 0, scan_turn = 0;
   cluster_arrive();  // all blocks run: their shared memory may be written
@@ -1854,19 +1870,19 @@ __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs
   int64_t from = 0;
   int rows = 0;
   if (rank_in_cluster == 0)
-    for (; from < a.T && rows <= 2 * teams; from += kTeamThreads) {
+    for (; from < a.T && rows <= 2 * teams; from += C::kThreads) {
       const int64_t t = from + threadIdx.x;
       rows += __syncthreads_count(t < a.T && is_open(__ldcg(&a.tokens[t])));
     }
-  if (rank_in_cluster == 0 && threadIdx.x < kTeam) cluster_store(&work.claim, threadIdx.x, (uint32_t)rows);
+  if (rank_in_cluster == 0 && threadIdx.x < C::kTeam) cluster_store(&work.claim, threadIdx.x, (uint32_t)rows);
   cluster_arrive();
   cluster_wait();
   rows = (int)work.claim;
   if (rows == 0) return;
-  const bool alone = rows > 2 * teams && a.V / Row<E>::kVec <= kTeamGroups * 32;
-  const int size = alone ? 1 : kTeam, rank = alone ? 0 : rank_in_cluster;
+  const bool alone = rows > 2 * teams && a.V / Row<E>::kVec <= C::kGroups * 32;
+  const int size = alone ? 1 : C::kTeam, rank = alone ? 0 : rank_in_cluster;
   // The search for a row begins at a place of the block's or cluster's own.
-  const int64_t start = a.T * (alone ? (int64_t)blockIdx.x : cluster * kTeam) / gridDim.x;
+  const int64_t start = a.T * (alone ? (int64_t)blockIdx.x : cluster * C::kTeam) / gridDim.x;
   int64_t seen = 0;
   for (;;) {
     int64_t t = -1;
@@ -1888,8 +1904,26 @@ __global__ void __launch_bounds__(kTeamThreads, 2) sample_open_kernel(SampleArgs
       ready = true;
     }
     {
-      open_row<E>(a, t, flag, rank, size, turn, scan_turn, sh, work);
+      open_row<E, C>(a, t, flag, rank, size, turn, scan_turn, sh, work);
     }
+  }
+}
+
+// The same for short rows, a block each.
+template <typename E>
+__global__ void __launch_bounds__(ShortTeam::kThreads, 8) sample_open_short_kernel(SampleArgs a) {
+  using C = ShortTeam;
+  extern __shared__ uint4 smem[];
+  TeamWork<C>& work = *reinterpret_cast<TeamWork<C>*>(smem);
+  SampleShared<C::kThreads>& sh = *reinterpret_cast<SampleShared<C::kThreads>*>(&work + 1);
+  bool ready = false;
+  int turn = 0, scan_turn = 0, flag = 0;
+  begin_kernel();
+  const int64_t start = (int64_t)a.T * blockIdx.x / gridDim.x;
+  int64_t seen = 0;
+  for (int64_t t; (t = claim(a, start, seen, flag, work)) >= 0;) {
+    if (!ready) load_powers(sh, work), ready = true;
+    open_row<E, C>(a, t, flag, 0, 1, turn, scan_turn, sh, work);
   }
 }
 
@@ -1901,20 +1935,28 @@ static int launch_sample(const SampleArgs& a, cudaStream_t s) {
   return launch_kernel(f, (unsigned)(a.T < most ? a.T : most), TH, kSaSmem<TH>, 1, s, a);
 }
 int launch_sample_tokens(const SampleArgs& a, cudaStream_t s) {
-  if (a.T <= gemm_num_ctas() / kTeam) {
-    auto f = a.dtype == MOE_DTYPE_BF16 ? sample_few_kernel<uint16_t> : sample_few_kernel<float>;
+  const bool bf = a.dtype == MOE_DTYPE_BF16;
+  const int sms = gemm_num_ctas();
+  if (a.T <= sms / LongTeam::kTeam) {
+    auto f = bf ? sample_few_kernel<uint16_t> : sample_few_kernel<float>;
     if (!allow_smem((const void*)f, (int)sizeof(FewWork), (int)sizeof(FewWork))) return -1;
-    return launch_kernel(f, (unsigned)(a.T * kTeam), kTeamThreads, sizeof(FewWork), kTeam, s, a);
+    return launch_kernel(f, (unsigned)(a.T * LongTeam::kTeam), LongTeam::kThreads, sizeof(FewWork), LongTeam::kTeam, s, a);
   }
-  // Two blocks of 512 threads per SM while each row has one at once; else four of
-  // 256, whose ends the others cover.
-  const int rc = a.T <= 2 * gemm_num_ctas() ? launch_sample<512>(a, s) : launch_sample<256>(a, s);
+  const int rc = a.T <= 2 * sms ? launch_sample<512>(a, s) : launch_sample<256>(a, s);
   if (rc != 0) return rc;
-  constexpr int smem = (int)(sizeof(TeamWork) + sizeof(TeamShared));
-  auto f = a.dtype == MOE_DTYPE_BF16 ? sample_open_kernel<uint16_t> : sample_open_kernel<float>;
+  if (a.V <= kShortV) {
+    using C = ShortTeam;
+    constexpr int smem = (int)(sizeof(TeamWork<C>) + sizeof(SampleShared<C::kThreads>));
+    auto f = bf ? sample_open_short_kernel<uint16_t> : sample_open_short_kernel<float>;
+    if (!allow_smem((const void*)f, smem, smem)) return -1;
+    return launch_kernel(f, (unsigned)(a.T < 8 * sms ? a.T : 8 * sms), C::kThreads, smem, 1, s, a);
+  }
+  using C = LongTeam;
+  constexpr int smem = (int)(sizeof(TeamWork<C>) + sizeof(SampleShared<C::kThreads>));
+  auto f = bf ? sample_open_kernel<uint16_t> : sample_open_kernel<float>;
   if (!allow_smem((const void*)f, smem, smem)) return -1;
-  const int teams = 2 * gemm_num_ctas() / kTeam;
-  return launch_kernel(f, (unsigned)((a.T < teams ? a.T : teams) * kTeam), kTeamThreads, smem, kTeam, s, a);
+  const int teams = 2 * sms / C::kTeam;
+  return launch_kernel(f, (unsigned)((a.T < teams ? a.T : teams) * C::kTeam), C::kThreads, smem, C::kTeam, s, a);
 }
 
 }  // namespace moe
