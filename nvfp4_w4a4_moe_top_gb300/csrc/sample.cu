@@ -57,7 +57,7 @@ __device__ __forceinline__ uint64_t fixed(float w, int s) {
 template <int TH>
 struct SampleShared {
   static constexpr int NW = TH / 32;
-  static constexpr int kList = TH < 256 ? 512 : 1536;  // weighed elements: top_k of 1000 among them
+  static constexpr int kList = TH < 256 ? 1024 : 1536;  // weighed elements: top_k of 1000 among them
   uint64_t exp2[64];               // 2^(j/64) 2^62
   uint64_t part[kSaRuns + 2][NW];  // sums of the runs by warp; the row's ends
   uint64_t sums[kSaRuns + 2];      // of all warps
@@ -73,7 +73,7 @@ struct SampleShared {
 // What shares its memory with the ring that the logits come through.
 template <int TH>
 struct SampleWork {
-  static constexpr int kHot = TH * kSaRuns, kListed = TH < 256 ? 512 : 2048;
+  static constexpr int kHot = TH * kSaRuns, kListed = TH < 256 ? 1024 : 2048;
   uint64_t list[kListed], weight[SampleShared<TH>::kList];
   union {
     struct {
@@ -88,6 +88,10 @@ constexpr int kSaRing = TH * kSaU * kSaD * 16;
 template <int TH>
 constexpr int kSaSmem = (kSaRing<TH> > (int)sizeof(SampleWork<TH>) ? kSaRing<TH> : (int)sizeof(SampleWork<TH>)) +
                         TH * kSaRuns * 8 + (int)sizeof(SampleShared<TH>);
+
+// Blocks of an SM, as many as its shared memory holds.
+template <int TH>
+constexpr int kSaBlocks = TH == 128 ? 6 : 1024 / TH;
 
 __device__ __forceinline__ void add64(uint32_t* lo, uint32_t* hi, uint64_t v) {
   const uint32_t l = (uint32_t)v, was = atomicAdd(lo, l);
@@ -646,7 +650,8 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
     if (by_count && fl.top_p < 1.0f) skip = 0;  // all of the top_k count for top_p
     if (threadIdx.x == 0) sh.found = 0, sh.listed = 0, sh.hot = 0;
     bool few = true;
-    if (by_count || by_mass) {
+    // by all elements where the maxima are fewer than top_k
+    for (bool whole = false; by_count || by_mass; whole = true) {
       for (int b = threadIdx.x; b < kSaNear; b += TH) work.lo[b] = 0, work.hi[b] = 0;
       __syncthreads();
       auto offer = [&](float x, uint64_t w) {
@@ -655,7 +660,9 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
         if (by_count) atomicAdd(&work.lo[d >> 17], 1u);
         else add64(&work.lo[d >> 17], &work.hi[d >> 17], w);
       };
-      if (by_count && fl.top_k <= TH / 4) {
+      if (whole) {
+        row.all(0, [&](float x, int) { offer(x, 0); });
+      } else if (by_count && fl.top_k <= TH / 4) {
         offer(own, 0);
       } else if (by_count) {
         for (int q = 0; q < row.runs; ++q) offer(highs[q * TH], 0);
@@ -691,10 +698,11 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
       __syncthreads();
       // (work.lo is read no more: the list of runs shares its memory)
       if (sh.found) skip = max(skip, top - min(top, ((uint32_t)(sh.bin + 1) << 17) - 1));
+      else if (by_count && !whole && fl.top_k <= kList) continue;
       else few = skip > 0;  // min_p's bound alone
-    } else {
-      __syncthreads();
+      break;
     }
+    __syncthreads();
     // ---- the elements from there on, if they are few ----
     if (few) {
       auto offer = [&](float x, int id) {
@@ -831,7 +839,7 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
 }
 
 template <typename E, int TH>
-__global__ void __launch_bounds__(TH, 1024 / TH) sample_tokens_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(TH, kSaBlocks<TH>) sample_tokens_kernel(SampleArgs a) {
   extern __shared__ uint4 smem[];
   uint4* ring = smem;
   SampleWork<TH>& work = *reinterpret_cast<SampleWork<TH>*>(smem);
@@ -1822,25 +1830,36 @@ __global__ void __launch_bounds__(LongTeam::kThreads, 1) sample_few_kernel(Sampl
 
 __device__ __forceinline__ bool is_open(int token) { return token <= kOpen && token > kClaimed; }
 
-// The next open row from place `seen` on of the rows taken in turn from `start`
-// on, or -1; taken by marking its token, so that no other block has it.
+// The next open row from place `seen` to `end` of the rows taken in turn from
+// `start` on, or -1; taken by marking its token, so that no other block has it.
 template <typename C>
-__device__ __noinline__ int64_t claim(const SampleArgs& a, int64_t start, int64_t& seen, int& flag, TeamWork<C>& work) {
-  while (seen < a.T) {
-    const int64_t place = seen + threadIdx.x;
-    int64_t t = place + start;
-    if (t >= a.T) t -= a.T;
-    const int token = place < a.T ? __ldcg(&a.tokens[t]) : 0;
-    if (threadIdx.x == 0) work.first = C::kThreads;
-    if (!__syncthreads_or(is_open(token))) {
-      seen += C::kThreads;
+__device__ __noinline__ int64_t claim(const SampleArgs& a, int64_t start, int64_t& seen, int64_t end, int& flag,
+                                      TeamWork<C>& work) {
+  constexpr int kEach = 4;
+  while (seen < end) {
+    int token[kEach], mine = kEach;
+    auto row = [&](int i) {
+      const int64_t t = seen + i * C::kThreads + threadIdx.x + start;
+      return t >= a.T ? t - a.T : t;
+    };
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) token[i] = seen + i * C::kThreads + threadIdx.x < end ? __ldcg(&a.tokens[row(i)]) : 0;
+#pragma unroll
+    for (int i = kEach - 1; i >= 0; --i)
+      if (is_open(token[i])) mine = i;
+    if (threadIdx.x == 0) work.first = kEach * C::kThreads;
+    if (!__syncthreads_or(mine < kEach)) {
+      seen += kEach * C::kThreads;
       continue;
     }
-    if (is_open(token)) atomicMin(&work.first, (int)threadIdx.x);
+    const int place = mine * C::kThreads + (int)threadIdx.x;
+    if (mine < kEach) atomicMin(&work.first, place);
     __syncthreads();
-    if ((int)threadIdx.x == work.first) {
-      work.claimed = atomicCAS(&a.tokens[t], token, kClaimed) == token ? t : -1;
-      work.flag = token;
+    if (place == work.first) {
+      const int64_t t = row(mine);
+      const int was = mine == 0 ? token[0] : mine == 1 ? token[1] : mine == 2 ? token[2] : token[3];
+      work.claimed = atomicCAS(&a.tokens[t], was, kClaimed) == was ? t : -1;
+      work.flag = was;
     }
     __syncthreads();
     const int64_t got = work.claimed;
@@ -1849,6 +1868,12 @@ __device__ __noinline__ int64_t claim(const SampleArgs& a, int64_t start, int64_
     if (got >= 0) return got;
   }
   return -1;
+}
+// How far a block that works alone looks: past its own share of the rows, so that
+// it has work where others have much, but not at all rows.
+__device__ __forceinline__ int64_t claim_window(int T, int blocks) {
+  const int64_t share = ((int64_t)T + blocks - 1) / blocks;
+  return min((long long)T, max(4ll * share, 4096ll));
 }
 
 template <typename E>
@@ -1870,9 +1895,18 @@ __global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(Samp
   int64_t from = 0;
   int rows = 0;
   if (rank_in_cluster == 0)
-    for (; from < a.T && rows <= 2 * teams; from += C::kThreads) {
-      const int64_t t = from + threadIdx.x;
-      rows += __syncthreads_count(t < a.T && is_open(__ldcg(&a.tokens[t])));
+    for (; from < a.T && rows <= 2 * teams; from += 8 * C::kThreads) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t t = from + i * C::kThreads + threadIdx.x;
+        n += t < a.T && is_open(__ldcg(&a.tokens[t]));
+      }
+      n = __reduce_add_sync(0xFFFFFFFFu, n);
+      if ((threadIdx.x & 31) == 0) sh.scan[0][threadIdx.x >> 5] = n;
+      __syncthreads();
+      for (int w = 0; w < C::kWarps; ++w) rows += (int)sh.scan[0][w];
+      __syncthreads();
     }
   if (rank_in_cluster == 0 && threadIdx.x < C::kTeam) cluster_store(&work.claim, threadIdx.x, (uint32_t)rows);
   cluster_arrive();
@@ -1883,11 +1917,12 @@ __global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(Samp
   const int size = alone ? 1 : C::kTeam, rank = alone ? 0 : rank_in_cluster;
   // The search for a row begins at a place of the block's or cluster's own.
   const int64_t start = a.T * (alone ? (int64_t)blockIdx.x : cluster * C::kTeam) / gridDim.x;
+  const int64_t end = alone ? claim_window(a.T, gridDim.x) : a.T;
   int64_t seen = 0;
   for (;;) {
     int64_t t = -1;
     int flag = 0;
-    if (rank == 0) t = claim(a, start, seen, flag, work);
+    if (rank == 0) t = claim(a, start, seen, end, flag, work);
     if (!alone) {  // the first block tells the others
       if (threadIdx.x == 0) work.row = t, work.claim = (uint32_t)flag;
       cluster_arrive();
@@ -1920,8 +1955,9 @@ __global__ void __launch_bounds__(ShortTeam::kThreads, 8) sample_open_short_kern
   int turn = 0, scan_turn = 0, flag = 0;
   begin_kernel();
   const int64_t start = (int64_t)a.T * blockIdx.x / gridDim.x;
+  const int64_t end = claim_window(a.T, gridDim.x);
   int64_t seen = 0;
-  for (int64_t t; (t = claim(a, start, seen, flag, work)) >= 0;) {
+  for (int64_t t; (t = claim(a, start, seen, end, flag, work)) >= 0;) {
     if (!ready) load_powers(sh, work), ready = true;
     open_row<E, C>(a, t, flag, 0, 1, turn, scan_turn, sh, work);
   }
@@ -1929,7 +1965,7 @@ __global__ void __launch_bounds__(ShortTeam::kThreads, 8) sample_open_short_kern
 
 template <int TH>
 static int launch_sample(const SampleArgs& a, cudaStream_t s) {
-  const int64_t most = (int64_t)gemm_num_ctas() * (1024 / TH) * 8;
+  const int64_t most = (int64_t)gemm_num_ctas() * kSaBlocks<TH> * 8;
   auto f = a.dtype == MOE_DTYPE_BF16 ? sample_tokens_kernel<uint16_t, TH> : sample_tokens_kernel<float, TH>;
   if (!allow_smem((const void*)f, kSaSmem<TH>, kSaSmem<TH>)) return -1;
   return launch_kernel(f, (unsigned)(a.T < most ? a.T : most), TH, kSaSmem<TH>, 1, s, a);
@@ -1942,7 +1978,16 @@ int launch_sample_tokens(const SampleArgs& a, cudaStream_t s) {
     if (!allow_smem((const void*)f, (int)sizeof(FewWork), (int)sizeof(FewWork))) return -1;
     return launch_kernel(f, (unsigned)(a.T * LongTeam::kTeam), LongTeam::kThreads, sizeof(FewWork), LongTeam::kTeam, s, a);
   }
-  const int rc = a.T <= 2 * sms ? launch_sample<512>(a, s) : launch_sample<256>(a, s);
+  // Threads per row.  What a row's end costs is barriers and dependent loads, so
+  // many rows are done by small blocks, whose ends the others cover; 512 threads
+  // where all rows have such a block at once (no filter, BF16, one in six rows flat:
+  // 512 x 131072 44 us with 256 threads, 51 with 512, 304 x 131072 30 and 27; 12000 x
+  // 12000 177 with 128, 238 with 256; 3000 x 32768 96 and 105; 2048 x 131072 117 with
+  // 256, 133 with 128).
+  const int64_t nvec = (int64_t)a.V * (bf ? 2 : 4) / 16;
+  const int rc = nvec <= 1024 || (nvec <= 4096 && a.T > 2 * sms) ? launch_sample<128>(a, s)
+                 : a.T <= 2 * sms                                ? launch_sample<512>(a, s)
+                                                                 : launch_sample<256>(a, s);
   if (rc != 0) return rc;
   if (a.V <= kShortV) {
     using C = ShortTeam;
