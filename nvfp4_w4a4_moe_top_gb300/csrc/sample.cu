@@ -926,9 +926,9 @@ struct TeamWork {
   uint64_t ties[C::kGroups + 2];
   uint32_t lo[C::kBins], hi[C::kBins];
   uint64_t box[2][2];               // what the blocks tell one another, in turn
-  int64_t row, claimed;             // a row that a block takes
-  uint32_t claim;
+  int64_t claimed;                  // a row that a block takes
   int flag, first;
+  uint32_t row[4];                  // the cluster's: number, flag, whether it is the only one; open rows
   uint64_t base, key, incl;
   int edge;
 };
@@ -1884,7 +1884,6 @@ __global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(Samp
   SampleShared<C::kThreads>& sh = *reinterpret_cast<SampleShared<C::kThreads>*>(&work + 1);
   const int rank_in_cluster = (int)blockIdx.x % C::kTeam;
   const int64_t teams = gridDim.x / C::kTeam, cluster = blockIdx.x / C::kTeam;
-  bool ready = false;
   int turn = 0, scan_turn = 0;
   cluster_arrive();  // all blocks run: their shared memory may be written
   cluster_wait();
@@ -1908,40 +1907,53 @@ __global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(Samp
       for (int w = 0; w < C::kWarps; ++w) rows += (int)sh.scan[0][w];
       __syncthreads();
     }
-  if (rank_in_cluster == 0 && threadIdx.x < C::kTeam) cluster_store(&work.claim, threadIdx.x, (uint32_t)rows);
+  if (rank_in_cluster == 0 && threadIdx.x < C::kTeam) cluster_store(&work.row[3], threadIdx.x, (uint32_t)rows);
   cluster_arrive();
   cluster_wait();
-  rows = (int)work.claim;
+  rows = (int)work.row[3];
   if (rows == 0) return;
+  // The first block takes a row and tells the others: a barrier per row.  A cluster
+  // that counts no more open rows than there are clusters takes one only, where all
+  // blocks look through all rows.  None is left over: the cluster that counted first
+  // counted all, before any was taken, and goes on until there are none if they were
+  // more; if they were not, a cluster that took none has seen all of them taken.
   const bool alone = rows > 2 * teams && a.V / Row<E>::kVec <= C::kGroups * 32;
-  const int size = alone ? 1 : C::kTeam, rank = alone ? 0 : rank_in_cluster;
-  // The search for a row begins at a place of the block's or cluster's own.
-  const int64_t start = a.T * (alone ? (int64_t)blockIdx.x : cluster * C::kTeam) / gridDim.x;
-  const int64_t end = alone ? claim_window(a.T, gridDim.x) : a.T;
-  int64_t seen = 0;
-  for (;;) {
-    int64_t t = -1;
-    int flag = 0;
-    if (rank == 0) t = claim(a, start, seen, end, flag, work);
-    if (!alone) {  // the first block tells the others
-      if (threadIdx.x == 0) work.row = t, work.claim = (uint32_t)flag;
-      cluster_arrive();
-      cluster_wait();
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(&work.row);
-      t = (int64_t)(cluster_load(p, 0) | (uint64_t)cluster_load(p + 1, 0) << 32);
-      flag = (int)cluster_load(&work.claim, 0);
-      cluster_arrive();
-      cluster_wait();
+  const bool one = rows <= teams && claim_window(a.T, gridDim.x) == a.T;
+  const int64_t start = (int64_t)a.T * (cluster * C::kTeam) / gridDim.x;
+  int64_t seen = 0, t = -1;
+  int flag = 0;
+  auto next = [&]() {  // the cluster's next row
+    if (rank_in_cluster == 0) {
+      t = claim(a, start, seen, a.T, flag, work);
+      if (threadIdx.x < C::kTeam) {
+        cluster_store(&work.row[0], threadIdx.x, (uint32_t)t);
+        cluster_store(&work.row[1], threadIdx.x, (uint32_t)flag);
+        cluster_store(&work.row[2], threadIdx.x, one ? 1u : 0u);
+      }
     }
-    if (t < 0) break;
-    if (!ready) {
-      load_powers(sh, work);
-      ready = true;
+    cluster_arrive();
+    cluster_wait();
+    t = (int)work.row[0], flag = (int)work.row[1];
+  };
+  if (alone) {  // every block for itself
+    const int64_t own = (int64_t)a.T * blockIdx.x / gridDim.x, end = claim_window(a.T, gridDim.x);
+    seen = 0;
+    for (bool ready = false; (t = claim(a, own, seen, end, flag, work)) >= 0;) {
+      if (!ready) load_powers(sh, work), ready = true;
+      open_row<E, C>(a, t, flag, 0, 1, turn, scan_turn, sh, work);
     }
-    {
-      open_row<E, C>(a, t, flag, rank, size, turn, scan_turn, sh, work);
-    }
+    return;
   }
+  for (bool ready = false;; ready = true) {
+    next();
+    if (t < 0) break;
+    if (!ready) load_powers(sh, work);
+    const bool last = work.row[2] != 0;
+    open_row<E, C>(a, t, flag, rank_in_cluster, C::kTeam, turn, scan_turn, sh, work);
+    if (last) break;
+  }
+  cluster_arrive();  // no block ends while another reads its shared memory
+  cluster_wait();
 }
 
 // The same for short rows, a block each.
