@@ -16,8 +16,8 @@
  * results deterministic bit for bit.  Host threads may call them at the same
  * time.  16-bit tensors, tables and gradients are 16-byte aligned, logits by
  * their element, int32 and float vectors 4-byte aligned.  Strides are in
- * elements; rows times a stride stay below 2^46.  T = 0 does nothing (but see
- * moe_embed_tokens_backward).
+ * elements; rows times a stride stay below 2^46.  No output overlaps an input or
+ * another output.  T = 0 does nothing (but see moe_embed_tokens_backward).
  */
 #ifndef MOE_TOKENS_H
 #define MOE_TOKENS_H

@@ -2,6 +2,10 @@
 //   out_t = scale table[ids_t];   dtable_v = scale sum_{t: ids_t = v} dy_t.
 // Both are bound by HBM: the rows that tokens name in and one row per token
 // out; one row per token in and every row of the table out.
+//   65536 tokens, d = 2048, V = 131072: embedding 62.5 us, 0.86 of the measured
+//   copy rate; gradient 232 us in five launches, 0.85 (counting 5, two passes of
+//   the sort 16 and 10, sums and zeros 193, joining 14, each by itself).
+//   512 tokens, d = 1024, V = 32768: gradient 23 us in one launch, 0.87.
 #include "tokens.cuh"
 
 namespace moe {
@@ -9,7 +13,8 @@ namespace moe {
 constexpr int kEmThreads = 256;
 
 // Vectors of 8 values: TX threads along a row (a power of two), 256 / TX rows
-// at a time, kEmRows rows per thread, their loads issued together.
+// at a time, kEmRows rows per thread, their loads issued together, as each waits
+// for its id first.
 constexpr int kEmRows = 4;
 
 __device__ __forceinline__ uint4 scaled8(const uint16_t* p, float scale) {
@@ -71,6 +76,10 @@ int launch_embed_tokens(const EmbedArgs& a, cudaStream_t s) {
 // summed run by run.  A run inside one tile goes to the table at once; the parts of
 // a run that crosses tiles go to the workspace and are added in the order of the
 // tiles by a last launch.  Ids out of range sort behind all others, as V.
+//
+// One launch looks through all ids in every block, the sort has five launches: with
+// V = 131072 and d = 2048, 300 tokens 146 us and 155, 1000 tokens 159 and 158, 2000
+// tokens 210 and 161; with V = 4096 and d = 512, 1000 tokens 8 and 19.
 constexpr int kFewTokens = 1024;
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -91,6 +100,9 @@ static SortPlan sort_plan(int T, int V, int d) {
   while ((int64_t(1) << n) <= V) ++n;  // ids up to V
   p.passes = (n + kMaxBits - 1) / kMaxBits;
   p.bits = (n + p.passes - 1) / p.passes;
+  // Up to 64 chunks, as every chunk reads the counts of all.  Tiles as long as leave
+  // 1024 of them for the columns of a block, up to 64: a run's parts are then few
+  // (32 tokens and 2048 tiles: 65536 x 2048 244 us, 236 so; 16003 x 1000 68 and 62).
   p.items = 1;
   while (p.items < 32 && (int64_t)p.items * kSortThreads * 64 < T) p.items *= 2;
   const int chunk = p.items * kSortThreads;
@@ -225,7 +237,8 @@ __global__ void __launch_bounds__(kSortThreads)
   }
 }
 
-// Eight values, as one store where the address allows it.
+// Eight values, as one store where the address allows it: with two stores of half
+// a sector each the 65536 x 2048 gradient took 296 us, 236 so.
 __device__ __forceinline__ void store8(float* p, const float4& lo, const float4& hi) {
   if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
     asm volatile("st.global.cs.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(lo.x), "f"(lo.y), "f"(lo.z),
@@ -393,10 +406,11 @@ __global__ void __launch_bounds__(kEmThreads) embed_join_kernel(SumArgs s) {
   }
 }
 
-// Few tokens.  Blocks 0 .. T * parts - 1: a token and 256 columns; the block of
-// the id's first occurrence lists all of them in order, its eight warps sum a
-// consecutive eighth each, and the eighths are added in turn.  The rest: zeros
-// into the rows that no token names, `zero_rows` of them per block.
+// Few tokens: no sort, as each block can look through all ids (512 tokens, d =
+// 1024, V = 32768: 23 us, sorted 37).  Blocks 0 .. T * parts - 1: a token and 256
+// columns; the block of the id's first occurrence lists all of them in order, its
+// eight warps sum a consecutive eighth each, and the eighths are added in turn.  The
+// rest: zeros into the rows that no token names, `zero_rows` of them per block.
 __global__ void __launch_bounds__(kEmThreads) embed_few_kernel(EmbedBwdArgs a, int parts, int zero_rows) {
   constexpr int kIds = kFewTokens / kEmThreads, kZeroWords = 8;
   __shared__ int list[kFewTokens];

@@ -9,11 +9,24 @@
 // are the same in any order: threads and atomics add them as they come, and the
 // result is one.
 //
-// There are two kinds of weights.  Weights from FP32 exponentials make sums with
-// a bounded relative error (sum_error); a row with a decision that is nearer to
-// its border than that, and a row that keeps too many elements for a list, is left
-// to a second launch, in which eight blocks together decide it with weights to
-// about 2^-34.
+// A token is one or another, so a decision is only taken where it is certain.
+// Weights from FP32 exponentials make sums with a bounded relative error
+// (sum_error).  A row with a decision that is nearer to its border than that, and a
+// row that keeps too many elements for a list, stays open and is decided by
+// weights to 2^-34, whose own error is below what 64-bit floating-point sums of so
+// many elements show.  How often: rows of 131072 ids without filters, one in 200
+// where the weight lies in a few ids, one in six where it lies in 40000.
+//
+//   sample_tokens_kernel  rows by a block each; marks open rows in tokens
+//   sample_open_kernel    the open rows, by eight blocks each or one
+//   sample_open_short_kernel  the same for up to kShortV ids
+//   sample_few_kernel     all of it for few rows, a cluster per row
+//
+// Times (BF16, 131072 ids, us; HBM's floor 79 for 2048 rows, 20 for 512): 2048 rows
+// whose weight lies in few ids 117 without filters, 129 with top-k 50, 110 with
+// min-p; 2048 rows of which one in seven is flat, with top-p 0.95, 277 (130 and 120
+// for the two launches); 512 rows without filters 35, and 40 for the second launch
+// where it has a row to decide, 3 where it has none; 2 rows with top-p 12.
 #include "exp_table.cuh"
 #include "tokens.cuh"
 
@@ -530,9 +543,15 @@ __device__ __forceinline__ void put_drawn(const SampleArgs& a, int64_t t, const 
   if (a.kept_logprob) a.kept_logprob[t] = z - log1pf((float)((int64_t)d.kept - one) * unit);
 }
 
-// The end of a row, from its runs' maxima and sums: the token and its numbers
-// written, 0; or what marks the row as open.  own: this thread's maximum; highs,
-// sums: its runs', TH apart.
+// The end of a row, from its runs' maxima and sums.  Without filters the runs' sums
+// give the run with the token, which is read again (from L2).  With filters the
+// maxima bound what is kept from below: at least top_k of them, or maxima with
+// top_p of the weight, reach a value, so only runs whose maximum reaches it are read
+// again, and what they hold from there on is listed, sorted, and weighed exactly;
+// only the row's sum, which top_p alone needs, is then of FP32 weights.  The
+// barriers and dependent reads of all this take 5 to 10 us, which other blocks'
+// reads cover.  Returns 0 with the token and its numbers written, or what marks the
+// row as open.  own: this thread's maximum; highs, sums: its runs', TH apart.
 template <typename E, int TH>
 __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const SampleRow<E, TH>& row, const Filters& fl,
                                        bool params, Weights weight, float own, const float* highs, const float* sums,
@@ -838,6 +857,14 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
   return done ? 0 : open;
 }
 
+// A row per block at a time.  The logits come through a ring of asynchronous copies
+// per thread (64 KB on the way per SM); each thread keeps maximum and sum of up to
+// eight runs of its vectors, so that nothing of the row but these needs to stay.
+// HBM's share: 2048 x 131072 with min-p 110 us, 0.72 of the measured copy rate; what
+// is missing are the ends of rows (a launch of 1216 rows issues in 57% of its slots,
+// 80 instructions per vector of 8).  Two and three times the bytes on the way, runs
+// of other lengths, and the end of a row as a function of its own (its call takes
+// registers from the pass) were slower.
 template <typename E, int TH>
 __global__ void __launch_bounds__(TH, kSaBlocks<TH>) sample_tokens_kernel(SampleArgs a) {
   extern __shared__ uint4 smem[];
@@ -1423,6 +1450,10 @@ struct Team {
   }
 
   // ---- BF16: a bin per value ----
+  // One histogram of whole numbers then gives every filter's end with exact
+  // weights, and a table of 4096 weights replaces their evaluation per element
+  // (2048 open rows of 131072 with top-p 1012 us, 1222 without this; 512 without
+  // filters 120 and 155).
   // The 16 bits in the order of the values, by distance below the maximum's: 2048
   // values (sixteen powers of two), one bin for all down to -2^-10, 2046 values (16
   // powers of two) below that, and a bin for the rest.
@@ -1876,6 +1907,12 @@ __device__ __forceinline__ int64_t claim_window(int T, int blocks) {
   return min((long long)T, max(4ll * share, 4096ll));
 }
 
+// Open rows, taken by marking their tokens.  Few are decided by eight blocks each,
+// one after the other within a cluster; their time is the chain of the cluster's
+// barriers (a launch for one row with top-p 48 us, half of the stalls at barriers).
+// Many are decided by one block each, two per SM, bound by instructions (52 per
+// element: 2048 open rows of 131072 BF16 ids with top-p 1012 us, 512 289).  With
+// nothing open the launch costs 3 us behind the first.
 template <typename E>
 __global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(SampleArgs a) {
   using C = LongTeam;
