@@ -37,8 +37,13 @@ constexpr int kSaD = 2;     // groups of them on the way
 constexpr int kSaRuns = 8;  // runs of a thread at most
 constexpr int kSaNear = 1024;  // bins of the sixteen powers of two below the maximum
 constexpr float kMinExponent = -42.0f;  // weights below 2^-42 count as 0
-// In tokens: left to the second launch, kOpen - ceil(log2(the row's weight)).
+// In tokens: left to the second launch, kOpen - (ceil(log2(the row's weight)) + 64
+// times the bits of its maximum, if they are 16).
 constexpr int kOpen = -2;
+template <typename E>
+__device__ __forceinline__ int open_flag(int log_s, float m) {
+  return kOpen - (log_s + (sizeof(E) == 2 ? (int)(__float_as_uint(m) >> 16) * 64 : 0));
+}
 
 // In parts of 27 bits, 32 of which add up in a word.
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
@@ -655,7 +660,7 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
                    : (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 2, filtered ? 0 : row.per * Row<E>::kVec + 5));
     err += (uint64_t)a.V << (weight.s - 42);  // weights below 2^-42, which the pass adds
   }
-  const int open = kOpen - (64 - __clzll((long long)out.total) - weight.s);
+  const int open = open_flag<E>(64 - __clzll((long long)out.total) - weight.s, m);
   bool done = false;
   if (!filtered) {
     err += weight_err;  // of the run with the token
@@ -955,7 +960,8 @@ struct TeamWork {
   uint64_t box[2][2];               // what the blocks tell one another, in turn
   int64_t claimed;                  // a row that a block takes
   int flag, first;
-  uint32_t row[4];                  // the cluster's: number, flag, whether it is the only one; open rows
+  uint32_t row[2], first_row[2];    // the cluster's next row and its first one: number, flag
+  uint32_t rows;                    // open rows that it counted
   uint64_t base, key, incl;
   int edge;
 };
@@ -1764,8 +1770,9 @@ __device__ __forceinline__ void load_powers(SampleShared<C::kThreads>& sh, TeamW
 template <typename E, typename C>
 __device__ __forceinline__ void open_row(const SampleArgs& a, int64_t t, int flag, int rank, int size, int& turn,
                                          int& scan_turn, SampleShared<C::kThreads>& sh, TeamWork<C>& work) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = size == 1 ? 0 : C::kTeamLog;
-  const int log_s = kOpen - flag;
+  [[maybe_unused]] const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lg = size == 1 ? 0 : C::kTeamLog;
+  const int log_s = (kOpen - flag) & 63;
   const E* logits = static_cast<const E*>(a.logits) + t * a.ld;
   const Row<E> whole(logits, a.V);
   const int v0 = whole.part(rank, lg), v1 = whole.part(rank + 1, lg);
@@ -1776,15 +1783,20 @@ __device__ __forceinline__ void open_row(const SampleArgs& a, int64_t t, int fla
   bool params;
   const Filters fl = filters_of(a, t, params);
   // the row's maximum, a number
-  const float high = team.high();
-  uint32_t top = __reduce_max_sync(0xFFFFFFFFu, rank_value(high));
-  if (lane == 0) sh.scan[0][warp] = top;
-  __syncthreads();
-  top = __reduce_max_sync(0xFFFFFFFFu, lane < C::kWarps ? (uint32_t)sh.scan[0][lane] : 0u);
-  __syncthreads();
-  uint64_t all, none;
-  team.share(top, 0, all, none);
-  top = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)all);
+  uint32_t top;
+  if constexpr (sizeof(E) == 2) {
+    top = rank_value(__uint_as_float((uint32_t)((kOpen - flag) >> 6) << 16));
+  } else {
+    const float high = team.high();
+    top = __reduce_max_sync(0xFFFFFFFFu, rank_value(high));
+    if (lane == 0) sh.scan[0][warp] = top;
+    __syncthreads();
+    top = __reduce_max_sync(0xFFFFFFFFu, lane < C::kWarps ? (uint32_t)sh.scan[0][lane] : 0u);
+    __syncthreads();
+    uint64_t all, none;
+    team.share(top, 0, all, none);
+    top = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)all);
+  }
   team.weight = weights_of(fl.inv_t, rank_logit((uint64_t)top << 32), a.V, sh.exp2);
   team.weight.s = min(52, 62 - log_s);  // as fine as the row's own sum allows
   Drawn out;
@@ -1800,8 +1812,8 @@ __device__ __forceinline__ void open_row(const SampleArgs& a, int64_t t, int fla
 // Few rows: a cluster of eight blocks per row, each of which reads one of the runs
 // that a block's threads have; the first block ends the row, and if it stays open
 // all eight decide it at once.
-template <typename E>
-__global__ void __launch_bounds__(LongTeam::kThreads, 1) sample_few_kernel(SampleArgs a) {
+template <typename E, int BLOCKS>
+__global__ void __launch_bounds__(LongTeam::kThreads, BLOCKS) sample_few_kernel(SampleArgs a) {
   using C = LongTeam;
   constexpr int TH = C::kThreads;
   static_assert(C::kTeam == kSaRuns, "a run per block");
@@ -1923,49 +1935,74 @@ __global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(Samp
   const int64_t teams = gridDim.x / C::kTeam, cluster = blockIdx.x / C::kTeam;
   int turn = 0, scan_turn = 0;
   cluster_arrive();  // all blocks run: their shared memory may be written
+  load_powers(sh, work);
   cluster_wait();
   begin_kernel();
   // Alone where there are more open rows than two per team, and where a block's
   // groups have room for a row.  The count may be short of rows that others have
   // taken; any mode is right.
+  const int64_t start = (int64_t)a.T * (cluster * C::kTeam) / gridDim.x;
+  const bool room = a.V / Row<E>::kVec <= C::kGroups * 32;
   int64_t from = 0;
   int rows = 0;
-  if (rank_in_cluster == 0)
+  if (rank_in_cluster == 0) {
+    // and the first of them from `start` on, by its distance
+    uint32_t near = 0xFFFFFFFFu, first = near;
+    int was = 0;
     for (; from < a.T && rows <= 2 * teams; from += 8 * C::kThreads) {
-      int n = 0;
+      uint32_t n = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t t = from + i * C::kThreads + threadIdx.x;
-        n += t < a.T && is_open(__ldcg(&a.tokens[t]));
+        const int token = t < a.T ? __ldcg(&a.tokens[t]) : 0;
+        if (!is_open(token)) continue;
+        const uint32_t d = (uint32_t)(t >= start ? t - start : t - start + a.T);
+        ++n;
+        if (d < near) near = d, was = token;
       }
       n = __reduce_add_sync(0xFFFFFFFFu, n);
-      if ((threadIdx.x & 31) == 0) sh.scan[0][threadIdx.x >> 5] = n;
+      const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, near);
+      if ((threadIdx.x & 31) == 0) sh.scan[0][threadIdx.x >> 5] = (uint64_t)least << 32 | n;
       __syncthreads();
-      for (int w = 0; w < C::kWarps; ++w) rows += (int)sh.scan[0][w];
+      for (int w = 0; w < C::kWarps; ++w) {
+        rows += (int)(uint32_t)sh.scan[0][w];
+        first = min(first, (uint32_t)(sh.scan[0][w] >> 32));
+      }
       __syncthreads();
     }
-  if (rank_in_cluster == 0 && threadIdx.x < C::kTeam) cluster_store(&work.row[3], threadIdx.x, (uint32_t)rows);
+    if (rows > 0 ? near == first : threadIdx.x == 0) {
+      int64_t t = -1;
+      if (rows > 0 && !(rows > 2 * teams && room)) {
+        t = start + first;
+        if (t >= a.T) t -= a.T;
+        if (atomicCAS(&a.tokens[t], was, kClaimed) != was) t = -1;
+      }
+      for (int q = 0; q < C::kTeam; ++q) {
+        cluster_store(&work.first_row[0], q, (uint32_t)t);
+        cluster_store(&work.first_row[1], q, (uint32_t)was);
+        cluster_store(&work.rows, q, (uint32_t)rows);
+      }
+    }
+  }
   cluster_arrive();
   cluster_wait();
-  rows = (int)work.row[3];
+  rows = (int)work.rows;
   if (rows == 0) return;
   // The first block takes a row and tells the others: a barrier per row.  A cluster
   // that counts no more open rows than there are clusters takes one only, where all
   // blocks look through all rows.  None is left over: the cluster that counted first
   // counted all, before any was taken, and goes on until there are none if they were
   // more; if they were not, a cluster that took none has seen all of them taken.
-  const bool alone = rows > 2 * teams && a.V / Row<E>::kVec <= C::kGroups * 32;
+  const bool alone = rows > 2 * teams && room;
   const bool one = rows <= teams && claim_window(a.T, gridDim.x) == a.T;
-  const int64_t start = (int64_t)a.T * (cluster * C::kTeam) / gridDim.x;
-  int64_t seen = 0, t = -1;
-  int flag = 0;
+  int64_t seen = 0, t = (int)work.first_row[0];
+  int flag = (int)work.first_row[1];
   auto next = [&]() {  // the cluster's next row
     if (rank_in_cluster == 0) {
       t = claim(a, start, seen, a.T, flag, work);
       if (threadIdx.x < C::kTeam) {
         cluster_store(&work.row[0], threadIdx.x, (uint32_t)t);
         cluster_store(&work.row[1], threadIdx.x, (uint32_t)flag);
-        cluster_store(&work.row[2], threadIdx.x, one ? 1u : 0u);
       }
     }
     cluster_arrive();
@@ -1975,19 +2012,16 @@ __global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(Samp
   if (alone) {  // every block for itself
     const int64_t own = (int64_t)a.T * blockIdx.x / gridDim.x, end = claim_window(a.T, gridDim.x);
     seen = 0;
-    for (bool ready = false; (t = claim(a, own, seen, end, flag, work)) >= 0;) {
-      if (!ready) load_powers(sh, work), ready = true;
+    while ((t = claim(a, own, seen, end, flag, work)) >= 0)
       open_row<E, C>(a, t, flag, 0, 1, turn, scan_turn, sh, work);
-    }
     return;
   }
-  for (bool ready = false;; ready = true) {
-    next();
+  for (;;) {
+    if (t < 0) next();
     if (t < 0) break;
-    if (!ready) load_powers(sh, work);
-    const bool last = work.row[2] != 0;
     open_row<E, C>(a, t, flag, rank_in_cluster, C::kTeam, turn, scan_turn, sh, work);
-    if (last) break;
+    if (one) break;
+    t = -1;
   }
   cluster_arrive();  // no block ends while another reads its shared memory
   cluster_wait();
@@ -2012,6 +2046,48 @@ __global__ void __launch_bounds__(ShortTeam::kThreads, 8) sample_open_short_kern
   }
 }
 
+// Clusters of eight blocks of kernel F that run at once on the current device, which
+// is less than its blocks would suggest (a cluster lies within a part of the chip: of
+// 152 SMs' 19 with one block per SM 15, of 38 with two 36); the answer is kept per
+// host thread.
+template <auto F>
+static int clusters_at_once(int threads, int smem) {
+  thread_local int cached_dev = -1, cached = 0;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev == cached_dev) return cached;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(8);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 8;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (!allow_smem((const void*)F, smem, smem) || cudaOccupancyMaxActiveClusters(&n, F, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  cached_dev = dev, cached = n;
+  return n;
+}
+
+// 1 where the rows are too many.
+template <typename E>
+static int launch_few(const SampleArgs& a, cudaStream_t s) {
+  constexpr int smem = (int)sizeof(FewWork);
+  auto f = sample_few_kernel<E, 1>;
+  if (a.T > clusters_at_once<sample_few_kernel<E, 1>>(LongTeam::kThreads, smem)) {
+    if (a.T >= clusters_at_once<sample_few_kernel<E, 2>>(LongTeam::kThreads, smem)) return 1;
+    f = sample_few_kernel<E, 2>;
+  }
+  if (!allow_smem((const void*)f, smem, smem)) return -1;
+  return launch_kernel(f, (unsigned)(a.T * LongTeam::kTeam), LongTeam::kThreads, smem, LongTeam::kTeam, s, a);
+}
+
 template <int TH>
 static int launch_sample(const SampleArgs& a, cudaStream_t s) {
   const int64_t most = (int64_t)gemm_num_ctas() * kSaBlocks<TH> * 8;
@@ -2022,11 +2098,13 @@ static int launch_sample(const SampleArgs& a, cudaStream_t s) {
 int launch_sample_tokens(const SampleArgs& a, cudaStream_t s) {
   const bool bf = a.dtype == MOE_DTYPE_BF16;
   const int sms = gemm_num_ctas();
-  if (a.T <= sms / LongTeam::kTeam) {
-    auto f = bf ? sample_few_kernel<uint16_t> : sample_few_kernel<float>;
-    if (!allow_smem((const void*)f, (int)sizeof(FewWork), (int)sizeof(FewWork))) return -1;
-    return launch_kernel(f, (unsigned)(a.T * LongTeam::kTeam), LongTeam::kThreads, sizeof(FewWork), LongTeam::kTeam, s, a);
-  }
+  // A cluster per row where all run at once, one block per SM, or, up to one row
+  // less, two, whose registers are half as many (2 x 131072 with top-p 15.1 us
+  // instead of 13.1; 32 rows 17.7 and, in two launches, 21.7; all of them flat 65 and
+  // 78; as many rows as clusters, 36: 21.4 and 20.5).
+  static_assert(LongTeam::kTeam == 8, "as clusters_at_once has it");
+  const int few = bf ? launch_few<uint16_t>(a, s) : launch_few<float>(a, s);
+  if (few <= 0) return few;
   // Threads per row.  What a row's end costs is barriers and dependent loads, so
   // many rows are done by small blocks, whose ends the others cover; 512 threads
   // where all rows have such a block at once (no filter, BF16, one in six rows flat:
@@ -2049,7 +2127,9 @@ int launch_sample_tokens(const SampleArgs& a, cudaStream_t s) {
   constexpr int smem = (int)(sizeof(TeamWork<C>) + sizeof(SampleShared<C::kThreads>));
   auto f = bf ? sample_open_kernel<uint16_t> : sample_open_kernel<float>;
   if (!allow_smem((const void*)f, smem, smem)) return -1;
-  const int teams = 2 * sms / C::kTeam;
+  const int n = bf ? clusters_at_once<sample_open_kernel<uint16_t>>(C::kThreads, smem)
+                   : clusters_at_once<sample_open_kernel<float>>(C::kThreads, smem);
+  const int teams = n > 0 ? n : 1;
   return launch_kernel(f, (unsigned)((a.T < teams ? a.T : teams) * C::kTeam), C::kThreads, smem, C::kTeam, s, a);
 }
 
