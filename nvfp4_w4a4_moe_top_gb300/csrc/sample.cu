@@ -1935,7 +1935,6 @@ __global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(Samp
   const int64_t teams = gridDim.x / C::kTeam, cluster = blockIdx.x / C::kTeam;
   int turn = 0, scan_turn = 0;
   cluster_arrive();  // all blocks run: their shared memory may be written
-  load_powers(sh, work);
   cluster_wait();
   begin_kernel();
   // Alone where there are more open rows than two per team, and where a block's
@@ -1943,51 +1942,59 @@ __global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(Samp
   // taken; any mode is right.
   const int64_t start = (int64_t)a.T * (cluster * C::kTeam) / gridDim.x;
   const bool room = a.V / Row<E>::kVec <= C::kGroups * 32;
-  int64_t from = 0;
   int rows = 0;
   if (rank_in_cluster == 0) {
-    // and the first of them from `start` on, by its distance
-    uint32_t near = 0xFFFFFFFFu, first = near;
-    int was = 0;
-    for (; from < a.T && rows <= 2 * teams; from += 8 * C::kThreads) {
-      uint32_t n = 0;
+    constexpr int kEach = 8, kBatch = kEach * C::kThreads;
+    int token[kEach];
+    int64_t from = 0;
+    for (; from < a.T && rows <= 2 * teams; from += kBatch) {
+      int n = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kEach; ++i) {
         const int64_t t = from + i * C::kThreads + threadIdx.x;
-        const int token = t < a.T ? __ldcg(&a.tokens[t]) : 0;
-        if (!is_open(token)) continue;
-        const uint32_t d = (uint32_t)(t >= start ? t - start : t - start + a.T);
-        ++n;
-        if (d < near) near = d, was = token;
+        token[i] = t < a.T ? __ldcg(&a.tokens[t]) : 0;
+        n += is_open(token[i]);
       }
       n = __reduce_add_sync(0xFFFFFFFFu, n);
+      if ((threadIdx.x & 31) == 0) sh.scan[0][threadIdx.x >> 5] = n;
+      __syncthreads();
+      for (int w = 0; w < C::kWarps; ++w) rows += (int)sh.scan[0][w];
+      __syncthreads();
+    }
+    // not alone: the first open row of the last tokens read, from `start` on
+    if (rows > 0 && !(rows > 2 * teams && room)) {
+      uint32_t near = 0xFFFFFFFFu;
+      int was = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int64_t t = from - kBatch + i * C::kThreads + threadIdx.x;
+        const uint32_t d = (uint32_t)(t >= start ? t - start : t - start + a.T);
+        if (is_open(token[i]) && d < near) near = d, was = token[i];
+      }
       const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, near);
-      if ((threadIdx.x & 31) == 0) sh.scan[0][threadIdx.x >> 5] = (uint64_t)least << 32 | n;
+      if ((threadIdx.x & 31) == 0) sh.scan[0][threadIdx.x >> 5] = least;
+      if (threadIdx.x == 0) work.claimed = -1;
       __syncthreads();
-      for (int w = 0; w < C::kWarps; ++w) {
-        rows += (int)(uint32_t)sh.scan[0][w];
-        first = min(first, (uint32_t)(sh.scan[0][w] >> 32));
-      }
-      __syncthreads();
-    }
-    if (rows > 0 ? near == first : threadIdx.x == 0) {
-      int64_t t = -1;
-      if (rows > 0 && !(rows > 2 * teams && room)) {
-        t = start + first;
+      const uint32_t first =
+          __reduce_min_sync(0xFFFFFFFFu, (uint32_t)sh.scan[0][(threadIdx.x & 31) % C::kWarps]);
+      if (near == first && is_open(was)) {
+        int64_t t = start + first;
         if (t >= a.T) t -= a.T;
-        if (atomicCAS(&a.tokens[t], was, kClaimed) != was) t = -1;
+        if (atomicCAS(&a.tokens[t], was, kClaimed) == was) work.claimed = t, work.flag = was;
       }
-      for (int q = 0; q < C::kTeam; ++q) {
-        cluster_store(&work.first_row[0], q, (uint32_t)t);
-        cluster_store(&work.first_row[1], q, (uint32_t)was);
-        cluster_store(&work.rows, q, (uint32_t)rows);
+      __syncthreads();
+      if (threadIdx.x < C::kTeam) {
+        cluster_store(&work.first_row[0], threadIdx.x, (uint32_t)work.claimed);
+        cluster_store(&work.first_row[1], threadIdx.x, (uint32_t)work.flag);
       }
     }
+    if (threadIdx.x < C::kTeam) cluster_store(&work.rows, threadIdx.x, (uint32_t)rows);
   }
   cluster_arrive();
   cluster_wait();
   rows = (int)work.rows;
   if (rows == 0) return;
+  load_powers(sh, work);
   // The first block takes a row and tells the others: a barrier per row.  A cluster
   // that counts no more open rows than there are clusters takes one only, where all
   // blocks look through all rows.  None is left over: the cluster that counted first
@@ -2092,16 +2099,22 @@ template <int TH>
 static int launch_sample(const SampleArgs& a, cudaStream_t s) {
   const int64_t most = (int64_t)gemm_num_ctas() * kSaBlocks<TH> * 8;
   auto f = a.dtype == MOE_DTYPE_BF16 ? sample_tokens_kernel<uint16_t, TH> : sample_tokens_kernel<float, TH>;
-  if (!allow_smem((const void*)f, kSaSmem<TH>, kSaSmem<TH>)) return -1;
-  return launch_kernel(f, (unsigned)(a.T < most ? a.T : most), TH, kSaSmem<TH>, 1, s, a);
+  // Where there is an SM for each row, shared memory for no second block: blocks of
+  // a launch that is set up early would otherwise lie two in an SM (152 x 131072 with
+  // min-p 19.5 us, 22.8 without).
+  constexpr int kAlone = 120 * 1024;
+  static_assert(TH != 512 || kSaSmem<TH> <= kAlone, "a block's own share");
+  const int smem = TH == 512 && a.T <= gemm_num_ctas() ? kAlone : kSaSmem<TH>;
+  if (!allow_smem((const void*)f, smem, TH == 512 ? kAlone : kSaSmem<TH>)) return -1;
+  return launch_kernel(f, (unsigned)(a.T < most ? a.T : most), TH, smem, 1, s, a);
 }
 int launch_sample_tokens(const SampleArgs& a, cudaStream_t s) {
   const bool bf = a.dtype == MOE_DTYPE_BF16;
   const int sms = gemm_num_ctas();
   // A cluster per row where all run at once, one block per SM, or, up to one row
   // less, two, whose registers are half as many (2 x 131072 with top-p 15.1 us
-  // instead of 13.1; 32 rows 17.7 and, in two launches, 21.7; all of them flat 65 and
-  // 78; as many rows as clusters, 36: 21.4 and 20.5).
+  // instead of 13.1; 16 rows 16.6 and, in two launches, 18; 32 flat rows 64 and 78; as
+  // many rows as clusters, 36: 21.4 and 18.1).
   static_assert(LongTeam::kTeam == 8, "as clusters_at_once has it");
   const int few = bf ? launch_few<uint16_t>(a, s) : launch_few<float>(a, s);
   if (few <= 0) return few;
@@ -2127,9 +2140,11 @@ int launch_sample_tokens(const SampleArgs& a, cudaStream_t s) {
   constexpr int smem = (int)(sizeof(TeamWork<C>) + sizeof(SampleShared<C::kThreads>));
   auto f = bf ? sample_open_kernel<uint16_t> : sample_open_kernel<float>;
   if (!allow_smem((const void*)f, smem, smem)) return -1;
+  // Not all that run at once: the last ones find their places late (nothing open, 152
+  // rows, 1 us less with 32 clusters than with 36).
   const int n = bf ? clusters_at_once<sample_open_kernel<uint16_t>>(C::kThreads, smem)
                    : clusters_at_once<sample_open_kernel<float>>(C::kThreads, smem);
-  const int teams = n > 0 ? n : 1;
+  const int teams = n > 1 ? n - n / 8 : 1;
   return launch_kernel(f, (unsigned)((a.T < teams ? a.T : teams) * C::kTeam), C::kThreads, smem, C::kTeam, s, a);
 }
 
