@@ -23,9 +23,9 @@
 //   sample_few_kernel     all of it for few rows, a cluster per row
 //
 // Times (BF16, 131072 ids, us; HBM's floor 79 for 2048 rows, 20 for 512): 2048 rows
-// whose weight lies in few ids 117 without filters, 129 with top-k 50, 110 with
-// min-p; 2048 rows of which one in seven is flat, with top-p 0.95, 277 (130 and 120
-// for the two launches); 512 rows without filters 35, and 40 for the second launch
+// whose weight lies in few ids 113 without filters, 125 with top-k 50, 107 with
+// min-p; 2048 rows of which one in ten stays open, with top-p 0.95, 274 (150 and 120
+// for the two launches); 512 rows without filters 35, and 37 for the second launch
 // where it has a row to decide, 3 where it has none; 2 rows with top-p 12.
 #include "exp_table.cuh"
 #include "tokens.cuh"
@@ -865,10 +865,10 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
 // A row per block at a time.  The logits come through a ring of asynchronous copies
 // per thread (64 KB on the way per SM); each thread keeps maximum and sum of up to
 // eight runs of its vectors, so that nothing of the row but these needs to stay.
-// HBM's share: 2048 x 131072 with min-p 110 us, 0.72 of the measured copy rate; what
+// HBM's share: 2048 x 131072 with min-p 107 us, 0.74 of the measured copy rate; what
 // is missing are the ends of rows (a launch of 1216 rows issues in 57% of its slots,
 // 80 instructions per vector of 8).  Two and three times the bytes on the way, runs
-// of other lengths, and the end of a row as a function of its own (its call takes
+// of other lengths, a prefetch of the row that comes next into L2, and the end of a row as a function of its own (its call takes
 // registers from the pass) were slower.
 template <typename E, int TH>
 __global__ void __launch_bounds__(TH, kSaBlocks<TH>) sample_tokens_kernel(SampleArgs a) {
@@ -1921,9 +1921,9 @@ __device__ __forceinline__ int64_t claim_window(int T, int blocks) {
 
 // Open rows, taken by marking their tokens.  Few are decided by eight blocks each,
 // one after the other within a cluster; their time is the chain of the cluster's
-// barriers (a launch for one row with top-p 48 us, half of the stalls at barriers).
+// barriers (a launch for one row with top-p some 45 us, half of the stalls at barriers).
 // Many are decided by one block each, two per SM, bound by instructions (52 per
-// element: 2048 open rows of 131072 BF16 ids with top-p 1012 us, 512 289).  With
+// element: 2048 open rows of 131072 BF16 ids with top-p 973 us).  With
 // nothing open the launch costs 3 us behind the first.
 template <typename E>
 __global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(SampleArgs a) {
