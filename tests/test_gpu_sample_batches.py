@@ -59,3 +59,37 @@ def test_open_rows_far_apart(at, dtype):
     peaked = np.setdiff1d(np.arange(T), at)
     assert np.array_equal(tokens[peaked], z[peaked].argmax(1))
     check(z[at], dtype, *(a[at] for a in args))
+
+
+FIRST = """
+import torch
+import nvfp4_w4a4_moe_top_gb300 as M
+g = torch.Generator(device="cuda").manual_seed(3)
+calls = []
+for T in [3, 20, 60, 400]:
+    z = (torch.randn((T, 9001), generator=g, device="cuda") * 2).bfloat16()
+    u = torch.rand(T, generator=g, device="cuda")
+    p = torch.full((T,), 0.9, device="cuda")
+    calls.append((z, u, p, torch.full((T,), -7, dtype=torch.int32, device="cuda")))
+torch.cuda.synchronize()
+graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(graph, stream=s):
+    for z, u, p, tokens in calls:
+        M.moe_sample_tokens(z, u, tokens, top_p=p)
+graph.replay()
+torch.cuda.synchronize()
+for z, u, p, tokens in calls:
+    again = torch.empty_like(tokens)
+    M.moe_sample_tokens(z, u, again, top_p=p)
+    assert torch.equal(again, tokens) and (tokens >= 0).all()
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture():
+    """What a call asks the device for the first time, it may ask while a graph is captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr
