@@ -26,7 +26,7 @@
 // whose weight lies in few ids 113 without filters, 125 with top-k 50, 107 with
 // min-p; 2048 rows of which one in ten stays open, with top-p 0.95, 274 (150 and 120
 // for the two launches); 512 rows without filters 35, and 37 for the second launch
-// where it has a row to decide, 3 where it has none; 2 rows with top-p 12.
+// where it has a row to decide, 3 where it has none; 2 rows with top-p 11.
 #include "exp_table.cuh"
 #include "tokens.cuh"
 
@@ -1822,53 +1822,51 @@ __global__ void __launch_bounds__(LongTeam::kThreads, BLOCKS) sample_few_kernel(
   TeamWork<C>& work = few.team;
   SampleShared<C::kThreads>& sh = few.sh;
   const int rank = (int)blockIdx.x % C::kTeam;
-  const int64_t clusters = gridDim.x / C::kTeam;
+  const int64_t t = blockIdx.x / C::kTeam;
   float *highs = few.highs + threadIdx.x, *sums = few.sums + threadIdx.x;
   int turn = 0, team_turn = 0;
   load_exp2(sh);
   cluster_arrive();  // all blocks run: their shared memory may be written
   cluster_wait();
   begin_kernel();
-  for (int64_t t = blockIdx.x / C::kTeam; t < a.T; t += clusters) {
-    const SampleRow<E, TH> row(static_cast<const E*>(a.logits) + t * a.ld, a.V, highs);
-    bool params;
-    const Filters fl = filters_of(a, t, params);
-    const Weights weight = weights_of(fl.inv_t, 0.0f, a.V, sh.exp2);
-    if (rank < row.runs) {
-      RunSum acc;
-      for (int j = 0; j < row.per; j += kSaU) {
-        const int i0 = (rank * row.per + j) * TH + (int)threadIdx.x;
-        uint4 v[kSaU];
+  const SampleRow<E, TH> row(static_cast<const E*>(a.logits) + t * a.ld, a.V, highs);
+  bool params;
+  const Filters fl = filters_of(a, t, params);
+  const Weights weight = weights_of(fl.inv_t, 0.0f, a.V, sh.exp2);
+  if (rank < row.runs) {
+    RunSum acc;
+    for (int j = 0; j < row.per; j += kSaU) {
+      const int i0 = (rank * row.per + j) * TH + (int)threadIdx.x;
+      uint4 v[kSaU];
 #pragma unroll
-        for (int u = 0; u < kSaU; ++u) {
-          v[u] = Stream<TH, 1, 1, 1, E, int>::none(E());
-          if (i0 + u * TH < row.r.nvec) v[u] = row.r.vec()[i0 + u * TH];
-        }
-        acc.add(v, weight.ch, E());
+      for (int u = 0; u < kSaU; ++u) {
+        v[u] = Stream<TH, 1, 1, 1, E, int>::none(E());
+        if (i0 + u * TH < row.r.nvec) v[u] = row.r.vec()[i0 + u * TH];
       }
-      cluster_store(&highs[rank * TH], 0, __float_as_uint(acc.m));
-      cluster_store(&sums[rank * TH], 0, __float_as_uint(acc.s));
+      acc.add(v, weight.ch, E());
     }
-    if (rank == 0 && fl.min_p > 0.0f && threadIdx.x == TH - 1) min_p_edge(fl, sh.edge);
-    cluster_arrive();
-    cluster_wait();
-    if (rank == 0) {
-      float m = neg_inf();
-      for (int q = 0; q < row.runs; ++q) m = max_nan(m, highs[q * TH]);
-      row.front([&](float x, int) { m = max_nan(m, x); });
-      row.back([&](float x, int) { m = max_nan(m, x); });
-      const int open = end_row<E, TH>(a, t, row, fl, params, weight, m, highs, sums, sh, few.work, turn);
-      if (threadIdx.x < C::kTeam) cluster_store(&few.open, threadIdx.x, (uint32_t)open);
-    }
-    cluster_arrive();
-    cluster_wait();
-    if (few.open) {
-      load_powers(sh, work);
-      open_row<E, C>(a, t, (int)few.open, rank, C::kTeam, team_turn, turn, sh, work);
-    }
-    cluster_arrive();  // the first block's maxima and sums are read no more
-    cluster_wait();
+    cluster_store(&highs[rank * TH], 0, __float_as_uint(acc.m));
+    cluster_store(&sums[rank * TH], 0, __float_as_uint(acc.s));
   }
+  if (rank == 0 && fl.min_p > 0.0f && threadIdx.x == TH - 1) min_p_edge(fl, sh.edge);
+  cluster_arrive();
+  cluster_wait();
+  if (rank == 0) {
+    float m = neg_inf();
+    for (int q = 0; q < row.runs; ++q) m = max_nan(m, highs[q * TH]);
+    row.front([&](float x, int) { m = max_nan(m, x); });
+    row.back([&](float x, int) { m = max_nan(m, x); });
+    const int open = end_row<E, TH>(a, t, row, fl, params, weight, m, highs, sums, sh, few.work, turn);
+    if (threadIdx.x < C::kTeam) cluster_store(&few.open, threadIdx.x, (uint32_t)open);
+  }
+  cluster_arrive();
+  cluster_wait();
+  if (few.open) {
+    load_powers(sh, work);
+    open_row<E, C>(a, t, (int)few.open, rank, C::kTeam, team_turn, turn, sh, work);
+  }
+  cluster_arrive();  // no block ends while another reads its shared memory
+  cluster_wait();
 }
 
 __device__ __forceinline__ bool is_open(int token) { return token <= kOpen && token > kClaimed; }
@@ -2112,9 +2110,9 @@ int launch_sample_tokens(const SampleArgs& a, cudaStream_t s) {
   const bool bf = a.dtype == MOE_DTYPE_BF16;
   const int sms = gemm_num_ctas();
   // A cluster per row where all run at once, one block per SM, or, up to one row
-  // less, two, whose registers are half as many (2 x 131072 with top-p 15.1 us
-  // instead of 13.1; 16 rows 16.6 and, in two launches, 18; 32 flat rows 64 and 78; as
-  // many rows as clusters, 36: 21.4 and 18.1).
+  // less, two, whose registers are half as many, which costs each row 2 us.  With
+  // top-p, 131072 ids: 15 rows 11.9 us; 16 rows 14.5 and, in two launches, 18; 32 flat
+  // rows 59 and 78; as many rows as clusters, 36, were slower so (21.4 and 18.1).
   static_assert(LongTeam::kTeam == 8, "as clusters_at_once has it");
   const int few = bf ? launch_few<uint16_t>(a, s) : launch_few<float>(a, s);
   if (few <= 0) return few;
