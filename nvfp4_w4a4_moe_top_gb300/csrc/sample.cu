@@ -1651,8 +1651,9 @@ struct Team {
         __syncthreads();
         const int first = work.edge;
         // among the values of the one bin, or those of the other where they count
+        if (first == C::kBins && last == C::kBins && rest) return false;
         if (first < last || (first == last && take > 0)) {
-          if (first == kMid + 1 || (first == C::kBins && rest)) return false;
+          if (first == kMid + 1) return false;
           last = first, take = 0;
         }
         __syncthreads();
