@@ -664,8 +664,10 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
   bool done = false;
   if (!filtered) {
     err += weight_err;  // of the run with the token
+    // In front of it there is nothing where `before` is 0; behind it there may be ids
+    // where `after` is the row's sum, which rounds light ones away.
     done = sh.id >= 0 && (sh.before == 0 || sh.target - sh.before > err) &&
-           (sh.after >= out.total || sh.after - sh.target > err);
+           sh.after > sh.target && sh.after - sh.target > err;
   } else {
     // ---- a lower bound of what is kept, from the maxima ----
     const uint32_t top = rank_value(m);
