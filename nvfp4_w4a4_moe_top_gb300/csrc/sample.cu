@@ -5,9 +5,10 @@
 // short runs; the rest of the work then touches a few hundred elements.
 //
 // Weights are w = 2^((x - m) c) about the row's maximum m, as 64-bit fixed-point
-// numbers of unit 2^-s, s such that a row's sum stays below 2^63.  Sums of them
-// are the same in any order: threads and atomics add them as they come, and the
-// result is one.
+// numbers of unit 2^-s, s such that a row's sum is 2^63 at most (of equal logits; a
+// sum of FP32 parts may be off it by a part of 2^-18, and fits 64 bits without a
+// sign).  Sums of them are the same in any order: threads and atomics add them as
+// they come, and the result is one.
 //
 // A token is one or another, so a decision is only taken where it is certain.
 // Weights from FP32 exponentials make sums with a bounded relative error
@@ -59,13 +60,13 @@ template <bool UP>
 __device__ __forceinline__ uint64_t part_of(uint64_t total, float p) {
   const uint32_t bits = __float_as_uint(p);
   const int down = 126 - (int)(bits >> 23);  // p = mantissa 2^-24 2^-down
-  if (!(p >= 0x1p-63f)) return UP && p > 0.0f && total > 0 ? 1 : 0;  // total < 2^63
+  if (!(p >= 0x1p-63f)) return UP && p > 0.0f && total > 0 ? 1 : 0;  // a part of 2^63, or little more
   const uint64_t a = (uint64_t)((bits & 0x7FFFFFu) | 0x800000u) << 40, hi = __umul64hi(total, a);
   const bool rest = (total * a | (hi & ((1ull << down) - 1))) != 0;
   return (hi >> down) + (UP && rest ? 1 : 0);
 }
 
-// w as a fixed-point number of unit 2^-s, 43 <= s <= 52, 0 <= w < 2^11.
+// w as a fixed-point number of unit 2^-s, 43 <= s <= 52, 0 <= w < 2^(64 - s).
 __device__ __forceinline__ uint64_t fixed(float w, int s) {
   const int e = (int)(__float_as_uint(w) >> 23) - 127;
   const uint64_t v = ((__float_as_uint(w) & 0x7FFFFFu) | 0x800000u);
@@ -542,10 +543,10 @@ __device__ __forceinline__ void load_exp2(SampleShared<TH>& sh) {
 }
 __device__ __forceinline__ void put_drawn(const SampleArgs& a, int64_t t, const Drawn& d, float inv_t, float m, int s) {
   const float z = (d.x - m) * inv_t, unit = ldexpf(1.0f, -s);
-  const int64_t one = int64_t(1) << s;
+  const uint64_t one = uint64_t(1) << s;  // the rest, below 0 where a sum of FP32 parts is below 1
   a.tokens[t] = d.id;
-  if (a.logprob) a.logprob[t] = z - log1pf((float)((int64_t)d.total - one) * unit);
-  if (a.kept_logprob) a.kept_logprob[t] = z - log1pf((float)((int64_t)d.kept - one) * unit);
+  if (a.logprob) a.logprob[t] = z - log1pf((float)(int64_t)(d.total - one) * unit);
+  if (a.kept_logprob) a.kept_logprob[t] = z - log1pf((float)(int64_t)(d.kept - one) * unit);
 }
 
 // The end of a row, from its runs' maxima and sums.  Without filters the runs' sums
