@@ -128,7 +128,6 @@ struct Weights {
     const float t = (x - m) * ch;
     return t >= kMinExponent ? exp2_fast(t) : 0.0f;
   }
-  static __device__ __forceinline__ uint64_t mantissa(float w) { return (__float_as_uint(w) & 0x7FFFFFu) | 0x800000u; }
   __device__ __forceinline__ uint64_t fast(float x) const {
     const float w = ratio(x);  // in [0, 1]
     return fixed(w, s);
@@ -597,7 +596,7 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
   uint64_t edge = 0;  // keys below have less than min_p
   if (fl.min_p > 0.0f) edge = min_p_key(m, sh.edge);
   Drawn out;
-  uint64_t sum = 0, err, weight_err;  // errors of sums of the pass, and of weights by themselves
+  uint64_t sum = 0, err;  // err: of sums of the pass
   const float unit = ldexpf(1.0f, -weight.s);
   int e = 0;  // the part of the row with the token
   if (filtered && !shift_ok) {  // the pass's weights are out of range
@@ -655,16 +654,15 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
     // for all.  Weights by themselves: 3 in a vector, and with the range of the
     // pass exceeded as many as a run has elements, and 5 over the warp.
     const float S = (float)out.total * unit;
-    const float near = sum_error(S, a.V, cl_ch, 2, 3);
-    weight_err = (uint64_t)((float)(filtered ? out.total : sh.sums[e]) * (near + 0x1p-22f));
     err = shift_ok ? (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 1, 7 + row.per / kSaU + (filtered ? 12 : 5)))
                    : (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 2, filtered ? 0 : row.per * Row<E>::kVec + 5));
     err += (uint64_t)a.V << (weight.s - 42);  // weights below 2^-42, which the pass adds
+    if (!filtered)  // of weights by themselves, in the part of the row with the token
+      err += (uint64_t)((float)sh.sums[e] * (sum_error(S, a.V, cl_ch, 2, 3) + 0x1p-22f));
   }
   const int open = open_flag<E>(64 - __clzll((long long)out.total) - weight.s, m);
   bool done = false;
   if (!filtered) {
-    err += weight_err;  // of the run with the token
     // In front of it there is nothing where `before` is 0; behind it there may be ids
     // where `after` is the row's sum, which rounds light ones away.
     done = sh.id >= 0 && (sh.before == 0 || sh.target - sh.before > err) &&
