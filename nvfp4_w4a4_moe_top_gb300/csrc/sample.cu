@@ -172,6 +172,14 @@ __device__ __forceinline__ float sum_error(float S, int V, const float cl_over_c
   const float t = __fdividef(rest, S) * __log2f(__fdividef((float)V, rest)) + 1.01f;
   return 0x1p-22f + 0x1p-24f * (float)adds + 0.7f * t * (0x1p-24f * (float)roundings + cl_over_ch);
 }
+// The error of a sum W of n weights by themselves, to add to sum_error's of the row:
+// their t is their own, at most log2(n / W) on average, as a part of light weights
+// has a larger one than its row.  3 additions in a vector; the last 2^-22 is of the
+// factor that brings the pass's sums, which say where the part begins, to the maximum.
+__device__ __forceinline__ float part_error(float W, int n, const float cl_over_ch) {
+  const float t = __log2f(__fdividef((float)n, fmaxf(W, 1e-12f))) + 1.01f;
+  return W * (0x1p-21f + 0x1p-24f * 3.0f + 0.7f * t * (0x1p-23f + cl_over_ch));
+}
 
 // Maximum and sum of a run in the pass over the row: about its own integer
 // shift, as Run's (learner.cuh), with four sums of pairs for a batch of vectors,
@@ -651,14 +659,19 @@ __device__ __forceinline__ int end_row(const SampleArgs& a, int64_t t, const Sam
     // in the pass 3 additions per sum of pairs, 3 to join them, one per batch of
     // a run, a product with to_m; then 5 over the warp, or, with the filters, 8
     // for the thread's runs, and to_m's own error, which is otherwise the same
-    // for all.  Weights by themselves: 3 in a vector, and with the range of the
-    // pass exceeded as many as a run has elements, and 5 over the warp.
+    // for all.  Where the range of the pass is exceeded, as many as a run has
+    // elements, and 5 over the warp.
     const float S = (float)out.total * unit;
     err = shift_ok ? (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 1, 7 + row.per / kSaU + (filtered ? 12 : 5)))
                    : (uint64_t)((float)out.total * sum_error(S, a.V, cl_ch, 2, filtered ? 0 : row.per * Row<E>::kVec + 5));
     err += (uint64_t)a.V << (weight.s - 42);  // weights below 2^-42, which the pass adds
-    if (!filtered)  // of weights by themselves, in the part of the row with the token
-      err += (uint64_t)((float)sh.sums[e] * (sum_error(S, a.V, cl_ch, 2, 3) + 0x1p-22f));
+    // The elements before and after the vectors are weights by themselves: one rounding
+    // more, 0.7 2^-24 w t each, and w t is 0.531 at most; and without to_m.
+    err += (uint64_t)(row.r.head + row.r.tail) * (3ull << (weight.s - 27));
+    if (!filtered) {
+      err += (sh.sums[0] + sh.sums[row.runs + 1]) >> 22;
+      err += (uint64_t)ldexpf(part_error((float)sh.sums[e] * unit, min(a.V, row.per * TH * Row<E>::kVec), cl_ch), weight.s);
+    }
   }
   const int open = open_flag<E>(64 - __clzll((long long)out.total) - weight.s, m);
   bool done = false;
