@@ -105,7 +105,7 @@ static SortPlan sort_plan(int T, int V, int d) {
   // Up to 64 chunks, as every chunk reads the counts of all, while a thread then has
   // no more than 32 tokens, that is up to 2^20 tokens; beyond, a chunk per 16384
   // tokens, and the counts read grow with the square: at 2^24 tokens 1024 chunks of
-  // 2 MB each in a pass (d = 8, three passes 3.6 ms).  Tiles as long as leave
+  // 2 MB each in a pass (V = 131072, d = 8, two passes: 3.6 ms).  Tiles as long as leave
   // 1024 of them for the columns of a block, up to 64: a run's parts are then few
   // (32 tokens and 2048 tiles: 65536 x 2048 244 us, 236 so; 16003 x 1000 68 and 62).
   p.items = 1;
