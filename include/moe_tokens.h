@@ -107,12 +107,17 @@ int moe_embed_tokens_backward(const uint16_t* dy, int64_t ldy,
  * +inf token -1, NaN twice and MOE_STATUS_NONFINITE_LOGITS; a row whose
  * inv_temperature or u is out of range or whose top_p or min_p is NaN token
  * -1, NaN twice and MOE_STATUS_BAD_SAMPLING.
- * The tokens do not depend on the other rows; the log-probabilities may differ
- * in their last bits with T.  Between its launches the call marks rows in tokens,
- * which nothing else may write or read meanwhile.
+ * A row's token does not depend on the other rows, unless a border lies within the
+ * distance above: T decides which launch takes the row, and their weights differ
+ * below it.  The log-probabilities may differ in their last bits with T.  Between
+ * its launches the call marks rows in tokens, which nothing else may write or read
+ * meanwhile.
  * Needs 1 <= V <= MOE_SAMPLE_MAX_V, ld >= V.  One launch for few rows (a cluster
  * of blocks each), else two: the second decides rows that the first leaves open,
- * which are few where the weight of each row lies in few ids. */
+ * which are few where the weight of each row lies in few ids and top_k is off or
+ * 1024 at most.  A top_k above that (above 1536 where rows are long or few) leaves
+ * its row open however the weight lies, unless min_p, with top_p off, keeps few;
+ * such a row costs what a flat one does. */
 int moe_sample_tokens(const void* logits, int dtype, int64_t ld, int T, int V,
                       const float* inv_temperature, const int32_t* top_k,
                       const float* top_p, const float* min_p, const float* u,

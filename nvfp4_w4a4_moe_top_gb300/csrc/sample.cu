@@ -16,7 +16,9 @@
 // row that keeps too many elements for a list, stays open and is decided by
 // weights to 2^-34, whose own error is below what 64-bit floating-point sums of so
 // many elements show.  How often: rows of 131072 ids without filters, one in 200
-// where the weight lies in a few ids, one in six where it lies in 40000.
+// where the weight lies in a few ids, one in six where it lies in 40000; with a top_k
+// beyond the list (1536, or 1024 for 128 threads) every row that min_p does not
+// shorten, peaked or not: 2048 x 131072 with top-k 5000 961 us, with top-p too 985.
 //
 //   sample_tokens_kernel  rows by a block each; marks open rows in tokens
 //   sample_open_kernel    the open rows, by eight blocks each or one
@@ -76,7 +78,7 @@ __device__ __forceinline__ uint64_t fixed(float w, int s) {
 template <int TH>
 struct SampleShared {
   static constexpr int NW = TH / 32;
-  static constexpr int kList = TH < 256 ? 1024 : 1536;  // weighed elements: top_k of 1000 among them
+  static constexpr int kList = TH < 256 ? 1024 : 1536;  // weighed elements: a longer top_k leaves the row open
   uint64_t exp2[64];               // 2^(j/64) 2^62
   uint64_t part[kSaRuns + 2][NW];  // sums of the runs by warp; the row's ends
   uint64_t sums[kSaRuns + 2];      // of all warps
@@ -1936,8 +1938,11 @@ __device__ __forceinline__ int64_t claim_window(int T, int blocks) {
 // one after the other within a cluster; their time is the chain of the cluster's
 // barriers (a launch for one row with top-p some 45 us, half of the stalls at barriers).
 // Many are decided by one block each, two per SM, bound by instructions (52 per
-// element: 2048 open rows of 131072 BF16 ids with top-p 973 us).  With
-// nothing open the launch costs 3 us behind the first.
+// element: 2048 open rows of 131072 BF16 ids with top-p 972 us).  Among these are
+// spills: two blocks of 512 threads leave a thread 64 registers, which the ways to
+// decide a row exceed (BF16 560 bytes stored and 832 loaded, FP32 168 and 316; short
+// BF16 rows 132 and 248, few BF16 rows by two blocks per SM 68 and 164).  With nothing
+// open the launch costs 3 us behind the first.
 template <typename E>
 __global__ void __launch_bounds__(LongTeam::kThreads, 2) sample_open_kernel(SampleArgs a) {
   using C = LongTeam;
