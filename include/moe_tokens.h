@@ -109,7 +109,8 @@ int moe_embed_tokens_backward(const uint16_t* dy, int64_t ldy,
  * -1, NaN twice and MOE_STATUS_BAD_SAMPLING.
  * A row's token does not depend on the other rows, unless a border lies within the
  * distance above: T decides which launch takes the row, and their weights differ
- * below it.  The log-probabilities may differ in their last bits with T.  Between
+ * below it.  The log-probabilities may differ in their last bits with T and with the
+ * alignment of a row's address, along whose 16-byte vectors FP32 sums are formed.  Between
  * its launches the call marks rows in tokens, which nothing else may write or read
  * meanwhile.
  * Needs 1 <= V <= MOE_SAMPLE_MAX_V, ld >= V.  One launch for few rows (a cluster
